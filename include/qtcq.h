@@ -373,6 +373,122 @@ qtcq_status qtcq_decode_matvec_mfma_noalloc(const uint32_t* bits, int M, int N, 
                                             qtcq_code code, int tailbiting, const float* x,
                                             int batch, float* y, void* stream);
 
+/* ---- Dense operators around the codec -------------------------------------------------
+ * What a model built on coded weights runs beside the products above: batches too wide
+ * for the decode -> product kernels (a prefill, a training step) multiply decoded rows --
+ * as 8-bit integers with a scale for each token and channel, or in 16 bits through the
+ * gated feed-forward's first half and its gradients, whose weight gradients are the
+ * upstream gradients of qtcq_bcjr_vjp.
+ *
+ * Shared by these entry points:
+ *  - Matrices are row-major with a row stride (ld*, in elements, >= the row's length), so
+ *    a slice of columns of a wider matrix is an operand too.  Rows may start on any
+ *    element; rows that start on 16 bytes are read fastest.  Elements between a row's end
+ *    and the next row are neither read into a result nor written.
+ *  - Outputs must not overlap inputs or each other.
+ *  - Rows, columns and inner lengths are at most 2^24, and a result at most 2^23 tiles of
+ *    128 rows by 64 columns (QTCQ_ERR_UNSUPPORTED beyond).  A length of zero is
+ *    allowed everywhere: an empty result is a no-op, an empty sum gives zeros.
+ *  - Inputs may hold infinities and NaN: they reach the results that their rows and
+ *    columns take part in, as the formulas have it, and no other result.
+ *  - Results are the same bits on every run.  The 16-bit products choose their kernel by
+ *    the sizes, so a row of theirs may round differently in another batch; the 8-bit
+ *    product's sums are exact, so its rows do not depend on the batch.
+ *  - Nothing is allocated; the calls may be captured into a HIP graph. */
+typedef enum { QTCQ_F32 = 0, QTCQ_BF16 = 1, QTCQ_F16 = 2, QTCQ_I8 = 3 } qtcq_dtype;
+
+/* The gate's activation: silu g / (1 + exp(-g)); gelu g Phi(g) (the normal distribution
+ * function); gelu_tanh g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2; relu max(g, 0),
+ * with derivative 0 at 0; sigmoid 1 / (1 + exp(-g)). */
+typedef enum {
+    QTCQ_ACT_SILU = 0,
+    QTCQ_ACT_GELU = 1,
+    QTCQ_ACT_GELU_TANH = 2,
+    QTCQ_ACT_RELU = 3,
+    QTCQ_ACT_SIGMOID = 4
+} qtcq_activation;
+
+/* Rows to 8-bit integers, one scale a row (activations a token a row, weights a channel a
+ * row).  scale[r] = fl32(max_c |x[r][c]| / 127); q[r][c] is x[r][c] / scale[r] rounded to
+ * the nearest integer, halves to even, of the exact quotient, within [-127, 127].  A row
+ * of zeros (or one so small that its scale underflows to 0) has scale 0 and q 0; a row
+ * that holds an infinity or NaN has scale NaN and q 0.
+ *   x      [rows][cols] of dtype QTCQ_F32, QTCQ_BF16 or QTCQ_F16, row stride ldx
+ *   q      [rows][cols] int8 (out), row stride ldq
+ *   scale  [rows] float32 (out)
+ * Errors: QTCQ_ERR_INVALID_ARG (negative sizes, a stride below cols, NULL or misaligned
+ * buffers), QTCQ_ERR_UNSUPPORTED (dtype, sizes), QTCQ_ERR_DEVICE. */
+qtcq_status qtcq_quantize_rows(const void* x, int dtype, int64_t rows, int cols, int64_t ldx,
+                               int8_t* q, int64_t ldq, float* scale, void* stream);
+
+/* The M x N matrix of tile streams (layout and tile numbering as qtcq_decode_matvec) as
+ * rows.  dtype QTCQ_F32: the code values; QTCQ_BF16, QTCQ_F16: each rounded once;
+ * QTCQ_I8: the rows as qtcq_quantize_rows gives them for the code values, with scale [M].
+ *   bits    [(M/16)*(N/16)][W] uint32 (W = 17, or 16 tail-biting), as qtcq_decode_matvec
+ *   M, N    multiples of 16
+ *   w       [M][N] of dtype (out), 16-byte aligned, row stride ldw a multiple of 16 bytes
+ *   scale   [M] float32 (out): required for QTCQ_I8, otherwise ignored (may be NULL)
+ * Errors: QTCQ_ERR_INVALID_ARG (M or N negative or not multiples of 16, ldw below N or not
+ * whole 16 bytes, NULL or misaligned buffers), QTCQ_ERR_UNSUPPORTED ((L, k), code, dtype,
+ * sizes), QTCQ_ERR_DEVICE. */
+qtcq_status qtcq_decode_matrix(const uint32_t* bits, int M, int N, int L, int k, qtcq_code code,
+                               int tailbiting, int dtype, void* w, int64_t ldw, float* scale,
+                               void* stream);
+
+/* Product of two 8-bit matrices with a scale for each token and each channel:
+ *   y[m][n] = fl(fl(fl32(sum_k a[m][k] w[n][k]) * a_scale[m]) * w_scale[n])
+ * rounded once more to dtype; the sum is exact (32-bit integers).
+ *   a  [M][K] int8, row stride lda; a_scale [M] float32
+ *   w  [N][K] int8, row stride ldw; w_scale [N] float32
+ *   y  [M][N] of dtype QTCQ_F32, QTCQ_BF16 or QTCQ_F16 (out), row stride ldy
+ *   K  at most 131071 (|sum| < 2^31 for any int8 inputs)
+ * Errors: QTCQ_ERR_INVALID_ARG (negative sizes, strides below the rows' lengths, NULL or
+ * misaligned buffers), QTCQ_ERR_UNSUPPORTED (dtype, sizes), QTCQ_ERR_DEVICE. */
+qtcq_status qtcq_matmul_int8(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* w,
+                             int64_t ldw, const float* w_scale, int M, int N, int K, int dtype,
+                             void* y, int64_t ldy, void* stream);
+
+/* The gated feed-forward's first half: with gate = x w_gate^T and up = x w_up^T,
+ *   h[m][f] = act(gate[m][f]) * up[m][f],
+ * sums, activation and product in binary32, h rounded once.
+ *   x             [M][K] of dtype QTCQ_BF16 or QTCQ_F16, row stride ldx
+ *   w_gate, w_up  [F][K] of dtype, row stride ldw both (two halves of one [2F][K] matrix,
+ *                 or two matrices)
+ *   h             [M][F] of dtype (out), row stride ldh
+ *   gate, up      [M][F] of dtype (out), row stride ldg: the projections, rounded once, for
+ *                 qtcq_gated_vjp; both or neither NULL
+ * Errors: QTCQ_ERR_INVALID_ARG (negative sizes, strides below the rows' lengths, NULL or
+ * misaligned buffers, one of gate and up NULL), QTCQ_ERR_UNSUPPORTED (dtype, activation,
+ * sizes), QTCQ_ERR_DEVICE. */
+qtcq_status qtcq_gated_forward(const void* x, int64_t ldx, const void* w_gate, const void* w_up,
+                               int64_t ldw, int dtype, int M, int F, int K, int activation, void* h,
+                               int64_t ldh, void* gate, void* up, int64_t ldg, void* stream);
+
+/* Workspace bytes of qtcq_gated_vjp: d_gate and d_up below.  0 for sizes out of range. */
+size_t qtcq_gated_vjp_workspace_bytes(int M, int F, int K);
+
+/* Gradients of the gated projections from grad_h = dLoss/dh.  With
+ *   d_gate = grad_h up act'(gate),   d_up = grad_h act(gate)
+ * (in binary32, each rounded once to dtype: in fp16 values beyond 65504 become infinite
+ * there, and values below 2^-14 lose precision, so scale the loss as usual),
+ *   grad_x = d_gate w_gate + d_up w_up,  grad_w_gate = d_gate^T x,  grad_w_up = d_up^T x,
+ * sums in binary32, each result rounded once to dtype.
+ *   x, w_gate, w_up, dtype, M, F, K, activation : as qtcq_gated_forward
+ *   gate, up     [M][F] as qtcq_gated_forward saved them, row stride ldg
+ *   grad_h       [M][F] of dtype, row stride ldgh
+ *   grad_x       [M][K] of dtype (out), row stride ldgx, or NULL (then w_gate and w_up are
+ *                not read and may be NULL)
+ *   grad_w_gate, grad_w_up  [F][K] of dtype (out), row stride ldgw; both or neither NULL
+ *                (then x is not read and may be NULL)
+ *   workspace    16-byte aligned, >= qtcq_gated_vjp_workspace_bytes(M, F, K)
+ * Errors: as qtcq_gated_forward, and QTCQ_ERR_WORKSPACE. */
+qtcq_status qtcq_gated_vjp(const void* x, int64_t ldx, const void* w_gate, const void* w_up,
+                           int64_t ldw, const void* gate, const void* up, int64_t ldg,
+                           const void* grad_h, int64_t ldgh, int dtype, int M, int F, int K,
+                           int activation, void* grad_x, int64_t ldgx, void* grad_w_gate,
+                           void* grad_w_up, int64_t ldgw, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -26,6 +26,17 @@ QTCQ_CODE_3INST = 1
 QTCQ_CODE_XOR = 2
 QTCQ_CODE_INVALID = 0xFF
 
+QTCQ_F32 = 0
+QTCQ_BF16 = 1
+QTCQ_F16 = 2
+QTCQ_I8 = 3
+
+QTCQ_ACT_SILU = 0
+QTCQ_ACT_GELU = 1
+QTCQ_ACT_GELU_TANH = 2
+QTCQ_ACT_RELU = 3
+QTCQ_ACT_SIGMOID = 4
+
 
 class QtcqError(RuntimeError):
     def __init__(self, status: int, where: str):
@@ -75,6 +86,16 @@ _SIGS = {
                                       _vp, _sz, _vp]),
     "qtcq_tailbiting_decode": (_int, [_vp, _i64, _int, _int, _int, _code, _vp, _vp, _vp, _vp,
                                       _vp]),
+    "qtcq_quantize_rows": (_int, [_vp, _int, _i64, _int, _i64, _vp, _i64, _vp, _vp]),
+    "qtcq_decode_matrix": (_int, [_vp, _int, _int, _int, _int, _code, _int, _int, _vp, _i64, _vp,
+                                  _vp]),
+    "qtcq_matmul_int8": (_int, [_vp, _i64, _vp, _vp, _i64, _vp, _int, _int, _int, _int, _vp, _i64,
+                                _vp]),
+    "qtcq_gated_forward": (_int, [_vp, _i64, _vp, _vp, _i64, _int, _int, _int, _int, _int, _vp,
+                                  _i64, _vp, _vp, _i64, _vp]),
+    "qtcq_gated_vjp_workspace_bytes": (_sz, [_int, _int, _int]),
+    "qtcq_gated_vjp": (_int, [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _int, _int,
+                              _int, _int, _int, _vp, _i64, _vp, _vp, _i64, _vp, _sz, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -233,3 +254,43 @@ def qtcq_decode_matvec_mfma_noalloc(bits: int, M: int, N: int, L: int, k: int, c
                                                 1 if tailbiting else 0, _ptr(x), batch, _ptr(y),
                                                 _ptr(stream)),
            "qtcq_decode_matvec_mfma_noalloc")
+
+
+def qtcq_quantize_rows(x: int, dtype: int, rows: int, cols: int, ldx: int, q: int, ldq: int,
+                       scale: int, stream: int = 0) -> None:
+    _check(_lib.qtcq_quantize_rows(_ptr(x), dtype, rows, cols, ldx, _ptr(q), ldq, _ptr(scale),
+                                   _ptr(stream)), "qtcq_quantize_rows")
+
+
+def qtcq_decode_matrix(bits: int, M: int, N: int, L: int, k: int, code: int, tailbiting: bool,
+                       dtype: int, w: int, ldw: int, scale, stream: int = 0) -> None:
+    _check(_lib.qtcq_decode_matrix(_ptr(bits), M, N, L, k, code, 1 if tailbiting else 0, dtype,
+                                   _ptr(w), ldw, _ptr(scale), _ptr(stream)), "qtcq_decode_matrix")
+
+
+def qtcq_matmul_int8(a: int, lda: int, a_scale: int, w: int, ldw: int, w_scale: int, M: int,
+                     N: int, K: int, dtype: int, y: int, ldy: int, stream: int = 0) -> None:
+    _check(_lib.qtcq_matmul_int8(_ptr(a), lda, _ptr(a_scale), _ptr(w), ldw, _ptr(w_scale), M, N, K,
+                                 dtype, _ptr(y), ldy, _ptr(stream)), "qtcq_matmul_int8")
+
+
+def qtcq_gated_forward(x: int, ldx: int, w_gate: int, w_up: int, ldw: int, dtype: int, M: int,
+                       F: int, K: int, activation: int, h: int, ldh: int, gate, up, ldg: int,
+                       stream: int = 0) -> None:
+    _check(_lib.qtcq_gated_forward(_ptr(x), ldx, _ptr(w_gate), _ptr(w_up), ldw, dtype, M, F, K,
+                                   activation, _ptr(h), ldh, _ptr(gate), _ptr(up), ldg,
+                                   _ptr(stream)), "qtcq_gated_forward")
+
+
+def qtcq_gated_vjp_workspace_bytes(M: int, F: int, K: int) -> int:
+    return _lib.qtcq_gated_vjp_workspace_bytes(M, F, K)
+
+
+def qtcq_gated_vjp(x, ldx: int, w_gate, w_up, ldw: int, gate: int, up: int, ldg: int, grad_h: int,
+                   ldgh: int, dtype: int, M: int, F: int, K: int, activation: int, grad_x,
+                   ldgx: int, grad_w_gate, grad_w_up, ldgw: int, workspace: int,
+                   workspace_bytes: int, stream: int = 0) -> None:
+    _check(_lib.qtcq_gated_vjp(_ptr(x), ldx, _ptr(w_gate), _ptr(w_up), ldw, _ptr(gate), _ptr(up),
+                               ldg, _ptr(grad_h), ldgh, dtype, M, F, K, activation, _ptr(grad_x),
+                               ldgx, _ptr(grad_w_gate), _ptr(grad_w_up), ldgw, _ptr(workspace),
+                               workspace_bytes, _ptr(stream)), "qtcq_gated_vjp")

@@ -390,3 +390,161 @@ def decode_matvec_mfma_noalloc(bits: torch.Tensor, M: int, N: int, x: torch.Tens
     nat.qtcq_decode_matvec_mfma_noalloc(bits.data_ptr(), M, N, L, k, _code(code), tailbiting,
                                         x2.data_ptr(), x2.shape[0], o2.data_ptr(), _stream())
     return out
+
+
+# ---- dense operators around the codec --------------------------------------------------
+
+DTYPES = {torch.float32: nat.QTCQ_F32, torch.bfloat16: nat.QTCQ_BF16, torch.float16: nat.QTCQ_F16,
+          torch.int8: nat.QTCQ_I8}
+ACTIVATIONS = {"silu": nat.QTCQ_ACT_SILU, "gelu": nat.QTCQ_ACT_GELU,
+               "gelu_tanh": nat.QTCQ_ACT_GELU_TANH, "relu": nat.QTCQ_ACT_RELU,
+               "sigmoid": nat.QTCQ_ACT_SIGMOID}
+
+
+def _rows(x: torch.Tensor, name: str, dtypes, shape=None) -> int:
+    """A 2-D device tensor of rows that do not overlap, each contiguous (a slice of columns
+    of a wider matrix too).  Returns its row stride."""
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dim() == 2 and x.dtype in dtypes):
+        raise ValueError("%s must be a 2-D device tensor of %s"
+                         % (name, " or ".join(str(d) for d in dtypes)))
+    _on_current_device(x, name)
+    if shape is not None and tuple(x.shape) != tuple(shape):
+        raise ValueError("%s must be %s" % (name, list(shape)))
+    rows, cols = x.shape
+    if rows == 0 or cols == 0:
+        return cols
+    if cols > 1 and x.stride(1) != 1:
+        raise ValueError("%s must have contiguous rows" % name)
+    if rows == 1:
+        return cols
+    if x.stride(0) < cols:
+        raise ValueError("the rows of %s overlap" % name)
+    return x.stride(0)
+
+
+def _scales(s: torch.Tensor, name: str, n: int) -> None:
+    if not (isinstance(s, torch.Tensor) and s.is_cuda and s.dtype == torch.float32
+            and tuple(s.shape) == (n,) and s.is_contiguous()):
+        raise ValueError("%s must be a contiguous float32 device tensor of %d values" % (name, n))
+    _on_current_device(s, name)
+
+
+def _activation(name) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError("activation must be one of %s" % ", ".join(ACTIVATIONS))
+    return ACTIVATIONS[name]
+
+
+def quantize_rows(x: torch.Tensor):
+    """Rows of x ([R][C] float32, bfloat16 or float16) to 8-bit integers with one scale a
+    row.  Returns (q [R][C] int8, scale [R] float32); x is about q * scale[:, None]."""
+    ldx = _rows(x, "x", (torch.float32, torch.bfloat16, torch.float16))
+    R, C = x.shape
+    q = torch.empty((R, C), dtype=torch.int8, device=x.device)
+    scale = torch.empty(R, dtype=torch.float32, device=x.device)
+    nat.qtcq_quantize_rows(x.data_ptr(), DTYPES[x.dtype], R, C, ldx, q.data_ptr(), C,
+                           scale.data_ptr(), _stream())
+    return q, scale
+
+
+def decode_matrix(bits: torch.Tensor, M: int, N: int, L: int = 16, k: int = 2, code="1mad",
+                  tailbiting: bool = False, dtype: torch.dtype = torch.int8):
+    """The M x N matrix whose row-major 16x16 tiles are the T = 256 streams `bits`
+    ([(M/16)(N/16)][W]) as rows.  Returns (w [M][N] int8, scale [M] float32) for
+    torch.int8, or w [M][N] in float32, bfloat16 or float16."""
+    if dtype not in DTYPES:
+        raise ValueError("dtype must be int8, float32, bfloat16 or float16")
+    if M < 0 or N < 0 or M % 16 or N % 16:
+        raise ValueError("M and N must be multiples of 16")
+    W = tailbiting_words(L, k, 256) if tailbiting else bitstream_words(L, k, 256)
+    if not (bits.is_cuda and bits.is_contiguous() and bits.element_size() == 4
+            and bits.numel() == (M // 16) * (N // 16) * W):
+        raise ValueError("bits must hold (M/16)*(N/16) contiguous streams of %d words" % W)
+    _on_current_device(bits, "bits")
+    w = torch.empty((M, N), dtype=dtype, device=bits.device)
+    scale = torch.empty(M, dtype=torch.float32, device=bits.device) if dtype == torch.int8 else None
+    nat.qtcq_decode_matrix(bits.data_ptr(), M, N, L, k, _code(code), tailbiting, DTYPES[dtype],
+                           w.data_ptr(), N, None if scale is None else scale.data_ptr(), _stream())
+    return w if scale is None else (w, scale)
+
+
+def matmul_int8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                dtype: torch.dtype = torch.float32) -> torch.Tensor:
+    """y [M][N] = (a w^T) a_scale[:, None] w_scale for a [M][K] and w [N][K] int8: exact
+    integer sums, then a scale for each token and each channel.  dtype float32, bfloat16
+    or float16."""
+    if dtype not in (torch.float32, torch.bfloat16, torch.float16):
+        raise ValueError("dtype must be float32, bfloat16 or float16")
+    lda = _rows(a, "a", (torch.int8,))
+    ldw = _rows(w, "w", (torch.int8,), (w.shape[0], a.shape[1]) if w.dim() == 2 else None)
+    (M, K), N = a.shape, w.shape[0]
+    _scales(a_scale, "a_scale", M)
+    _scales(w_scale, "w_scale", N)
+    y = torch.empty((M, N), dtype=dtype, device=a.device)
+    nat.qtcq_matmul_int8(a.data_ptr(), lda, a_scale.data_ptr(), w.data_ptr(), ldw,
+                         w_scale.data_ptr(), M, N, K, DTYPES[dtype], y.data_ptr(), N, _stream())
+    return y
+
+
+def _gated_inputs(x, w_gate, w_up):
+    ldx = _rows(x, "x", (torch.bfloat16, torch.float16))
+    ldw = _rows(w_gate, "w_gate", (x.dtype,))
+    if w_gate.shape[1] != x.shape[1]:
+        raise ValueError("w_gate must have the columns of x")
+    if _rows(w_up, "w_up", (x.dtype,), w_gate.shape) != ldw:
+        raise ValueError("w_up must have the row stride of w_gate")
+    return ldx, ldw
+
+
+def gated(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, activation: str = "silu",
+          save: bool = False):
+    """h [M][F] = act(x w_gate^T) * (x w_up^T) for x [M][K] and w_gate, w_up [F][K], all
+    bfloat16 or all float16.  With save, returns (h, gate, up): the two projections too,
+    for gated_vjp."""
+    act = _activation(activation)
+    ldx, ldw = _gated_inputs(x, w_gate, w_up)
+    (M, K), F = x.shape, w_gate.shape[0]
+    h = torch.empty((M, F), dtype=x.dtype, device=x.device)
+    gate, up = (torch.empty_like(h), torch.empty_like(h)) if save else (None, None)
+    nat.qtcq_gated_forward(x.data_ptr(), ldx, w_gate.data_ptr(), w_up.data_ptr(), ldw,
+                           DTYPES[x.dtype], M, F, K, act, h.data_ptr(), F,
+                           gate.data_ptr() if save else None, up.data_ptr() if save else None, F,
+                           _stream())
+    return (h, gate, up) if save else h
+
+
+def gated_vjp_workspace(M: int, F: int, K: int) -> torch.Tensor:
+    """Device scratch for gated_vjp (reusable across calls on one stream)."""
+    n = nat.qtcq_gated_vjp_workspace_bytes(M, F, K)
+    if n == 0:
+        raise ValueError("sizes out of range")
+    return torch.empty(n, dtype=torch.uint8, device="cuda")
+
+
+def gated_vjp(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, gate: torch.Tensor,
+              up: torch.Tensor, grad_h: torch.Tensor, activation: str = "silu",
+              want_x: bool = True, want_w: bool = True, workspace: torch.Tensor | None = None):
+    """Gradients of sum(grad_h * h) for h of gated(x, w_gate, w_up), with the gate and up
+    that it saved.  Returns (grad_x [M][K], grad_w_gate [F][K], grad_w_up [F][K]), None
+    where not wanted; `workspace` (gated_vjp_workspace(M, F, K)) is allocated when not
+    given."""
+    act = _activation(activation)
+    ldx, ldw = _gated_inputs(x, w_gate, w_up)
+    (M, K), F = x.shape, w_gate.shape[0]
+    ldg = _rows(gate, "gate", (x.dtype,), (M, F))
+    if _rows(up, "up", (x.dtype,), (M, F)) != ldg:
+        raise ValueError("up must have the row stride of gate")
+    ldgh = _rows(grad_h, "grad_h", (x.dtype,), (M, F))
+    if workspace is None:
+        workspace = gated_vjp_workspace(M, F, K)
+    ws_bytes = _dev_workspace(workspace)
+    grad_x = torch.empty((M, K), dtype=x.dtype, device=x.device) if want_x else None
+    grad_wg, grad_wu = ((torch.empty((F, K), dtype=x.dtype, device=x.device) for _ in range(2))
+                        if want_w else (None, None))
+    nat.qtcq_gated_vjp(x.data_ptr(), ldx, w_gate.data_ptr(), w_up.data_ptr(), ldw, gate.data_ptr(),
+                       up.data_ptr(), ldg, grad_h.data_ptr(), ldgh, DTYPES[x.dtype], M, F, K, act,
+                       None if grad_x is None else grad_x.data_ptr(), K,
+                       None if grad_wg is None else grad_wg.data_ptr(),
+                       None if grad_wu is None else grad_wu.data_ptr(), K, workspace.data_ptr(),
+                       ws_bytes, _stream())
+    return grad_x, grad_wg, grad_wu

@@ -1,7 +1,7 @@
 """Build the gfx950 HIP library libqtcq.so in-tree with hipcc.
 
-The library is one C-ABI unit (csrc/qtcq.hip) and one launch unit per kernel family
-(csrc/launch_*.hip).  Each is compiled to an object on its own, in parallel, and the
+The library is the C-ABI units (csrc/qtcq.hip, and csrc/qtcq_dense.hip for the dense
+operators) and one launch unit per kernel family (csrc/launch_*.hip).  Each is compiled to an object on its own, in parallel, and the
 objects are linked into the shared library.
 
 Flags that matter for results:
@@ -36,7 +36,8 @@ FLAGS = [
 
 
 def sources() -> list[str]:
-    return [os.path.join(CSRC, "qtcq.hip")] + sorted(glob.glob(os.path.join(CSRC, "launch_*.hip")))
+    return (sorted(glob.glob(os.path.join(CSRC, "qtcq*.hip")))
+            + sorted(glob.glob(os.path.join(CSRC, "launch_*.hip"))))
 
 
 def _jobs() -> int:

@@ -1,0 +1,81 @@
+// dense.hpp -- element types, roundings and gate activations shared by the dense
+// operators (row quantization, decode to rows, 8-bit product, gated projections), gfx950.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace qtcq {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// the activation of the gate (qtcq_activation)
+enum : int { kActSilu = 0, kActGelu = 1, kActGeluTanh = 2, kActRelu = 3, kActSigmoid = 4 };
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__bf16 v) { return (float)v; }
+__device__ __forceinline__ float to_f32(_Float16 v) { return (float)v; }
+
+// One rounding of the binary32 value, to nearest even (out of fp16's range: infinity).
+// The value is kept as computed: without that, a product about to become fp16 turns into a
+// v_fma_mixlo_f16, which rounds the exact product once and not the binary32 one.
+template <typename T>
+__device__ __forceinline__ T from_f32(float v)
+{
+    if constexpr (sizeof(T) == 2) asm volatile("" : "+v"(v));
+    return (T)v;
+}
+
+// 1 / (1 + exp(-g)): exp overflows to infinity for g below -88.7, which gives 0
+__device__ __forceinline__ float sigmoid_f32(float g) { return 1.0f / (1.0f + expf(-g)); }
+
+constexpr float kGeluTanhC = 1.5957691216057308f;        // 2 sqrt(2 / pi)
+constexpr float kGeluTanhC3 = 0.0713548162726009f;       // 0.044715 * 2 sqrt(2 / pi)
+
+// act(g).  gelu_tanh: g (1 + tanh z) / 2 = g sigmoid(2 z), z = sqrt(2 / pi) (g + 0.044715 g^3).
+template <int ACT>
+__device__ __forceinline__ float activate(float g)
+{
+    if constexpr (ACT == kActSilu) return g * sigmoid_f32(g);
+    if constexpr (ACT == kActGelu) return 0.5f * g * erfcf(-0.7071067811865476f * g);
+    if constexpr (ACT == kActGeluTanh) return g * sigmoid_f32(g * (kGeluTanhC + kGeluTanhC3 * g * g));
+    if constexpr (ACT == kActRelu) return g < 0.0f ? 0.0f : g;            // NaN stays NaN
+    return sigmoid_f32(g);
+}
+
+// act(g) and act'(g).  A saturated sigmoid times a large g: 1 - s is exactly 0 for g > 17,
+// and s underflows to 0 before g (1 - s) can matter.
+template <int ACT>
+__device__ __forceinline__ void activate_grad(float g, float& a, float& d)
+{
+    if constexpr (ACT == kActSilu) {
+        const float s = sigmoid_f32(g);
+        a = g * s;
+        d = s * (1.0f + g * (1.0f - s));
+    } else if constexpr (ACT == kActGelu) {
+        const float c = 0.5f * erfcf(-0.7071067811865476f * g);
+        a = g * c;
+        d = c + g * (0.3989422804014327f * expf(-0.5f * g * g));
+    } else if constexpr (ACT == kActGeluTanh) {
+        const float s = sigmoid_f32(g * (kGeluTanhC + kGeluTanhC3 * g * g));
+        a = g * s;
+        // g^2 s (1 - s): the polynomial's slope multiplies s (1 - s) before g, so that a
+        // large |g| meets an exact 0
+        const float t = s * (1.0f - s);
+        d = t == 0.0f ? s : s + g * t * (kGeluTanhC + 3.0f * kGeluTanhC3 * g * g);
+    } else if constexpr (ACT == kActRelu) {
+        a = g < 0.0f ? 0.0f : g;
+        d = g > 0.0f ? 1.0f : (g == g ? 0.0f : g);
+    } else {
+        const float s = sigmoid_f32(g);
+        a = s;
+        d = s * (1.0f - s);
+    }
+}
+
+}  // namespace qtcq

@@ -1,0 +1,332 @@
+// quantize.hpp -- rows to 8-bit integers with one scale a row, from dense rows
+// (quantize_rows) and straight from trellis streams (decode_matrix), gfx950.
+//
+// A row's scale is s = fl32(max|x| / 127) and q = x / s rounded to the nearest integer,
+// halves to even, of the exact quotient: the int8 of a value is a function of the value
+// and of s alone, whichever path or launch shape computes it.  A row of zeros has s = 0
+// and q = 0; a row holding an infinity or NaN has s = NaN and q = 0, so that a product
+// with its scale says so.
+//
+// The exact quotient without a division: with r = fl32(1 / s), u = fma(x, r, 1.5 * 2^23)
+// holds the integer nearest to x r in its low bits.  x r is within 2^-17 of x / s
+// (|x / s| <= 127), so that integer is right unless x / s lies that close to a half step.
+// The residual d = fma(-q, s, x) shows it: |d| < s / 2 proves q (the rounding of d is
+// monotone and s / 2 is exact), anything else is settled in binary64, where x - q s is
+// exact.  Halves come up only where a value is an odd multiple of s / 2 to 24 bits, so
+// the branch is all but never taken.
+#pragma once
+
+#include "codes.hpp"
+#include "dense.hpp"
+
+namespace qtcq {
+
+// below this s the residual test could meet subnormals: the row is rounded in binary64
+constexpr float kQuantTiny = 0x1p-100f;
+
+struct RowScale {
+    float s, r, half;
+    bool tiny;      // s below kQuantTiny (and not 0)
+    bool zero;      // every q is 0 (s is 0 or NaN)
+};
+
+// amax: the row's largest |x| as its binary32 bits (an infinity or NaN is above every
+// finite value as an integer)
+__device__ __forceinline__ RowScale row_scale(uint32_t amax)
+{
+    RowScale o;
+    const bool finite = amax < 0x7F800000u;
+    o.s = finite ? __builtin_bit_cast(float, amax) / 127.0f : __builtin_nanf("");
+    o.zero = !finite || o.s == 0.0f;
+    o.tiny = !o.zero && o.s < kQuantTiny;
+    o.r = 1.0f / o.s;
+    o.half = 0.5f * o.s;
+    return o;
+}
+
+// x / s in binary64 where s is small enough for subnormals (x / s may pass 127 there)
+__device__ __forceinline__ int quant_tiny(float x, float s)
+{
+    double t = rint((double)x / (double)s);
+    t = t > 127.0 ? 127.0 : (t < -127.0 ? -127.0 : t);
+    return (int)t;
+}
+
+// the int8 of x in the low byte of the result (a row that is neither tiny nor zero)
+__device__ __forceinline__ uint32_t quant_bits(float x, const RowScale& o)
+{
+    constexpr float kMagic = 12582912.0f;                  // 1.5 * 2^23
+    const float u = __builtin_fmaf(x, o.r, kMagic);
+    const float q = u - kMagic;
+    const float d = __builtin_fmaf(-q, o.s, x);
+    uint32_t b = __builtin_bit_cast(uint32_t, u);
+    if (__builtin_expect(!(__builtin_fabsf(d) < o.half), 0)) {
+        const double e = __builtin_fma(-(double)q, (double)o.s, (double)x), h = 0.5 * (double)o.s;
+        const bool odd = (b & 1u) != 0u;
+        if (e > h || (e == h && odd)) b += 1u;
+        if (e < -h || (e == -h && odd)) b -= 1u;
+    }
+    return b;
+}
+
+__device__ __forceinline__ uint32_t quant_any(float x, const RowScale& o)
+{
+    if (o.zero) return 0u;
+    return o.tiny ? (uint32_t)quant_tiny(x, o.s) : quant_bits(x, o);
+}
+
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0C0C0400u), hi = __builtin_amdgcn_perm(d, c, 0x04000C0Cu);
+    return lo | hi;
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu; }
+
+// Largest of m over the wave's 64 lanes.
+__device__ __forceinline__ uint32_t wave_max(uint32_t m)
+{
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+        const uint32_t v = (uint32_t)__shfl_xor((int)m, o, 64);
+        m = v > m ? v : m;
+    }
+    return m;
+}
+
+struct QuantShape {
+    static constexpr int kThreads = 256;
+};
+
+// One row per RT threads (64: a wave a row; 256: a workgroup a row).  E elements of T in
+// 16 bytes; a thread holds NCH such chunks of its row in registers between the two
+// passes, and rows longer than RT * NCH chunks are read a second time.  VEC: rows start
+// on 16 bytes, whole chunks are loaded and stored at once; otherwise element by element.
+//   grid.x = ceil(rows / (256 / RT)), block = 256
+template <typename T, int RT, int NCH, bool VEC>
+__global__ void __launch_bounds__(QuantShape::kThreads)
+quantize_rows(const T* __restrict__ x, int64_t rows, int cols, int64_t ldx, int8_t* __restrict__ q, int64_t ldq,
+              float* __restrict__ scale)
+{
+    constexpr int E = 16 / (int)sizeof(T);
+    __shared__ uint32_t red[QuantShape::kThreads / 64];
+    const int tid = threadIdx.x, t = tid % RT;
+    const int64_t row = (int64_t)blockIdx.x * (QuantShape::kThreads / RT) + tid / RT;
+    const bool live = row < rows;
+    const T* xr = x + (live ? row : 0) * ldx;
+    const int n = live ? cols : 0;
+    const int nch = (n + E - 1) / E;
+
+    struct Chunk { T v[E]; };
+    auto load = [&](int c) {
+        Chunk o;
+        if (VEC && (c + 1) * E <= n) {
+            o = __builtin_bit_cast(Chunk, *reinterpret_cast<const u32x4*>(xr + (int64_t)c * E));
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) o.v[e] = c * E + e < n ? xr[c * E + e] : (T)0.0f;
+        }
+        return o;
+    };
+    Chunk held[NCH];
+    uint32_t m = 0;
+    auto take = [&](const Chunk& o) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const uint32_t a = abs_bits(to_f32(o.v[e]));
+            m = a > m ? a : m;
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+        const int c = t + i * RT;
+        if (c < nch) {
+            held[i] = load(c);
+            take(held[i]);
+        }
+    }
+    for (int c = t + NCH * RT; c < nch; c += RT) take(load(c));
+    m = wave_max(m);
+    if constexpr (RT > 64) {
+        if ((tid & 63) == 0) red[tid >> 6] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < RT / 64; ++w) m = red[w] > m ? red[w] : m;
+    }
+    if (!live) return;
+    const RowScale sc = row_scale(m);
+    if (t == 0) scale[row] = sc.s;
+    int8_t* qr = q + row * ldq;
+    auto store = [&](int c, const Chunk& o) {
+        uint32_t b[E];
+        if (__builtin_expect(sc.zero || sc.tiny, 0)) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) b[e] = quant_any(to_f32(o.v[e]), sc);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) b[e] = quant_bits(to_f32(o.v[e]), sc);
+        }
+        if (VEC && (c + 1) * E <= n) {
+            if constexpr (E == 8) {
+                const u32x2 p = {pack4(b[0], b[1], b[2], b[3]), pack4(b[4], b[5], b[6], b[7])};
+                *reinterpret_cast<u32x2*>(qr + (int64_t)c * E) = p;
+            } else {
+                *reinterpret_cast<uint32_t*>(qr + (int64_t)c * E) = pack4(b[0], b[1], b[2], b[3]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (c * E + e < n) qr[c * E + e] = (int8_t)b[e];
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+        const int c = t + i * RT;
+        if (c < nch) store(c, held[i]);
+    }
+    for (int c = t + NCH * RT; c < nch; c += RT) store(c, load(c));
+}
+
+// ---- streams to rows ----------------------------------------------------------------------
+// W [M][N] from its tile streams (tile (I, J) is sequence I (N/16) + J, weight 16 r + c of
+// a tile is row 16 I + r, column 16 J + c).  One workgroup of 16 waves per band of 16 rows:
+// wave w decodes rows 4 (w & 3) .. + 3 of tiles 64 (w >> 2) + lane, + 256, ...: a lane reads
+// the five stream words of its four rows and writes whole tile rows, so that a wave's
+// stores of one row are contiguous.  Row r of a tile is stream bits [32 r, 32 r + 30 + L),
+// inside words r and r + 1 (word 16 of a tail-biting stream is word 0).
+//
+// int8 takes two passes over the band, the largest magnitude of each row first; the
+// words of the first 256 tiles stay in registers, others are read again (from L2).  The
+// largest value is found on the codes before their rescale (code_rescale is odd and
+// monotone).
+struct DecodeRowsShape {
+    static constexpr int kThreads = 1024;
+    static constexpr int kTiles = 256;       // tiles of a band in flight
+};
+
+// OUT: 0 int8 + scale, 1 bf16, 2 fp16, 3 binary32.  grid.x = M / 16.
+template <int L, int CODE, bool TB, int OUT>
+__global__ void __launch_bounds__(DecodeRowsShape::kThreads)
+decode_rows(const uint32_t* __restrict__ bits, int NTJ, void* __restrict__ w, int64_t ldw,
+            float* __restrict__ scale, CodeArg ca)
+{
+    constexpr int Wd = TB ? 16 : (L + 2 * 255 + 31) / 32;
+    __shared__ uint32_t red[16][4];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r0 = 4 * (wave & 3), j0 = 64 * (wave >> 2) + lane;
+    const int I = blockIdx.x;
+    const uint32_t* band = bits + (int64_t)I * NTJ * Wd;
+
+    struct Words { uint32_t w[5]; };
+    auto load = [&](int j) {
+        Words o;
+        const uint32_t* p = band + (int64_t)j * Wd;
+#pragma unroll
+        for (int i = 0; i < 5; ++i) o.w[i] = p[TB ? ((r0 + i) & 15) : (r0 + i)];
+        return o;
+    };
+    // the 16 codes of row r0 + a before their rescale
+    auto raw_row = [&](const Words& o, int a, float* v) {
+        const uint32_t f0 = o.w[a], f1 = __builtin_amdgcn_alignbit(o.w[a], o.w[a + 1], 16);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            const uint32_t f = c < 8 ? f0 : f1;
+            v[c] = code_raw<CODE>((f >> (32 - L - 2 * (c & 7))) & ((1u << L) - 1u), ca);
+        }
+    };
+    const int64_t row0 = 16 * (int64_t)I + r0;
+    if constexpr (OUT == 0) {
+        Words held = {};
+        float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        auto take = [&](const Words& o) {
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                float v[16];
+                raw_row(o, a, v);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) m[a] = __builtin_fmaxf(m[a], __builtin_fabsf(v[c]));
+            }
+        };
+        if (j0 < NTJ) {
+            held = load(j0);
+            take(held);
+        }
+        for (int j = j0 + DecodeRowsShape::kTiles; j < NTJ; j += DecodeRowsShape::kTiles) take(load(j));
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            const uint32_t mm = wave_max(__builtin_bit_cast(uint32_t, m[a]));
+            if (lane == 0) red[wave][a] = mm;
+        }
+        __syncthreads();
+        RowScale sc[4];
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            uint32_t mm = 0;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const uint32_t v = red[4 * g + (wave & 3)][a];
+                mm = v > mm ? v : mm;
+            }
+            // the smallest nonzero code value of any code is far above kQuantTiny
+            sc[a] = row_scale(__builtin_bit_cast(uint32_t, code_rescale<CODE>(__builtin_bit_cast(float, mm))));
+            if (wave < 4 && lane == 0) scale[row0 + a] = sc[a].s;
+        }
+        int8_t* out = static_cast<int8_t*>(w) + row0 * ldw;
+        auto put = [&](int j, const Words& o) {
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                float v[16];
+                raw_row(o, a, v);
+                uint32_t p[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    uint32_t b[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) b[e] = quant_bits(code_rescale<CODE>(v[4 * g + e]), sc[a]);
+                    p[g] = sc[a].zero ? 0u : pack4(b[0], b[1], b[2], b[3]);
+                }
+                const u32x4 pv = {p[0], p[1], p[2], p[3]};
+                *reinterpret_cast<u32x4*>(out + a * ldw + 16 * (int64_t)j) = pv;
+            }
+        };
+        if (j0 < NTJ) put(j0, held);
+        for (int j = j0 + DecodeRowsShape::kTiles; j < NTJ; j += DecodeRowsShape::kTiles) put(j, load(j));
+    } else {
+        for (int j = j0; j < NTJ; j += DecodeRowsShape::kTiles) {
+            const Words o = load(j);
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                float v[16];
+                raw_row(o, a, v);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) v[c] = code_rescale<CODE>(v[c]);
+                const int64_t at = (row0 + a) * ldw + 16 * (int64_t)j;
+                if constexpr (OUT == 3) {
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const f32x4 p = {v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
+                        reinterpret_cast<f32x4*>(static_cast<float*>(w) + at)[g] = p;
+                    }
+                } else {
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        if constexpr (OUT == 1) {
+                            bf16x8 p;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) p[e] = (__bf16)v[8 * g + e];
+                            reinterpret_cast<bf16x8*>(static_cast<__bf16*>(w) + at)[g] = p;
+                        } else {
+                            f16x8 p;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) p[e] = (_Float16)v[8 * g + e];
+                            reinterpret_cast<f16x8*>(static_cast<_Float16*>(w) + at)[g] = p;
+                        }
+                    }
+                }
+            }
+        }
+    }
+}
+
+}  // namespace qtcq
