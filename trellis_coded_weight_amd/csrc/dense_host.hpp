@@ -1,5 +1,5 @@
 // dense_host.hpp -- host-side declarations of the dense operators, shared by their C ABI
-// (qtcq_dense.hip) and their launch unit (launch_dense.hip).
+// (qtcq_dense.hip) and their launch units (launch_rows.hip, launch_products.hip).
 #pragma once
 
 #include "host.hpp"

@@ -1,65 +1,37 @@
-// launch_dense.hip -- launches of the dense operators: row quantization, decode to rows
-// (quantize.hpp), the 8-bit product and the gated projections (tile_product.hpp).
+// launch_products.hip -- launches of the 8-bit product and of the gated projections and
+// their gradients (tile_product.hpp, block_product.hpp).
 #include "dense_host.hpp"
-#include "quantize.hpp"
-#include "tile_product.hpp"
+#include "block_product.hpp"
 
 namespace qtcq {
 namespace host {
 namespace {
 
-template <typename T, int RT, int NCH>
-void quantize_go(bool vec, const void* x, int64_t rows, int cols, int64_t ldx, int8_t* q, int64_t ldq, float* scale,
-                 hipStream_t st)
-{
-    const dim3 grid(blocks_for(rows, QuantShape::kThreads / RT)), block(QuantShape::kThreads);
-    if (vec)
-        hipLaunchKernelGGL((quantize_rows<T, RT, NCH, true>), grid, block, 0, st, static_cast<const T*>(x), rows, cols,
-                           ldx, q, ldq, scale);
-    else
-        hipLaunchKernelGGL((quantize_rows<T, RT, NCH, false>), grid, block, 0, st, static_cast<const T*>(x), rows, cols,
-                           ldx, q, ldq, scale);
-}
-
+// rows that start on 16 bytes and whose last chunk is whole, `inner` elements long
 template <typename T>
-qtcq_status quantize_impl(const void* x, int64_t rows, int cols, int64_t ldx, int8_t* q, int64_t ldq, float* scale,
-                          hipStream_t st)
+bool whole_chunks(const void* p, int64_t ld, int inner)
 {
     constexpr int E = 16 / (int)sizeof(T);
-    const bool vec = aligned16(x) && ldx % E == 0 && (reinterpret_cast<uintptr_t>(q) & 7u) == 0 && ldq % 8 == 0;
-    const int chunks = (cols + E - 1) / E;
-    if (chunks <= 64)
-        quantize_go<T, 64, 1>(vec, x, rows, cols, ldx, q, ldq, scale, st);
-    else if (chunks <= 256)
-        quantize_go<T, 64, 4>(vec, x, rows, cols, ldx, q, ldq, scale, st);
-    else if (chunks <= 1024)
-        quantize_go<T, 256, 4>(vec, x, rows, cols, ldx, q, ldq, scale, st);
-    else
-        quantize_go<T, 256, 8>(vec, x, rows, cols, ldx, q, ldq, scale, st);
-    return launch_status();
+    return aligned16(p) && ld % E == 0 && inner % E == 0 && ld * (int64_t)sizeof(T) <= BlockShape::kMaxStride;
 }
 
-template <int L, int CODE, bool TB>
-qtcq_status decode_rows_impl(const uint32_t* bits, int M, int N, int dtype, void* w, int64_t ldw, float* scale,
-                             const CodeArg& ca, hipStream_t st)
+template <typename T, int MODE>
+bool block_ok(const ProductArgs& a)
 {
-    const dim3 grid((unsigned)(M / 16)), block(DecodeRowsShape::kThreads);
-    auto go = [&](auto out) {
-        hipLaunchKernelGGL((decode_rows<L, CODE, TB, decltype(out)::value>), grid, block, 0, st, bits, N / 16, w, ldw,
-                           scale, ca);
-        return launch_status();
-    };
-    switch (dtype) {
-    case QTCQ_I8: return go(int_c<0>{});
-    case QTCQ_BF16: return go(int_c<1>{});
-    case QTCQ_F16: return go(int_c<2>{});
-    default: return go(int_c<3>{});
-    }
+    const int pk = MODE == kGradW ? a.m : (MODE == kGradX ? a.kp : a.k);
+    const bool p = whole_chunks<T>(a.p[0], a.ldp, pk) && aligned16(a.p[1]);
+    return p && whole_chunks<T>(a.q[0], a.ldq, MODE == kGradX || MODE == kGradW ? a.n : a.k) && aligned16(a.q[1]);
 }
 
 template <typename T, typename O, int MODE>
 qtcq_status tiles_go(const ProductArgs& a, hipStream_t st)
 {
+    if (block_ok<T, MODE>(a) && a.m > 64) {
+        const int64_t n = (int64_t)blocks_for(a.m, BlockShape::kRows) * blocks_for(a.n, BlockShape::cols(MODE));
+        hipLaunchKernelGGL((block_product<T, O, MODE>), dim3((unsigned)n, 1, MODE == kGradW ? 2 : 1),
+                           dim3(BlockShape::kThreads), 0, st, a);
+        return launch_status();
+    }
     const int64_t tiles = (int64_t)blocks_for(a.m, TileShape::kRows) * blocks_for(a.n, TileShape::cols(MODE));
     const dim3 grid((unsigned)tiles, 1, MODE == kGradW ? 2 : 1), block(TileShape::kThreads);
     hipLaunchKernelGGL((tile_product<T, O, MODE>), grid, block, 0, st, a);
@@ -106,6 +78,7 @@ qtcq_status gated_vjp_impl(const GatedVjpCall& c, void* ws, hipStream_t st)
         a.m = c.M;
         a.n = c.K;
         a.k = c.F;
+        a.kp = ldd;
         if (const qtcq_status s = tiles_go<T, T, kGradX>(a, st); s != QTCQ_OK) return s;
     }
     if (c.grad_w_gate) {
@@ -127,27 +100,6 @@ qtcq_status gated_vjp_impl(const GatedVjpCall& c, void* ws, hipStream_t st)
 }
 
 }  // namespace
-
-qtcq_status launch_quantize_rows(const void* x, int dtype, int64_t rows, int cols, int64_t ldx, int8_t* q, int64_t ldq,
-                                 float* scale, hipStream_t st)
-{
-    switch (dtype) {
-    case QTCQ_BF16: return quantize_impl<__bf16>(x, rows, cols, ldx, q, ldq, scale, st);
-    case QTCQ_F16: return quantize_impl<_Float16>(x, rows, cols, ldx, q, ldq, scale, st);
-    default: return quantize_impl<float>(x, rows, cols, ldx, q, ldq, scale, st);
-    }
-}
-
-qtcq_status launch_decode_matrix(int L, const CodeSel& code, bool tb, const uint32_t* bits, int M, int N, int dtype,
-                                 void* w, int64_t ldw, float* scale, hipStream_t st)
-{
-    return with_L_code(L, code.id, [&](auto l, auto c) {
-        return with_bool(tb, [&](auto t) {
-            return decode_rows_impl<decltype(l)::value, decltype(c)::value, decltype(t)::value>(
-                bits, M, N, dtype, w, ldw, scale, code.arg, st);
-        });
-    });
-}
 
 qtcq_status launch_matmul_int8(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* w, int64_t ldw,
                                const float* w_scale, int M, int N, int K, int dtype, void* y, int64_t ldy,

@@ -1,0 +1,83 @@
+// launch_rows.hip -- launches of the row quantization and of the decode of streams to rows
+// (quantize.hpp).
+#include "dense_host.hpp"
+#include "quantize.hpp"
+
+namespace qtcq {
+namespace host {
+namespace {
+
+template <typename T, int RT, int NCH>
+void quantize_go(bool vec, const void* x, int64_t rows, int cols, int64_t ldx, int8_t* q, int64_t ldq, float* scale,
+                 hipStream_t st)
+{
+    const dim3 grid(blocks_for(rows, QuantShape::kThreads / RT)), block(QuantShape::kThreads);
+    if (vec)
+        hipLaunchKernelGGL((quantize_rows<T, RT, NCH, true>), grid, block, 0, st, static_cast<const T*>(x), rows, cols,
+                           ldx, q, ldq, scale);
+    else
+        hipLaunchKernelGGL((quantize_rows<T, RT, NCH, false>), grid, block, 0, st, static_cast<const T*>(x), rows, cols,
+                           ldx, q, ldq, scale);
+}
+
+template <typename T>
+qtcq_status quantize_impl(const void* x, int64_t rows, int cols, int64_t ldx, int8_t* q, int64_t ldq, float* scale,
+                          hipStream_t st)
+{
+    constexpr int E = 16 / (int)sizeof(T);
+    const bool vec = aligned16(x) && ldx % E == 0 && (reinterpret_cast<uintptr_t>(q) & 7u) == 0 && ldq % 8 == 0;
+    const int chunks = (cols + E - 1) / E;
+    if (chunks <= 64)
+        quantize_go<T, 64, 1>(vec, x, rows, cols, ldx, q, ldq, scale, st);
+    else if (chunks <= 256)
+        quantize_go<T, 64, 4>(vec, x, rows, cols, ldx, q, ldq, scale, st);
+    else if (chunks <= 1024)
+        quantize_go<T, 256, 4>(vec, x, rows, cols, ldx, q, ldq, scale, st);
+    else
+        quantize_go<T, 256, 8>(vec, x, rows, cols, ldx, q, ldq, scale, st);
+    return launch_status();
+}
+
+template <int L, int CODE, bool TB>
+qtcq_status decode_rows_impl(const uint32_t* bits, int M, int N, int dtype, void* w, int64_t ldw, float* scale,
+                             const CodeArg& ca, hipStream_t st)
+{
+    const dim3 grid((unsigned)(M / 16)), block(DecodeRowsShape::kThreads);
+    auto go = [&](auto out) {
+        hipLaunchKernelGGL((decode_rows<L, CODE, TB, decltype(out)::value>), grid, block, 0, st, bits, N / 16, w, ldw,
+                           scale, ca);
+        return launch_status();
+    };
+    switch (dtype) {
+    case QTCQ_I8: return go(int_c<0>{});
+    case QTCQ_BF16: return go(int_c<1>{});
+    case QTCQ_F16: return go(int_c<2>{});
+    default: return go(int_c<3>{});
+    }
+}
+
+}  // namespace
+
+qtcq_status launch_quantize_rows(const void* x, int dtype, int64_t rows, int cols, int64_t ldx, int8_t* q, int64_t ldq,
+                                 float* scale, hipStream_t st)
+{
+    switch (dtype) {
+    case QTCQ_BF16: return quantize_impl<__bf16>(x, rows, cols, ldx, q, ldq, scale, st);
+    case QTCQ_F16: return quantize_impl<_Float16>(x, rows, cols, ldx, q, ldq, scale, st);
+    default: return quantize_impl<float>(x, rows, cols, ldx, q, ldq, scale, st);
+    }
+}
+
+qtcq_status launch_decode_matrix(int L, const CodeSel& code, bool tb, const uint32_t* bits, int M, int N, int dtype,
+                                 void* w, int64_t ldw, float* scale, hipStream_t st)
+{
+    return with_L_code(L, code.id, [&](auto l, auto c) {
+        return with_bool(tb, [&](auto t) {
+            return decode_rows_impl<decltype(l)::value, decltype(c)::value, decltype(t)::value>(
+                bits, M, N, dtype, w, ldw, scale, code.arg, st);
+        });
+    });
+}
+
+}  // namespace host
+}  // namespace qtcq

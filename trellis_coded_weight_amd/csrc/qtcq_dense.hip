@@ -1,5 +1,6 @@
 // qtcq_dense.hip -- the C ABI of the dense operators (include/qtcq.h, "Dense operators
-// around the codec"): argument validation; accepted calls go to launch_dense.hip.
+// around the codec"): argument validation; accepted calls go to launch_rows.hip and
+// launch_products.hip.
 #include "dense_host.hpp"
 
 namespace host = qtcq::host;

@@ -34,6 +34,7 @@ struct ProductArgs {
     void* out[2];            // out (kGradW: both weight gradients)
     int64_t ldo;
     int m, n, k;             // rows and columns of out, length of one sum
+    int kp;                  // kGradX: k of P with its zero-filled columns
     const float* p_scale;    // kInt8
     const float* q_scale;
     void* save[2];           // kGated: the projections, or NULL
@@ -101,12 +102,18 @@ __device__ __forceinline__ float activate_any(int act, float g)
     }
 }
 
-// four consecutive outputs of a row, of which n are inside the matrix
+// four consecutive outputs of a row, of which n are inside the matrix (stores need no
+// alignment beyond the element's here)
 template <typename O>
 __device__ __forceinline__ void store4(O* p, const float (&v)[4], int n)
 {
+    struct __attribute__((packed, aligned(sizeof(O)))) Four { O e[4]; };
+    if (n >= 4) {
+        *reinterpret_cast<Four*>(p) = Four{{from_f32<O>(v[0]), from_f32<O>(v[1]), from_f32<O>(v[2]), from_f32<O>(v[3])}};
+        return;
+    }
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < 3; ++e)
         if (e < n) p[e] = from_f32<O>(v[e]);
 }
 
