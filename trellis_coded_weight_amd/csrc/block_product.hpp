@@ -2,9 +2,23 @@
 // 16 bytes and hold whole 16-byte chunks, in workgroup tiles of 256 x 256, gfx950.
 //
 // Eight waves, 2 x 4, each 128 rows of P by 64 rows of Q (128 accumulator registers a
-// lane); a step is 128 bytes of k of both operands (64 KB), double-buffered in LDS.  The
-// next step's operands go from memory straight to LDS (buffer loads with the lds bit)
-// while the matrix instructions take the present one's from registers.
+// lane).  A step is 128 bytes of k: two half tiles of 32 KB, P's and Q's, which go from
+// memory straight to LDS (buffer loads with the lds bit).  Half tiles 0, 1, 2, ... = P0, Q0,
+// P1, Q1, ... take the five 32 KB places of the compute unit's LDS in turn.
+//
+// A wave works in half steps of 64 bytes of k, with the next half step's fragments on
+// their way from LDS to registers (two sets of 48) during the matrix instructions of the
+// present one.  Step s:
+//   read the fragments of its second half; matrix instructions of its first half;
+//   wait until this wave's reads are done and its loads of step s + 1 have landed, barrier
+//   (now step s + 1 is in LDS and step s's two places are free);
+//   start the loads of half tiles 2 s + 5 and 2 s + 6 into those places;
+//   read the fragments of step s + 1's first half; matrix instructions of the second half.
+// So three half tiles are in flight during a step.  Steps of 64 bytes with five of them in
+// LDS were slower (958 against 875 us on the 4096x14336x4096 gated product, even with all
+// loads behind one wait there): each row's 128-byte line is then fetched twice.  Half tiles
+// past the last step are loaded as zeros (every lane out of range), which keeps the count
+// of loads in flight the same.
 //
 // LDS holds an operand in one of two layouts, both written by the loads in whole kilobytes
 // of consecutive lanes, so the order inside a tile is chosen by which chunk of memory each
@@ -35,6 +49,8 @@ struct BlockShape {
     static constexpr int kRows = 256;         // rows of P and of Q in a tile
     static constexpr int kStep = 128;         // bytes of k in a step ([k][row] operands: 64 k)
     static constexpr int kTile = kRows * kStep;
+    static constexpr int kPlaces = 5;         // half tiles in LDS: 5 x 32 KB
+    static constexpr int kLoads = 4;          // loads of a half tile by one wave
     static constexpr int64_t kMaxStride = (int64_t)1 << 22;
     static constexpr int cols(int mode) { return mode == kGated ? kRows / 2 : kRows; }
 };
@@ -58,17 +74,17 @@ __device__ __forceinline__ void block_tile(int b, int tiles_m, int tiles_n, int&
 }
 
 // grid.x = tiles, grid.z = 2 for kGradW; block = 512.
-template <typename T, typename O, int MODE>
+template <typename T, typename O, int MODE, int ACT = 0>
 __global__ void __launch_bounds__(BlockShape::kThreads)
 block_product(ProductArgs a)
 {
     typedef Mfma<T> MM;
-    constexpr int R = BlockShape::kRows, TILE = BlockShape::kTile;
+    constexpr int R = BlockShape::kRows, TILE = BlockShape::kTile, NP = BlockShape::kPlaces;
     constexpr int SZ = (int)sizeof(T);
     constexpr int KS = BlockShape::kStep / SZ;           // k of a step
     constexpr bool PT = MODE == kGradW, QT = MODE == kGradX || MODE == kGradW;
     constexpr int COLS = BlockShape::cols(MODE);
-    __shared__ __align__(1024) char lds[4 * TILE];        // P and Q of one step, then of the next
+    __shared__ __align__(1024) char lds[NP * TILE];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -89,9 +105,9 @@ block_product(ProductArgs a)
     const int ct_h = (ct_k & 3) | ((wave >> 2) << 2);
     const int ct_chunk = ((((lane & 31) >> 1) ^ ct_h) << 1) | (lane & 1);
 
-    auto rsrc = [](const char* p, int64_t bytes) {
-        const int n = bytes > 0x7FFFFFFF ? 0x7FFFFFFF : (bytes > 0 ? (int)bytes : 0);
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), (short)0, n, kRawBufferWord3);
+    // sizes fit 32 bits: a tile's rows or a step's k, times at most kMaxStride
+    auto rsrc = [](const char* p, int bytes) {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), (short)0, bytes, kRawBufferWord3);
     };
     auto to_lds = [&](__amdgpu_buffer_rsrc_t r, char* dst, int off) {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, off, 0, 0, 0);
@@ -100,22 +116,24 @@ block_product(ProductArgs a)
     auto stage_rows = [&](const void* base, int64_t ld, int row0, int nrows, int k, int k0, char* dst, auto hr) {
         const int left = (k - k0) * SZ;                 // bytes of k from k0
         const __amdgpu_buffer_rsrc_t r = rsrc(static_cast<const char*>(base) + row0 * ld + (int64_t)k0 * SZ,
-                                              nrows > row0 ? (int64_t)(nrows - row0 - 1) * ld + left : 0);
+                                              (nrows - row0 < R ? nrows - row0 - 1 : R - 1) * (int)ld + left);
         int off = rk_row * (int)ld + rk_chunk * 16;
-        const bool out = rk_chunk * 16 >= left;
+        const bool out = rk_chunk * 16 >= left;           // every lane past the last step
 #pragma unroll
         for (int h = 0; h < decltype(hr)::value; ++h)
             to_lds(r, dst + (64 * h + 8 * wave) * 128, out ? 0x7FFFFFFF : off + h * 64 * (int)ld);
     };
     auto stage_cols = [&](const void* base, int64_t ld, int row0, int nrows, int k0, char* dst) {
-        const int64_t left = a.k - k0;
+        const int left = a.k - k0 < KS ? a.k - k0 : KS;
         const __amdgpu_buffer_rsrc_t r = rsrc(static_cast<const char*>(base) + k0 * ld + (int64_t)row0 * SZ,
-                                              left > 0 ? (left - 1) * ld + (int64_t)(nrows - row0) * SZ : 0);
+                                              left > 0 ? (left - 1) * (int)ld + (nrows - row0) * SZ : 0);
         const int off = ct_k * (int)ld + ct_chunk * 16;
 #pragma unroll
         for (int h = 0; h < 4; ++h) to_lds(r, dst + (16 * h + 2 * wave) * 512, off + h * 16 * (int)ld);
     };
-    auto stage = [&](int s, char* dst) {
+    // half tile 2 s (P) or 2 s + 1 (Q) into a place
+    auto stage_p = [&](int s, int place) {
+        char* dst = lds + place * TILE;
         const int seg = MODE == kGradX && s >= steps1 ? 1 : 0;
         const int k0 = (s - seg * steps1) * KS;
         const void* p = a.p[MODE == kGradW ? z : seg];
@@ -123,59 +141,92 @@ block_product(ProductArgs a)
             stage_cols(p, ldp, i0, a.m, k0, dst);
         else
             stage_rows(p, ldp, i0, a.m, MODE == kGradX ? a.kp : a.k, k0, dst, std::integral_constant<int, 4>{});
+    };
+    auto stage_q = [&](int s, int place) {
+        char* dst = lds + place * TILE;
+        const int seg = MODE == kGradX && s >= steps1 ? 1 : 0;
+        const int k0 = (s - seg * steps1) * KS;
         if constexpr (MODE == kGated) {
-            stage_rows(a.q[0], ldq, j0, a.n, a.k, k0, dst + TILE, std::integral_constant<int, 2>{});
-            stage_rows(a.q[1], ldq, j0, a.n, a.k, k0, dst + TILE + TILE / 2, std::integral_constant<int, 2>{});
+            stage_rows(a.q[0], ldq, j0, a.n, a.k, k0, dst, std::integral_constant<int, 2>{});
+            stage_rows(a.q[1], ldq, j0, a.n, a.k, k0, dst + TILE / 2, std::integral_constant<int, 2>{});
         } else if constexpr (QT) {
-            stage_cols(a.q[seg], ldq, j0, a.n, k0, dst + TILE);
+            stage_cols(a.q[seg], ldq, j0, a.n, k0, dst);
         } else {
-            stage_rows(a.q[0], ldq, j0, a.n, a.k, k0, dst + TILE, std::integral_constant<int, 4>{});
+            stage_rows(a.q[0], ldq, j0, a.n, a.k, k0, dst, std::integral_constant<int, 4>{});
         }
     };
 
     // first row of Q's group j of 16 (kGated: two gate groups, the two up groups beside them)
     auto qrow = [&](int j) { return MODE == kGated ? (j >> 1) * 128 + wn * 32 + (j & 1) * 16 : wn * 64 + j * 16; };
-    // LDS address of a lane's 16 bytes: rows of k
+    // LDS address of a lane's 16 bytes: rows of k, the two halves of a step
     const int rk0 = (lane & 15) * 128 + (((lane >> 4) ^ ((lane >> 1) & 7)) * 16);
-    const int rk1 = (lane & 15) * 128 + (((4 + (lane >> 4)) ^ ((lane >> 1) & 7)) * 16);
+    const int rk1 = rk0 ^ 64;
     // columns: k 8 (lane / 16) + (lane / 4 & 3) of a half step, block b of 16 rows
     const int ct_hr = ((lane >> 2) & 3) | (((lane >> 4) & 1) << 2);
     const int ct0 = (8 * (lane >> 4) + ((lane >> 2) & 3)) * 512 + (lane & 3) * 8;
-    auto frag_rows = [&](const char* t, int row, int kk) {
-        return *reinterpret_cast<const u32x4*>(t + row * 128 + (kk ? rk1 : rk0));
+    auto frag_rows = [&](const char* t, int row, int half) {
+        return *reinterpret_cast<const u32x4*>(t + row * 128 + (half ? rk1 : rk0));
     };
-    auto frag_cols = [&](const char* t, int row, int kk) {
-        const char* p = t + ct0 + (((row >> 4) ^ ct_hr) << 5) + kk * 32 * 512;
+    auto frag_cols = [&](const char* t, int row, int half) {
+        const char* p = t + ct0 + (((row >> 4) ^ ct_hr) << 5) + half * 32 * 512;
         const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
             (__attribute__((address_space(3))) s16x4*)(lds_char*)const_cast<char*>(p)));
         const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
             (__attribute__((address_space(3))) s16x4*)(lds_char*)const_cast<char*>(p + 4 * 512)));
         return u32x4{lo.x, lo.y, hi.x, hi.y};
     };
-
+    struct Frags { u32x4 p[8], q[4]; };
+    // the reads are issued here, ahead of the matrix instructions that follow (the compiler
+    // would move each next to its use)
+    auto read = [&](int pp, int pq, int half, Frags& f) {
+        const char* tp = lds + pp * TILE;
+        const char* tq = lds + pq * TILE;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f.q[j] = QT ? frag_cols(tq, qrow(j), half) : frag_rows(tq, qrow(j), half);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            f.p[i] = PT ? frag_cols(tp, wm * 128 + i * 16, half) : frag_rows(tp, wm * 128 + i * 16, half);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
     typename MM::Acc acc[8][4] = {};
-    if (steps > 0) stage(0, lds);
-    for (int s = 0; s < steps; ++s) {
-        // the step's loads are in LDS, and every wave is done with the other buffer
-        __syncthreads();
-        const char* tp = lds + (s & 1) * 2 * TILE;
-        const char* tq = tp + TILE;
-        u32x4 pf[2][8], qf[2][4];
+    auto multiply = [&](const Frags& f) {
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) qf[kk][j] = QT ? frag_cols(tq, qrow(j), kk) : frag_rows(tq, qrow(j), kk);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                pf[kk][i] = PT ? frag_cols(tp, wm * 128 + i * 16, kk) : frag_rows(tp, wm * 128 + i * 16, kk);
+            for (int j = 0; j < 4; ++j) acc[i][j] = MM::mul(f.q[j], f.p[i], acc[i][j]);
+    };
+    // this wave's reads are done and all but its newest n half tiles' loads have landed,
+    // then the same of all waves
+    auto landed = [&](auto n) {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(decltype(n)::value * BlockShape::kLoads) : "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto place = [&](int p) { return p < NP ? p : p - NP; };
+    if (steps > 0) {
+        Frags f0, f1;
+        stage_p(0, 0);
+        stage_q(0, 1);
+        stage_p(1, 2);
+        stage_q(1, 3);
+        stage_p(2, 4);
+        landed(std::integral_constant<int, 3>{});
+        int pp = 0;                           // the place of P of step s; Q's is the next
+        read(0, 1, 0, f0);
+        for (int s = 0; s < steps; ++s) {
+            const int pq = place(pp + 1), np = place(pp + 2), nq = place(pp + 3);
+            read(pp, pq, 1, f1);
+            multiply(f0);
+            landed(std::integral_constant<int, 1>{});
+            stage_q(s + 2, pp);
+            stage_p(s + 3, pq);
+            read(np, nq, 0, f0);
+            multiply(f1);
+            pp = np;
         }
-        if (s + 1 < steps) stage(s + 1, lds + ((s + 1) & 1) * 2 * TILE);
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = MM::mul(qf[kk][j], pf[kk][i], acc[i][j]);
+        // nothing may still be on its way to LDS when the workgroup ends
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
 
     constexpr int NJ = MODE == kGated ? 2 : 4;
@@ -195,7 +246,7 @@ block_product(ProductArgs a)
                 for (int e = 0; e < 4; ++e) {
                     g[e] = acc[i][j][e];
                     u[e] = acc[i][j + 2][e];
-                    v[e] = activate_any(a.act, g[e]) * u[e];
+                    v[e] = activate<ACT>(g[e]) * u[e];
                 }
                 if (a.save[0]) {
                     store4(static_cast<O*>(a.save[0]) + (int64_t)row * a.lds + col, g, left);

@@ -23,38 +23,44 @@ bool block_ok(const ProductArgs& a)
     return p && whole_chunks<T>(a.q[0], a.ldq, MODE == kGradX || MODE == kGradW ? a.n : a.k) && aligned16(a.q[1]);
 }
 
-template <typename T, typename O, int MODE>
+template <typename T, typename O, int MODE, int ACT = 0>
 qtcq_status tiles_go(const ProductArgs& a, hipStream_t st)
 {
     if (block_ok<T, MODE>(a) && a.m > 64) {
         const int64_t n = (int64_t)blocks_for(a.m, BlockShape::kRows) * blocks_for(a.n, BlockShape::cols(MODE));
-        hipLaunchKernelGGL((block_product<T, O, MODE>), dim3((unsigned)n, 1, MODE == kGradW ? 2 : 1),
+        hipLaunchKernelGGL((block_product<T, O, MODE, ACT>), dim3((unsigned)n, 1, MODE == kGradW ? 2 : 1),
                            dim3(BlockShape::kThreads), 0, st, a);
         return launch_status();
     }
     const int64_t tiles = (int64_t)blocks_for(a.m, TileShape::kRows) * blocks_for(a.n, TileShape::cols(MODE));
     const dim3 grid((unsigned)tiles, 1, MODE == kGradW ? 2 : 1), block(TileShape::kThreads);
-    hipLaunchKernelGGL((tile_product<T, O, MODE>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((tile_product<T, O, MODE, ACT>), grid, block, 0, st, a);
     return launch_status();
 }
 
+// f(int_c<ACT>{})
+template <typename F>
+qtcq_status with_act(int act, F&& f)
+{
+    switch (act) {
+    case kActSilu: return f(int_c<kActSilu>{});
+    case kActGelu: return f(int_c<kActGelu>{});
+    case kActGeluTanh: return f(int_c<kActGeluTanh>{});
+    case kActRelu: return f(int_c<kActRelu>{});
+    default: return f(int_c<kActSigmoid>{});
+    }
+}
+
 template <typename T>
-qtcq_status slopes(int act, const GatedVjpCall& c, int ldd, T* dg, T* du, hipStream_t st)
+qtcq_status slopes(const GatedVjpCall& c, int ldd, T* dg, T* du, hipStream_t st)
 {
     const dim3 grid(blocks_for((int64_t)c.M * (ldd / 8), 256)), block(256);
-    auto go = [&](auto act_c) {
-        hipLaunchKernelGGL((gated_slopes<T, decltype(act_c)::value>), grid, block, 0, st,
+    return with_act(c.act, [&](auto act) {
+        hipLaunchKernelGGL((gated_slopes<T, decltype(act)::value>), grid, block, 0, st,
                            static_cast<const T*>(c.gate), static_cast<const T*>(c.up), c.ldg,
                            static_cast<const T*>(c.grad_h), c.ldgh, c.M, c.F, ldd, dg, du);
         return launch_status();
-    };
-    switch (act) {
-    case kActSilu: return go(int_c<kActSilu>{});
-    case kActGelu: return go(int_c<kActGelu>{});
-    case kActGeluTanh: return go(int_c<kActGeluTanh>{});
-    case kActRelu: return go(int_c<kActRelu>{});
-    default: return go(int_c<kActSigmoid>{});
-    }
+    });
 }
 
 template <typename T>
@@ -64,7 +70,7 @@ qtcq_status gated_vjp_impl(const GatedVjpCall& c, void* ws, hipStream_t st)
     T* dg = static_cast<T*>(ws);
     T* du = dg + (int64_t)c.M * ldd;
     if (c.M > 0 && c.F > 0)
-        if (const qtcq_status s = slopes<T>(c.act, c, ldd, dg, du, st); s != QTCQ_OK) return s;
+        if (const qtcq_status s = slopes<T>(c, ldd, dg, du, st); s != QTCQ_OK) return s;
     if (c.grad_x) {
         ProductArgs a = {};
         a.p[0] = dg;
@@ -140,8 +146,11 @@ qtcq_status launch_gated_forward(const GatedCall& c, hipStream_t st)
     p.save[0] = c.gate;
     p.save[1] = c.up;
     p.lds = c.ldg;
-    p.act = c.act;
-    return c.dtype == QTCQ_BF16 ? tiles_go<__bf16, __bf16, kGated>(p, st) : tiles_go<_Float16, _Float16, kGated>(p, st);
+    return with_act(c.act, [&](auto act) {
+        constexpr int ACT = decltype(act)::value;
+        return c.dtype == QTCQ_BF16 ? tiles_go<__bf16, __bf16, kGated, ACT>(p, st)
+                                    : tiles_go<_Float16, _Float16, kGated, ACT>(p, st);
+    });
 }
 
 qtcq_status launch_gated_vjp(const GatedVjpCall& c, void* ws, hipStream_t st)

@@ -39,7 +39,6 @@ struct ProductArgs {
     const float* q_scale;
     void* save[2];           // kGated: the projections, or NULL
     int64_t lds;
-    int act;                 // kGated
 };
 
 struct TileShape {
@@ -90,18 +89,6 @@ __device__ __forceinline__ u32x4 load_chunk(const T* p, int at, int n)
     return __builtin_bit_cast(u32x4, o);
 }
 
-// gate epilogue by a run-time activation (uniform over the grid)
-__device__ __forceinline__ float activate_any(int act, float g)
-{
-    switch (act) {
-    case kActSilu: return activate<kActSilu>(g);
-    case kActGelu: return activate<kActGelu>(g);
-    case kActGeluTanh: return activate<kActGeluTanh>(g);
-    case kActRelu: return activate<kActRelu>(g);
-    default: return activate<kActSigmoid>(g);
-    }
-}
-
 // four consecutive outputs of a row, of which n are inside the matrix (stores need no
 // alignment beyond the element's here)
 template <typename O>
@@ -118,7 +105,7 @@ __device__ __forceinline__ void store4(O* p, const float (&v)[4], int n)
 }
 
 // grid.x = tiles of out (columns fastest), grid.z = 2 for kGradW; block = 256.
-template <typename T, typename O, int MODE>
+template <typename T, typename O, int MODE, int ACT = 0>
 __global__ void __launch_bounds__(TileShape::kThreads)
 tile_product(ProductArgs a)
 {
@@ -239,7 +226,7 @@ tile_product(ProductArgs a)
                 for (int e = 0; e < 4; ++e) {
                     g[e] = acc[i][j][e];
                     u[e] = acc[i][j + 2][e];
-                    v[e] = activate_any(a.act, g[e]) * u[e];
+                    v[e] = activate<ACT>(g[e]) * u[e];
                 }
                 if (a.save[0]) {
                     store4(static_cast<O*>(a.save[0]) + (int64_t)row * a.lds + col, g, left);
