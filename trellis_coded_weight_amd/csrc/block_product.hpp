@@ -105,17 +105,24 @@ block_product(ProductArgs a)
     const int ct_h = (ct_k & 3) | ((wave >> 2) << 2);
     const int ct_chunk = ((((lane & 31) >> 1) ^ ct_h) << 1) | (lane & 1);
 
-    // sizes fit 32 bits: a tile's rows or a step's k, times at most kMaxStride
+    // A raw buffer descriptor of `bytes` from p (both the same in every lane).  Sizes fit
+    // 32 bits: a tile's rows or a step's k, times at most kMaxStride.
     auto rsrc = [](const char* p, int bytes) {
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), (short)0, bytes, kRawBufferWord3);
+        const uint64_t at = reinterpret_cast<uint64_t>(p);
+        return u32x4{(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu, (uint32_t)bytes, (uint32_t)kRawBufferWord3};
     };
-    auto to_lds = [&](__amdgpu_buffer_rsrc_t r, char* dst, int off) {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, off, 0, 0, 0);
+    // 16 bytes a lane from r + off to LDS at dst + 16 lane.  Written out because the compiler
+    // would wait for all such loads ahead of every ds_read_b64_tr_b16; `landed` below waits
+    // for the ones that matter.  It has no output register: the data goes to LDS.
+    auto to_lds = [&](u32x4 r, const char* dst, int off) {
+        const uint32_t at = (uint32_t)reinterpret_cast<uintptr_t>((lds_char*)dst);
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                     ::"s"(at), "v"(off), "s"(r) : "memory", "m0");
     };
     // HR groups of 64 rows (of k) from row0 of `base` [nrows][k] into dst
     auto stage_rows = [&](const void* base, int64_t ld, int row0, int nrows, int k, int k0, char* dst, auto hr) {
         const int left = (k - k0) * SZ;                 // bytes of k from k0
-        const __amdgpu_buffer_rsrc_t r = rsrc(static_cast<const char*>(base) + row0 * ld + (int64_t)k0 * SZ,
+        const u32x4 r = rsrc(static_cast<const char*>(base) + row0 * ld + (int64_t)k0 * SZ,
                                               (nrows - row0 < R ? nrows - row0 - 1 : R - 1) * (int)ld + left);
         int off = rk_row * (int)ld + rk_chunk * 16;
         const bool out = rk_chunk * 16 >= left;           // every lane past the last step
@@ -125,7 +132,7 @@ block_product(ProductArgs a)
     };
     auto stage_cols = [&](const void* base, int64_t ld, int row0, int nrows, int k0, char* dst) {
         const int left = a.k - k0 < KS ? a.k - k0 : KS;
-        const __amdgpu_buffer_rsrc_t r = rsrc(static_cast<const char*>(base) + k0 * ld + (int64_t)row0 * SZ,
+        const u32x4 r = rsrc(static_cast<const char*>(base) + k0 * ld + (int64_t)row0 * SZ,
                                               left > 0 ? (left - 1) * (int)ld + (nrows - row0) * SZ : 0);
         const int off = ct_k * (int)ld + ct_chunk * 16;
 #pragma unroll
