@@ -386,9 +386,16 @@ qtcq_status qtcq_decode_matvec_mfma_noalloc(const uint32_t* bits, int M, int N, 
  *    element; rows that start on 16 bytes are read fastest.  Elements between a row's end
  *    and the next row are neither read into a result nor written.
  *  - Outputs must not overlap inputs or each other.
- *  - Rows, columns and inner lengths are at most 2^24, and a result at most 2^23 tiles of
- *    128 rows by 64 columns (QTCQ_ERR_UNSUPPORTED beyond).  A length of zero is
- *    allowed everywhere: an empty result is a no-op, an empty sum gives zeros.
+ *  - Rows, columns and inner lengths are at most 2^24 (F and K of the gated products 2^21),
+ *    and a result at most 2^23 tiles of 128 rows by 64 columns (QTCQ_ERR_UNSUPPORTED
+ *    beyond).  A length of zero is allowed everywhere: an empty result is a no-op, an empty
+ *    sum gives zeros.
+ *  - The products take a device workspace, 16-byte aligned, whose contents on entry are
+ *    ignored: sums of shares of k where the result is small, and padded copies of operands
+ *    that are not whole 16-byte chunks.  Its size query takes `whole_rows`: nonzero promises
+ *    that every operand's rows start on 16 bytes (pointer and stride), are a multiple of 16
+ *    bytes long (K) and at most 4 MB apart; 0 allows for copies of all.  A size of 0 means
+ *    that none is needed (the workspace may then be NULL), or sizes out of range.
  *  - Inputs may hold infinities and NaN: they reach the results that their rows and
  *    columns take part in, as the formulas have it, and no other result.
  *  - Results are the same bits on every run.  The 16-bit products choose their kernel by
@@ -442,11 +449,15 @@ qtcq_status qtcq_decode_matrix(const uint32_t* bits, int M, int N, int L, int k,
  *   w  [N][K] int8, row stride ldw; w_scale [N] float32
  *   y  [M][N] of dtype QTCQ_F32, QTCQ_BF16 or QTCQ_F16 (out), row stride ldy
  *   K  at most 131071 (|sum| < 2^31 for any int8 inputs)
+ *   workspace  >= qtcq_matmul_int8_workspace_bytes(M, N, K, whole_rows)
  * Errors: QTCQ_ERR_INVALID_ARG (negative sizes, strides below the rows' lengths, NULL or
- * misaligned buffers), QTCQ_ERR_UNSUPPORTED (dtype, sizes), QTCQ_ERR_DEVICE. */
+ * misaligned buffers), QTCQ_ERR_UNSUPPORTED (dtype, sizes), QTCQ_ERR_WORKSPACE (NULL,
+ * misaligned or too small for these operands), QTCQ_ERR_DEVICE. */
+size_t qtcq_matmul_int8_workspace_bytes(int M, int N, int K, int whole_rows);
 qtcq_status qtcq_matmul_int8(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* w,
                              int64_t ldw, const float* w_scale, int M, int N, int K, int dtype,
-                             void* y, int64_t ldy, void* stream);
+                             void* y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                             void* stream);
 
 /* The gated feed-forward's first half: with gate = x w_gate^T and up = x w_up^T,
  *   h[m][f] = act(gate[m][f]) * up[m][f],
@@ -457,15 +468,18 @@ qtcq_status qtcq_matmul_int8(const int8_t* a, int64_t lda, const float* a_scale,
  *   h             [M][F] of dtype (out), row stride ldh
  *   gate, up      [M][F] of dtype (out), row stride ldg: the projections, rounded once, for
  *                 qtcq_gated_vjp; both or neither NULL
+ *   workspace     >= qtcq_gated_workspace_bytes(M, F, K, whole_rows)
  * Errors: QTCQ_ERR_INVALID_ARG (negative sizes, strides below the rows' lengths, NULL or
  * misaligned buffers, one of gate and up NULL), QTCQ_ERR_UNSUPPORTED (dtype, activation,
- * sizes), QTCQ_ERR_DEVICE. */
+ * sizes), QTCQ_ERR_WORKSPACE, QTCQ_ERR_DEVICE. */
+size_t qtcq_gated_workspace_bytes(int M, int F, int K, int whole_rows);
 qtcq_status qtcq_gated_forward(const void* x, int64_t ldx, const void* w_gate, const void* w_up,
                                int64_t ldw, int dtype, int M, int F, int K, int activation, void* h,
-                               int64_t ldh, void* gate, void* up, int64_t ldg, void* stream);
+                               int64_t ldh, void* gate, void* up, int64_t ldg, void* workspace,
+                               size_t workspace_bytes, void* stream);
 
-/* Workspace bytes of qtcq_gated_vjp: d_gate and d_up below.  0 for sizes out of range. */
-size_t qtcq_gated_vjp_workspace_bytes(int M, int F, int K);
+/* Workspace bytes of qtcq_gated_vjp: d_gate and d_up below, shares of grad_x, copies. */
+size_t qtcq_gated_vjp_workspace_bytes(int M, int F, int K, int whole_rows);
 
 /* Gradients of the gated projections from grad_h = dLoss/dh.  With
  *   d_gate = grad_h up act'(gate),   d_up = grad_h act(gate)
@@ -480,7 +494,8 @@ size_t qtcq_gated_vjp_workspace_bytes(int M, int F, int K);
  *                not read and may be NULL)
  *   grad_w_gate, grad_w_up  [F][K] of dtype (out), row stride ldgw; both or neither NULL
  *                (then x is not read and may be NULL)
- *   workspace    16-byte aligned, >= qtcq_gated_vjp_workspace_bytes(M, F, K)
+ *   workspace    >= qtcq_gated_vjp_workspace_bytes(M, F, K, whole_rows), where whole_rows
+ *                is about x, w_gate and w_up
  * Errors: as qtcq_gated_forward, and QTCQ_ERR_WORKSPACE. */
 qtcq_status qtcq_gated_vjp(const void* x, int64_t ldx, const void* w_gate, const void* w_up,
                            int64_t ldw, const void* gate, const void* up, int64_t ldg,

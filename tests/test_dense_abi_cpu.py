@@ -51,8 +51,9 @@ def test_decode_matrix(nat):
 
 def test_matmul_int8(nat):
     call = caller(nat, "qtcq_matmul_int8",
-                  ["a", "lda", "sa", "w", "ldw", "sw", "M", "N", "K", "dtype", "y", "ldy", "stream"],
-                  [FAKE, 64, FAKE, FAKE, 64, FAKE, 4, 8, 64, nat.QTCQ_F32, FAKE, 8, None])
+                  ["a", "lda", "sa", "w", "ldw", "sw", "M", "N", "K", "dtype", "y", "ldy", "ws", "wsb",
+                   "stream"],
+                  [FAKE, 64, FAKE, FAKE, 64, FAKE, 4, 8, 64, nat.QTCQ_F32, FAKE, 8, None, 0, None])
     bad, no = nat.QTCQ_ERR_INVALID_ARG, nat.QTCQ_ERR_UNSUPPORTED
     for kw in (dict(M=-1), dict(N=-1), dict(K=-1), dict(lda=63), dict(ldw=63), dict(ldy=7), dict(a=None),
                dict(w=None), dict(sa=None), dict(sw=None), dict(y=None), dict(y=FAKE + 2), dict(sa=FAKE + 2),
@@ -64,13 +65,23 @@ def test_matmul_int8(nat):
         assert call(**kw) == no, kw
     assert call(M=0, a=None, sa=None, y=None) == nat.QTCQ_OK
     assert call(N=0, w=None, sw=None, y=None) == nat.QTCQ_OK
+    # a result of one tile and a long sum: shares of k; rows of 65 bytes: copies too
+    size = nat.qtcq_matmul_int8_workspace_bytes
+    ws = size(100, 256, 65536, True)
+    assert ws >= 2 * 100 * 256 * 4 and size(100, 256, 65536, False) > ws
+    assert size(1, 256, 65536, True) == 0 and size(4096, 4096, 4096, True) == 0
+    assert size(-1, 8, 8, True) == 0 and size(8, 8, 131072, True) == 0
+    wide = dict(M=100, N=256, K=65536, lda=65536, ldw=65536, ldy=256)
+    for kw in (dict(ws=None, wsb=ws), dict(ws=FAKE + 8, wsb=ws), dict(ws=FAKE, wsb=ws - 1),
+               dict(ws=FAKE, wsb=ws, ldw=65537), dict(ws=FAKE, wsb=ws, a=FAKE + 1)):
+        assert call(**dict(wide, **kw)) == nat.QTCQ_ERR_WORKSPACE, kw
 
 
 def test_gated_forward(nat):
     call = caller(nat, "qtcq_gated_forward",
                   ["x", "ldx", "wg", "wu", "ldw", "dtype", "M", "F", "K", "act", "h", "ldh", "gate", "up", "ldg",
-                   "stream"],
-                  [FAKE, 64, FAKE, FAKE, 64, nat.QTCQ_BF16, 4, 8, 64, 0, FAKE, 8, FAKE, FAKE, 8, None])
+                   "ws", "wsb", "stream"],
+                  [FAKE, 64, FAKE, FAKE, 64, nat.QTCQ_BF16, 4, 8, 64, 0, FAKE, 8, FAKE, FAKE, 8, None, 0, None])
     bad, no = nat.QTCQ_ERR_INVALID_ARG, nat.QTCQ_ERR_UNSUPPORTED
     for kw in (dict(M=-1), dict(F=-1), dict(K=-1), dict(ldx=63), dict(ldw=63), dict(ldh=7), dict(ldg=7),
                dict(gate=None), dict(up=None), dict(x=None), dict(wg=None), dict(wu=None), dict(h=None),
@@ -79,20 +90,29 @@ def test_gated_forward(nat):
         assert call(**kw) == bad, kw
     big = 1 << 25
     for kw in (dict(dtype=nat.QTCQ_F32), dict(dtype=nat.QTCQ_I8), dict(dtype=5), dict(act=-1), dict(act=5),
-               dict(M=(1 << 24) + 1), dict(K=(1 << 24) + 1, ldx=big, ldw=big),
-               dict(M=1 << 24, F=1 << 24, ldh=big, ldg=big)):
+               dict(M=(1 << 24) + 1), dict(K=(1 << 21) + 1, ldx=big, ldw=big),
+               dict(M=1 << 24, F=1 << 21, ldh=big, ldg=big)):
         assert call(**kw) == no, kw
     assert call(M=0, x=None, h=None) == nat.QTCQ_OK
     assert call(F=0, wg=None, wu=None, h=None) == nat.QTCQ_OK
+    size = nat.qtcq_gated_workspace_bytes
+    ws = size(100, 128, 32768, True)
+    assert ws >= 2 * 2 * 100 * 128 * 4 and size(100, 128, 32768, False) > ws
+    assert size(1, 128, 32768, True) == 0 and size(8, 8, (1 << 21) + 1, True) == 0
+    wide = dict(M=100, F=128, K=32768, ldx=32768, ldw=32768, ldh=128, ldg=128)
+    for kw in (dict(ws=None, wsb=ws), dict(ws=FAKE + 8, wsb=ws), dict(ws=FAKE, wsb=ws - 1),
+               dict(ws=FAKE, wsb=ws, ldx=32769), dict(ws=FAKE, wsb=ws, wu=FAKE + 2)):
+        assert call(**dict(wide, **kw)) == nat.QTCQ_ERR_WORKSPACE, kw
 
 
 def test_gated_vjp(nat):
-    ws = nat.qtcq_gated_vjp_workspace_bytes(4, 8, 64)
+    size = nat.qtcq_gated_vjp_workspace_bytes
+    ws = size(4, 8, 64, True)
     assert ws >= 2 * 2 * 4 * 8 and ws % 256 == 0
-    assert nat.qtcq_gated_vjp_workspace_bytes(0, 8, 64) > 0
-    assert nat.qtcq_gated_vjp_workspace_bytes(-1, 8, 64) == 0
-    assert nat.qtcq_gated_vjp_workspace_bytes(4, (1 << 24) + 1, 64) == 0
-    assert nat.qtcq_gated_vjp_workspace_bytes(1 << 20, 1 << 20, 64) == 0
+    assert size(4, 8, 64, False) > ws
+    assert size(-1, 8, 64, True) == 0
+    assert size(4, (1 << 21) + 1, 64, True) == 0
+    assert size(1 << 20, 1 << 20, 64, True) == 0
     call = caller(nat, "qtcq_gated_vjp",
                   ["x", "ldx", "wg", "wu", "ldw", "gate", "up", "ldg", "gh", "ldgh", "dtype", "M", "F", "K", "act",
                    "gx", "ldgx", "gwg", "gwu", "ldgw", "ws", "wsb", "stream"],
@@ -108,6 +128,7 @@ def test_gated_vjp(nat):
         assert call(**kw) == no, kw
     for kw in (dict(ws=None), dict(ws=FAKE + 8), dict(wsb=ws - 1)):
         assert call(**kw) == small, kw
+    assert call(x=FAKE + 2) == small and call(ldw=65) == small
     assert call(gx=None, gwg=None, gwu=None) == nat.QTCQ_OK
     assert call(K=0) == nat.QTCQ_OK
     assert call(M=0, gwg=None, gwu=None) == nat.QTCQ_OK

@@ -15,7 +15,7 @@ ACTS = ["silu", "gelu", "gelu_tanh", "relu", "sigmoid"]
 SIZES = [(1, 1, 1), (1, 16, 64), (1, 33, 129), (2, 256, 512), (5, 100, 24), (8, 1000, 1024), (16, 130, 4096),
          (17, 64, 136), (31, 513, 520), (33, 520, 1000), (64, 128, 256), (65, 127, 255), (96, 704, 320),
          (128, 256, 64), (129, 257, 65), (200, 48, 2056), (256, 512, 768), (300, 1032, 328), (512, 256, 1024),
-         (1, 5000, 16), (4, 24, 14336)]
+         (1, 5000, 16), (4, 24, 14336), (100, 264, 4104), (150, 130, 5001), (70, 2000, 72)]
 
 
 @pytest.fixture(scope="module")
@@ -229,9 +229,10 @@ def test_results_stay_inside_their_rows(M, F, K):
         return b.data_ptr() + 2 * (b.shape[1] + 3)
 
     bh, bg, bu = buf(M, F), buf(M, F), buf(M, F)
+    wf, w8 = api.gated_workspace(M, F, K), api.matmul_int8_workspace(M, F, K)
     say("gated inside rows %dx%dx%d" % (M, F, K))
     nat.qtcq_gated_forward(x.data_ptr(), K, wg.data_ptr(), wu.data_ptr(), K, nat.QTCQ_BF16, M, F, K,
-                           nat.QTCQ_ACT_SILU, at(bh), F + 9, at(bg), at(bu), F + 9, st)
+                           nat.QTCQ_ACT_SILU, at(bh), F + 9, at(bg), at(bu), F + 9, wf.data_ptr(), wf.numel(), st)
     bx, bwg, bwu = buf(M, K), buf(F, K), buf(F, K)
     ws = api.gated_vjp_workspace(M, F, K)
     nat.qtcq_gated_vjp(x.data_ptr(), K, wg.data_ptr(), wu.data_ptr(), K, at(bg), at(bu), F + 9, gh.data_ptr(), F,
@@ -241,7 +242,7 @@ def test_results_stay_inside_their_rows(M, F, K):
     sa, sw = scales(M, 7), scales(F, 8)
     by = buf(M, F)
     nat.qtcq_matmul_int8(a.data_ptr(), K, sa.data_ptr(), w.data_ptr(), K, sw.data_ptr(), M, F, K, nat.QTCQ_BF16,
-                         at(by), F + 9, st)
+                         at(by), F + 9, w8.data_ptr(), w8.numel(), st)
     torch.cuda.synchronize()
     for b, want in ((bh, h), (bg, gate), (bu, up), (bx, gx), (bwg, gwg), (bwu, gwu),
                     (by, api.matmul_int8(a, sa, w, sw, dtype=t))):

@@ -89,11 +89,13 @@ _SIGS = {
     "qtcq_quantize_rows": (_int, [_vp, _int, _i64, _int, _i64, _vp, _i64, _vp, _vp]),
     "qtcq_decode_matrix": (_int, [_vp, _int, _int, _int, _int, _code, _int, _int, _vp, _i64, _vp,
                                   _vp]),
+    "qtcq_matmul_int8_workspace_bytes": (_sz, [_int, _int, _int, _int]),
     "qtcq_matmul_int8": (_int, [_vp, _i64, _vp, _vp, _i64, _vp, _int, _int, _int, _int, _vp, _i64,
-                                _vp]),
+                                _vp, _sz, _vp]),
+    "qtcq_gated_workspace_bytes": (_sz, [_int, _int, _int, _int]),
     "qtcq_gated_forward": (_int, [_vp, _i64, _vp, _vp, _i64, _int, _int, _int, _int, _int, _vp,
-                                  _i64, _vp, _vp, _i64, _vp]),
-    "qtcq_gated_vjp_workspace_bytes": (_sz, [_int, _int, _int]),
+                                  _i64, _vp, _vp, _i64, _vp, _sz, _vp]),
+    "qtcq_gated_vjp_workspace_bytes": (_sz, [_int, _int, _int, _int]),
     "qtcq_gated_vjp": (_int, [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _int, _int,
                               _int, _int, _int, _vp, _i64, _vp, _vp, _i64, _vp, _sz, _vp]),
 }
@@ -268,22 +270,33 @@ def qtcq_decode_matrix(bits: int, M: int, N: int, L: int, k: int, code: int, tai
                                    _ptr(w), ldw, _ptr(scale), _ptr(stream)), "qtcq_decode_matrix")
 
 
+def qtcq_matmul_int8_workspace_bytes(M: int, N: int, K: int, whole_rows: bool) -> int:
+    return _lib.qtcq_matmul_int8_workspace_bytes(M, N, K, 1 if whole_rows else 0)
+
+
 def qtcq_matmul_int8(a: int, lda: int, a_scale: int, w: int, ldw: int, w_scale: int, M: int,
-                     N: int, K: int, dtype: int, y: int, ldy: int, stream: int = 0) -> None:
+                     N: int, K: int, dtype: int, y: int, ldy: int, workspace,
+                     workspace_bytes: int, stream: int = 0) -> None:
     _check(_lib.qtcq_matmul_int8(_ptr(a), lda, _ptr(a_scale), _ptr(w), ldw, _ptr(w_scale), M, N, K,
-                                 dtype, _ptr(y), ldy, _ptr(stream)), "qtcq_matmul_int8")
+                                 dtype, _ptr(y), ldy, _ptr(workspace), workspace_bytes,
+                                 _ptr(stream)), "qtcq_matmul_int8")
+
+
+def qtcq_gated_workspace_bytes(M: int, F: int, K: int, whole_rows: bool) -> int:
+    return _lib.qtcq_gated_workspace_bytes(M, F, K, 1 if whole_rows else 0)
 
 
 def qtcq_gated_forward(x: int, ldx: int, w_gate: int, w_up: int, ldw: int, dtype: int, M: int,
                        F: int, K: int, activation: int, h: int, ldh: int, gate, up, ldg: int,
-                       stream: int = 0) -> None:
+                       workspace, workspace_bytes: int, stream: int = 0) -> None:
     _check(_lib.qtcq_gated_forward(_ptr(x), ldx, _ptr(w_gate), _ptr(w_up), ldw, dtype, M, F, K,
                                    activation, _ptr(h), ldh, _ptr(gate), _ptr(up), ldg,
-                                   _ptr(stream)), "qtcq_gated_forward")
+                                   _ptr(workspace), workspace_bytes, _ptr(stream)),
+           "qtcq_gated_forward")
 
 
-def qtcq_gated_vjp_workspace_bytes(M: int, F: int, K: int) -> int:
-    return _lib.qtcq_gated_vjp_workspace_bytes(M, F, K)
+def qtcq_gated_vjp_workspace_bytes(M: int, F: int, K: int, whole_rows: bool) -> int:
+    return _lib.qtcq_gated_vjp_workspace_bytes(M, F, K, 1 if whole_rows else 0)
 
 
 def qtcq_gated_vjp(x, ldx: int, w_gate, w_up, ldw: int, gate: int, up: int, ldg: int, grad_h: int,

@@ -429,6 +429,25 @@ def _scales(s: torch.Tensor, name: str, n: int) -> None:
     _on_current_device(s, name)
 
 
+def _whole_rows(*xs) -> bool:
+    """Whether the kernels can read these operands in 16-byte chunks where they are
+    (otherwise the workspace holds padded copies)."""
+    return all(x.data_ptr() % 16 == 0 and x.shape[1] * x.element_size() % 16 == 0
+               and (x.shape[0] < 2 or (x.stride(0) * x.element_size() % 16 == 0
+                                       and x.stride(0) * x.element_size() <= 1 << 22))
+               for x in xs)
+
+
+def _workspace(workspace, nbytes: int, like: torch.Tensor):
+    """(pointer or None, bytes) of a workspace, allocated when not given and needed; the
+    tensor comes along so that it lives until the call."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, None, 0
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    return workspace, workspace.data_ptr(), _dev_workspace(workspace)
+
+
 def _activation(name) -> int:
     if name not in ACTIVATIONS:
         raise ValueError("activation must be one of %s" % ", ".join(ACTIVATIONS))
@@ -468,21 +487,35 @@ def decode_matrix(bits: torch.Tensor, M: int, N: int, L: int = 16, k: int = 2, c
     return w if scale is None else (w, scale)
 
 
+def matmul_int8_workspace(M: int, N: int, K: int, whole_rows: bool = False) -> torch.Tensor:
+    """Device scratch for matmul_int8 (reusable across calls on one stream).  whole_rows:
+    the rows of a and w start on 16 bytes and are a multiple of 16 bytes long."""
+    return torch.empty(nat.qtcq_matmul_int8_workspace_bytes(M, N, K, whole_rows),
+                       dtype=torch.uint8, device="cuda")
+
+
 def matmul_int8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
-                dtype: torch.dtype = torch.float32) -> torch.Tensor:
+                dtype: torch.dtype = torch.float32,
+                workspace: torch.Tensor | None = None) -> torch.Tensor:
     """y [M][N] = (a w^T) a_scale[:, None] w_scale for a [M][K] and w [N][K] int8: exact
     integer sums, then a scale for each token and each channel.  dtype float32, bfloat16
-    or float16."""
+    or float16; `workspace` (matmul_int8_workspace(M, N, K)) is allocated when not given
+    and needed."""
     if dtype not in (torch.float32, torch.bfloat16, torch.float16):
         raise ValueError("dtype must be float32, bfloat16 or float16")
     lda = _rows(a, "a", (torch.int8,))
-    ldw = _rows(w, "w", (torch.int8,), (w.shape[0], a.shape[1]) if w.dim() == 2 else None)
+    ldw = _rows(w, "w", (torch.int8,))
     (M, K), N = a.shape, w.shape[0]
+    if w.shape[1] != K:
+        raise ValueError("w must have the columns of a")
     _scales(a_scale, "a_scale", M)
     _scales(w_scale, "w_scale", N)
+    need = nat.qtcq_matmul_int8_workspace_bytes(M, N, K, _whole_rows(a, w))
+    _keep, ws, ws_bytes = _workspace(workspace, need, a)
     y = torch.empty((M, N), dtype=dtype, device=a.device)
     nat.qtcq_matmul_int8(a.data_ptr(), lda, a_scale.data_ptr(), w.data_ptr(), ldw,
-                         w_scale.data_ptr(), M, N, K, DTYPES[dtype], y.data_ptr(), N, _stream())
+                         w_scale.data_ptr(), M, N, K, DTYPES[dtype], y.data_ptr(), N, ws, ws_bytes,
+                         _stream())
     return y
 
 
@@ -496,29 +529,38 @@ def _gated_inputs(x, w_gate, w_up):
     return ldx, ldw
 
 
+def gated_workspace(M: int, F: int, K: int, whole_rows: bool = False) -> torch.Tensor:
+    """Device scratch for gated (reusable across calls on one stream).  whole_rows: the rows
+    of x, w_gate and w_up start on 16 bytes and are a multiple of 16 bytes long."""
+    return torch.empty(nat.qtcq_gated_workspace_bytes(M, F, K, whole_rows), dtype=torch.uint8,
+                       device="cuda")
+
+
 def gated(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, activation: str = "silu",
-          save: bool = False):
+          save: bool = False, workspace: torch.Tensor | None = None):
     """h [M][F] = act(x w_gate^T) * (x w_up^T) for x [M][K] and w_gate, w_up [F][K], all
     bfloat16 or all float16.  With save, returns (h, gate, up): the two projections too,
-    for gated_vjp."""
+    for gated_vjp.  `workspace` (gated_workspace(M, F, K)) is allocated when not given and
+    needed."""
     act = _activation(activation)
     ldx, ldw = _gated_inputs(x, w_gate, w_up)
     (M, K), F = x.shape, w_gate.shape[0]
+    need = nat.qtcq_gated_workspace_bytes(M, F, K, _whole_rows(x, w_gate, w_up))
+    _keep, ws, ws_bytes = _workspace(workspace, need, x)
     h = torch.empty((M, F), dtype=x.dtype, device=x.device)
     gate, up = (torch.empty_like(h), torch.empty_like(h)) if save else (None, None)
     nat.qtcq_gated_forward(x.data_ptr(), ldx, w_gate.data_ptr(), w_up.data_ptr(), ldw,
                            DTYPES[x.dtype], M, F, K, act, h.data_ptr(), F,
                            gate.data_ptr() if save else None, up.data_ptr() if save else None, F,
-                           _stream())
+                           ws, ws_bytes, _stream())
     return (h, gate, up) if save else h
 
 
-def gated_vjp_workspace(M: int, F: int, K: int) -> torch.Tensor:
-    """Device scratch for gated_vjp (reusable across calls on one stream)."""
-    n = nat.qtcq_gated_vjp_workspace_bytes(M, F, K)
-    if n == 0:
-        raise ValueError("sizes out of range")
-    return torch.empty(n, dtype=torch.uint8, device="cuda")
+def gated_vjp_workspace(M: int, F: int, K: int, whole_rows: bool = False) -> torch.Tensor:
+    """Device scratch for gated_vjp (reusable across calls on one stream); whole_rows as
+    gated_workspace."""
+    return torch.empty(nat.qtcq_gated_vjp_workspace_bytes(M, F, K, whole_rows),
+                       dtype=torch.uint8, device="cuda")
 
 
 def gated_vjp(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, gate: torch.Tensor,
@@ -535,9 +577,8 @@ def gated_vjp(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, gate: t
     if _rows(up, "up", (x.dtype,), (M, F)) != ldg:
         raise ValueError("up must have the row stride of gate")
     ldgh = _rows(grad_h, "grad_h", (x.dtype,), (M, F))
-    if workspace is None:
-        workspace = gated_vjp_workspace(M, F, K)
-    ws_bytes = _dev_workspace(workspace)
+    need = nat.qtcq_gated_vjp_workspace_bytes(M, F, K, _whole_rows(x, w_gate, w_up))
+    _keep, ws, ws_bytes = _workspace(workspace, need, x)
     grad_x = torch.empty((M, K), dtype=x.dtype, device=x.device) if want_x else None
     grad_wg, grad_wu = ((torch.empty((F, K), dtype=x.dtype, device=x.device) for _ in range(2))
                         if want_w else (None, None))
@@ -545,6 +586,5 @@ def gated_vjp(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, gate: t
                        up.data_ptr(), ldg, grad_h.data_ptr(), ldgh, DTYPES[x.dtype], M, F, K, act,
                        None if grad_x is None else grad_x.data_ptr(), K,
                        None if grad_wg is None else grad_wg.data_ptr(),
-                       None if grad_wu is None else grad_wu.data_ptr(), K, workspace.data_ptr(),
-                       ws_bytes, _stream())
+                       None if grad_wu is None else grad_wu.data_ptr(), K, ws, ws_bytes, _stream())
     return grad_x, grad_wg, grad_wu

@@ -1,24 +1,30 @@
-// block_product.hpp -- the products of tile_product.hpp for operands whose rows start on
-// 16 bytes and hold whole 16-byte chunks, in workgroup tiles of 256 x 256, gfx950.
+// block_product.hpp -- the products of product.hpp for operands whose rows start on 16
+// bytes and hold whole 16-byte chunks, in workgroup tiles of 32 FP x 256 (FP = 8, 4, 2),
+// gfx950.
 //
-// Eight waves, 2 x 4, each 128 rows of P by 64 rows of Q (128 accumulator registers a
-// lane).  A step is 128 bytes of k: two half tiles of 32 KB, P's and Q's, which go from
-// memory straight to LDS (buffer loads with the lds bit).  Half tiles 0, 1, 2, ... = P0, Q0,
-// P1, Q1, ... take the five 32 KB places of the compute unit's LDS in turn.
+// Eight waves, 2 x 4, each 16 FP rows of P by 64 rows of Q (FP = 8: 128 accumulator
+// registers a lane).  A step is 128 bytes of k.  Its half tiles, P's of 4 FP KB and Q's of
+// 32 KB, go from memory straight to LDS (buffer loads with the lds bit), where P and Q have
+// a ring of places each, together all of the compute unit's 160 KB: 3 and 2 at FP = 8, 3
+// and 3 at FP = 4, 4 and 4 at FP = 2.
 //
 // A wave works in half steps of 64 bytes of k, with the next half step's fragments on
-// their way from LDS to registers (two sets of 48) during the matrix instructions of the
-// present one.  Step s:
+// their way from LDS to registers (two sets of 4 FP + 16) during the matrix instructions of
+// the present one.  Step s:
 //   read the fragments of its second half; matrix instructions of its first half;
 //   wait until this wave's reads are done and its loads of step s + 1 have landed, barrier
 //   (now step s + 1 is in LDS and step s's two places are free);
-//   start the loads of half tiles 2 s + 5 and 2 s + 6 into those places;
+//   start the loads of the next half tiles into those places;
 //   read the fragments of step s + 1's first half; matrix instructions of the second half.
-// So three half tiles are in flight during a step.  Steps of 64 bytes with five of them in
-// LDS were slower (958 against 875 us on the 4096x14336x4096 gated product, even with all
-// loads behind one wait there): each row's 128-byte line is then fetched twice.  Half tiles
-// past the last step are loaded as zeros (every lane out of range), which keeps the count
-// of loads in flight the same.
+// So at FP = 8 three half tiles are in flight during a step.  Steps of 64 bytes with five of
+// them in LDS were slower (958 against 875 us on the 4096x14336x4096 gated product, even
+// with all loads behind one wait there): each row's 128-byte line is then fetched twice.
+// Half tiles past the last step are loaded as zeros (every lane out of range), which keeps
+// the count of loads in flight the same.
+//
+// Where the tiles of out are fewer than the compute units, k is cut into shares of
+// split_steps steps (grid.y); each writes its sums in 32 bits, and join_shares adds them in
+// order.
 //
 // LDS holds an operand in one of two layouts, both written by the loads in whole kilobytes
 // of consecutive lanes, so the order inside a tile is chosen by which chunk of memory each
@@ -40,19 +46,21 @@
 #include <type_traits>
 
 #include "codes.hpp"
-#include "tile_product.hpp"
+#include "product.hpp"
 
 namespace qtcq {
 
 struct BlockShape {
     static constexpr int kThreads = 512;
-    static constexpr int kRows = 256;         // rows of P and of Q in a tile
+    static constexpr int kRows = 256;         // rows of Q in a tile
     static constexpr int kStep = 128;         // bytes of k in a step ([k][row] operands: 64 k)
     static constexpr int kTile = kRows * kStep;
-    static constexpr int kPlaces = 5;         // half tiles in LDS: 5 x 32 KB
-    static constexpr int kLoads = 4;          // loads of a half tile by one wave
     static constexpr int64_t kMaxStride = (int64_t)1 << 22;
+    static constexpr int rows(int fp) { return 32 * fp; }
     static constexpr int cols(int mode) { return mode == kGated ? kRows / 2 : kRows; }
+    // places of the two rings in LDS
+    static constexpr int p_places(int fp) { return fp == 2 ? 4 : 3; }
+    static constexpr int q_places(int fp) { return fp == 8 ? 2 : (fp == 4 ? 3 : 4); }
 };
 
 typedef __attribute__((address_space(3))) char lds_char;
@@ -73,28 +81,34 @@ __device__ __forceinline__ void block_tile(int b, int tiles_m, int tiles_n, int&
     tj = in / rows;
 }
 
-// grid.x = tiles, grid.z = 2 for kGradW; block = 512.
-template <typename T, typename O, int MODE, int ACT = 0>
+// grid.x = tiles, grid.y = shares of k, grid.z = 2 for kGradW; block = 512.  FP = 8 for
+// kGradW, whose P is stored [k][row].
+template <typename T, typename O, int MODE, int ACT, int FP>
 __global__ void __launch_bounds__(BlockShape::kThreads)
 block_product(ProductArgs a)
 {
     typedef Mfma<T> MM;
-    constexpr int R = BlockShape::kRows, TILE = BlockShape::kTile, NP = BlockShape::kPlaces;
+    constexpr int R = BlockShape::kRows, TQ = BlockShape::kTile, TP = BlockShape::rows(FP) * BlockShape::kStep;
+    constexpr int NPP = BlockShape::p_places(FP), NPQ = BlockShape::q_places(FP);
+    constexpr int LP = FP / 2, LQ = 4;                   // loads of a half tile by one wave
     constexpr int SZ = (int)sizeof(T);
     constexpr int KS = BlockShape::kStep / SZ;           // k of a step
     constexpr bool PT = MODE == kGradW, QT = MODE == kGradX || MODE == kGradW;
     constexpr int COLS = BlockShape::cols(MODE);
-    __shared__ __align__(1024) char lds[NP * TILE];
+    static_assert(!PT || FP == 8, "[k][row] tiles are 256 rows wide");
+    __shared__ __align__(1024) char lds[NPP * TP + NPQ * TQ];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
     int ti, tj;
-    block_tile(blockIdx.x, (a.m + R - 1) / R, (a.n + COLS - 1) / COLS, ti, tj);
-    const int i0 = ti * R, j0 = tj * COLS;
+    block_tile(blockIdx.x, (a.m + BlockShape::rows(FP) - 1) / BlockShape::rows(FP), (a.n + COLS - 1) / COLS, ti, tj);
+    const int i0 = ti * BlockShape::rows(FP), j0 = tj * COLS;
     const int z = MODE == kGradW ? blockIdx.z : 0;
     const int steps1 = (a.k + KS - 1) / KS;
     const int steps = MODE == kGradX ? 2 * steps1 : steps1;
+    // this workgroup's share of the steps
+    const int s0 = blockIdx.y * a.split_steps, s1 = s0 + a.split_steps < steps ? s0 + a.split_steps : steps;
     const int64_t ldp = a.ldp * SZ, ldq = a.ldq * SZ;     // in bytes
 
     // where a lane's chunks come from: row-of-k tiles, row 64 h + 8 wave + lane / 8;
@@ -113,53 +127,58 @@ block_product(ProductArgs a)
     };
     // 16 bytes a lane from r + off to LDS at dst + 16 lane.  Written out because the compiler
     // would wait for all such loads ahead of every ds_read_b64_tr_b16; `landed` below waits
-    // for the ones that matter.  It has no output register: the data goes to LDS.
+    // for the ones that matter.  It has no output register: the data goes to LDS.  (The
+    // compiler keeps no value in m0: it sets it where it uses it.)
     auto to_lds = [&](u32x4 r, const char* dst, int off) {
         const uint32_t at = (uint32_t)reinterpret_cast<uintptr_t>((lds_char*)dst);
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                     ::"s"(at), "v"(off), "s"(r) : "memory", "m0");
+                     ::"s"(at), "v"(off), "s"(r) : "memory");
     };
-    // HR groups of 64 rows (of k) from row0 of `base` [nrows][k] into dst
-    auto stage_rows = [&](const void* base, int64_t ld, int row0, int nrows, int k, int k0, char* dst, auto hr) {
-        const int left = (k - k0) * SZ;                 // bytes of k from k0
+    // HR groups of 64 rows (of k) from row0 of `base` [nrows][k] into dst; nothing but zeros
+    // if this step is not there
+    auto stage_rows = [&](bool there, const void* base, int64_t ld, int row0, int nrows, int k, int k0, char* dst, auto hr) {
+        constexpr int HR = decltype(hr)::value;
+        const int left = there ? (k - k0) * SZ : 0;       // bytes of k from k0
         const u32x4 r = rsrc(static_cast<const char*>(base) + row0 * ld + (int64_t)k0 * SZ,
-                                              (nrows - row0 < R ? nrows - row0 - 1 : R - 1) * (int)ld + left);
+                             (nrows - row0 < 64 * HR ? nrows - row0 - 1 : 64 * HR - 1) * (int)ld + left);
         int off = rk_row * (int)ld + rk_chunk * 16;
-        const bool out = rk_chunk * 16 >= left;           // every lane past the last step
+        const bool out = rk_chunk * 16 >= left;
 #pragma unroll
-        for (int h = 0; h < decltype(hr)::value; ++h)
+        for (int h = 0; h < HR; ++h)
             to_lds(r, dst + (64 * h + 8 * wave) * 128, out ? 0x7FFFFFFF : off + h * 64 * (int)ld);
     };
-    auto stage_cols = [&](const void* base, int64_t ld, int row0, int nrows, int k0, char* dst) {
-        const int left = a.k - k0 < KS ? a.k - k0 : KS;
+    auto stage_cols = [&](bool there, const void* base, int64_t ld, int row0, int nrows, int k0, char* dst) {
+        const int left = !there ? 0 : (a.k - k0 < KS ? a.k - k0 : KS);
         const u32x4 r = rsrc(static_cast<const char*>(base) + k0 * ld + (int64_t)row0 * SZ,
-                                              left > 0 ? (left - 1) * (int)ld + (nrows - row0) * SZ : 0);
+                             left > 0 ? (left - 1) * (int)ld + (nrows - row0) * SZ : 0);
         const int off = ct_k * (int)ld + ct_chunk * 16;
 #pragma unroll
         for (int h = 0; h < 4; ++h) to_lds(r, dst + (16 * h + 2 * wave) * 512, off + h * 16 * (int)ld);
     };
-    // half tile 2 s (P) or 2 s + 1 (Q) into a place
-    auto stage_p = [&](int s, int place) {
-        char* dst = lds + place * TILE;
+    // the half tiles of step s into place i of their ring
+    auto stage_p = [&](int s, int i) {
+        char* dst = lds + i * TP;
+        const bool there = s < s1;
         const int seg = MODE == kGradX && s >= steps1 ? 1 : 0;
         const int k0 = (s - seg * steps1) * KS;
         const void* p = a.p[MODE == kGradW ? z : seg];
         if constexpr (PT)
-            stage_cols(p, ldp, i0, a.m, k0, dst);
+            stage_cols(there, p, ldp, i0, a.pm, k0, dst);
         else
-            stage_rows(p, ldp, i0, a.m, MODE == kGradX ? a.kp : a.k, k0, dst, std::integral_constant<int, 4>{});
+            stage_rows(there, p, ldp, i0, a.m, a.pk, k0, dst, std::integral_constant<int, FP / 2>{});
     };
-    auto stage_q = [&](int s, int place) {
-        char* dst = lds + place * TILE;
+    auto stage_q = [&](int s, int i) {
+        char* dst = lds + NPP * TP + i * TQ;
+        const bool there = s < s1;
         const int seg = MODE == kGradX && s >= steps1 ? 1 : 0;
         const int k0 = (s - seg * steps1) * KS;
         if constexpr (MODE == kGated) {
-            stage_rows(a.q[0], ldq, j0, a.n, a.k, k0, dst, std::integral_constant<int, 2>{});
-            stage_rows(a.q[1], ldq, j0, a.n, a.k, k0, dst + TILE / 2, std::integral_constant<int, 2>{});
+            stage_rows(there, a.q[0], ldq, j0, a.n, a.qk, k0, dst, std::integral_constant<int, 2>{});
+            stage_rows(there, a.q[1], ldq, j0, a.n, a.qk, k0, dst + TQ / 2, std::integral_constant<int, 2>{});
         } else if constexpr (QT) {
-            stage_cols(a.q[seg], ldq, j0, a.n, k0, dst);
+            stage_cols(there, a.q[seg], ldq, j0, a.qn, k0, dst);
         } else {
-            stage_rows(a.q[0], ldq, j0, a.n, a.k, k0, dst, std::integral_constant<int, 4>{});
+            stage_rows(there, a.q[0], ldq, j0, a.n, a.qk, k0, dst, std::integral_constant<int, 4>{});
         }
     };
 
@@ -182,55 +201,64 @@ block_product(ProductArgs a)
             (__attribute__((address_space(3))) s16x4*)(lds_char*)const_cast<char*>(p + 4 * 512)));
         return u32x4{lo.x, lo.y, hi.x, hi.y};
     };
-    struct Frags { u32x4 p[8], q[4]; };
+    struct Frags { u32x4 p[FP], q[4]; };
     // the reads are issued here, ahead of the matrix instructions that follow (the compiler
     // would move each next to its use)
-    auto read = [&](int pp, int pq, int half, Frags& f) {
-        const char* tp = lds + pp * TILE;
-        const char* tq = lds + pq * TILE;
+    auto read = [&](int ip, int iq, int half, Frags& f) {
+        const char* tp = lds + ip * TP;
+        const char* tq = lds + NPP * TP + iq * TQ;
 #pragma unroll
         for (int j = 0; j < 4; ++j) f.q[j] = QT ? frag_cols(tq, qrow(j), half) : frag_rows(tq, qrow(j), half);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            f.p[i] = PT ? frag_cols(tp, wm * 128 + i * 16, half) : frag_rows(tp, wm * 128 + i * 16, half);
+        for (int i = 0; i < FP; ++i)
+            f.p[i] = PT ? frag_cols(tp, (wm * FP + i) * 16, half) : frag_rows(tp, (wm * FP + i) * 16, half);
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
     };
-    typename MM::Acc acc[8][4] = {};
+    typename MM::Acc acc[FP][4] = {};
     auto multiply = [&](const Frags& f) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < FP; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = MM::mul(f.q[j], f.p[i], acc[i][j]);
     };
-    // this wave's reads are done and all but its newest n half tiles' loads have landed,
-    // then the same of all waves
+    // this wave's reads are done and all but its newest n loads have landed, then the same
+    // of all waves
     auto landed = [&](auto n) {
         __builtin_amdgcn_sched_barrier(0);
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(decltype(n)::value * BlockShape::kLoads) : "memory");
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(decltype(n)::value) : "memory");
         __builtin_amdgcn_sched_barrier(0);
     };
-    auto place = [&](int p) { return p < NP ? p : p - NP; };
-    if (steps > 0) {
+    // The order of loads: P0 Q0 P1 Q1 ... where the rings are equally long; with one more
+    // place for P (FP = 8) P is a step ahead, P0 Q0 P1 Q1 P2 Q2 ... with Q(s) and P(s + 1)
+    // started together.  `after`: the loads that follow those of step 0 in the prologue,
+    // `newer`: those that follow step s + 1's when step s waits for them.
+    constexpr bool AHEAD = NPP > NPQ;
+    static_assert(NPP == NPQ || NPP == NPQ + 1, "ring lengths");
+    constexpr int after = (NPP - 1) * LP + (NPQ - 1) * LQ;
+    constexpr int newer = after - (LP + LQ);
+    if (s0 < s1) {
         Frags f0, f1;
-        stage_p(0, 0);
-        stage_q(0, 1);
-        stage_p(1, 2);
-        stage_q(1, 3);
-        stage_p(2, 4);
-        landed(std::integral_constant<int, 3>{});
-        int pp = 0;                           // the place of P of step s; Q's is the next
-        read(0, 1, 0, f0);
-        for (int s = 0; s < steps; ++s) {
-            const int pq = place(pp + 1), np = place(pp + 2), nq = place(pp + 3);
-            read(pp, pq, 1, f1);
+#pragma unroll
+        for (int i = 0; i < NPP; ++i) {
+            stage_p(s0 + i, i);
+            if (i < NPQ) stage_q(s0 + i, i);
+        }
+        landed(std::integral_constant<int, after>{});
+        int ip = 0, iq = 0;                   // places of step s
+        read(0, 0, 0, f0);
+        for (int s = s0; s < s1; ++s) {
+            const int np = ip + 1 < NPP ? ip + 1 : 0, nq = iq + 1 < NPQ ? iq + 1 : 0;
+            read(ip, iq, 1, f1);
             multiply(f0);
-            landed(std::integral_constant<int, 1>{});
-            stage_q(s + 2, pp);
-            stage_p(s + 3, pq);
+            landed(std::integral_constant<int, newer>{});
+            if constexpr (AHEAD) stage_q(s + NPQ, iq);
+            stage_p(s + NPP, ip);
+            if constexpr (!AHEAD) stage_q(s + NPQ, iq);
             read(np, nq, 0, f0);
             multiply(f1);
-            pp = np;
+            ip = np;
+            iq = nq;
         }
         // nothing may still be on its way to LDS when the workgroup ends
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -238,37 +266,22 @@ block_product(ProductArgs a)
 
     constexpr int NJ = MODE == kGated ? 2 : 4;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int row = i0 + wm * 128 + i * 16 + (lane & 15);
+    for (int i = 0; i < FP; ++i) {
+        const int row = i0 + (wm * FP + i) * 16 + (lane & 15);
         if (row >= a.m) continue;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             const int col = j0 + (MODE == kGated ? wn * 32 : wn * 64) + j * 16 + 4 * (lane >> 4);
             const int left = a.n - col;
             if (left <= 0) continue;
-            float v[4];
-            if constexpr (MODE == kGated) {
-                float g[4], u[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    g[e] = acc[i][j][e];
-                    u[e] = acc[i][j + 2][e];
-                    v[e] = activate<ACT>(g[e]) * u[e];
-                }
-                if (a.save[0]) {
-                    store4(static_cast<O*>(a.save[0]) + (int64_t)row * a.lds + col, g, left);
-                    store4(static_cast<O*>(a.save[1]) + (int64_t)row * a.lds + col, u, left);
-                }
-            } else if constexpr (MODE == kInt8) {
-                const float ps = a.p_scale[row];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    v[e] = (float)acc[i][j][e] * ps * (e < left ? a.q_scale[col + e] : 0.0f);
+            if (MODE != kGradW && a.part) {
+                typedef typename MM::Acc Acc;
+                Acc* p = static_cast<Acc*>(a.part) + ((((int64_t)blockIdx.y * a.m + row) * a.part_pitch + col) >> 2);
+                p[0] = acc[i][j];
+                if constexpr (MODE == kGated) p[a.part_pitch >> 3] = acc[i][j + 2];
             } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = acc[i][j][e];
+                finish4<O, MODE, ACT>(a, z, row, col, left, acc[i][j], acc[i][MODE == kGated ? j + 2 : j]);
             }
-            store4(static_cast<O*>(a.out[z]) + (int64_t)row * a.ldo + col, v, left);
         }
     }
 }

@@ -1,5 +1,6 @@
 // dense_host.hpp -- host-side declarations of the dense operators, shared by their C ABI
-// (qtcq_dense.hip) and their launch units (launch_rows.hip, launch_products.hip).
+// (qtcq_dense.hip) and their launch units (launch_rows.hip, launch_int8.hip,
+// launch_gated.hip, launch_gated_vjp.hip).
 #pragma once
 
 #include "host.hpp"
@@ -10,17 +11,113 @@ namespace host {
 // Lengths a call may have: tile counts, row offsets inside a tile and element indices
 // inside a row stay within 32 bits.
 constexpr int kDenseMaxDim = 1 << 24;
+// rows of the 16-bit products, in elements: 4 MB, so that a tile's offsets stay below 2^31
+constexpr int kHalfMaxRow = 1 << 21;
 // 2^14 K, the largest magnitude of a sum of K products of 8-bit integers, below 2^31
 constexpr int kInt8MaxK = 131071;
 // the largest grid of 128-wide tiles of 256 threads a launch can hold
 constexpr int64_t kDenseMaxTiles = (int64_t)1 << 23;
 
+// whole 16-byte chunks, in elements
+inline int chunk_pitch(int cols, int size) { return (cols + 16 / size - 1) / (16 / size) * (16 / size); }
+inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
 // row stride of the two slope matrices of the gated gradient, in elements: whole steps
 // of its products, zero-filled past F
 inline int slope_pitch(int F) { return (F + 63) / 64 * 64; }
-inline size_t gated_vjp_bytes(int M, int F)
+
+// ---- which kernel a product takes, and its scratch (product_launch.hpp) ----------------------
+enum : int { kPlanInt8 = 0, kPlanGated = 1, kPlanGradX = 2, kPlanGradW = 3 };
+
+struct ProductPlan {
+    bool skinny;             // the kernel for few rows, which takes no scratch
+    int fp;                  // block kernel: 32 fp rows a tile
+    int shares, share_steps; // shares of k, and the steps of each
+    int part_pitch;          // row pitch of the shares' sums
+    size_t part_bytes;       // the shares' sums
+    size_t p_bytes, q_bytes; // padded copies of the operands
+};
+
+// The compute units of the chip the tile and share counts are chosen for.
+constexpr int kComputeUnits = 256;
+// shares of k hold at least this many steps: a share's first loads and its sums' way
+// through memory cost about as much as six steps
+constexpr int kShareSteps = 8;
+
+// Whether the kernel for few rows takes a product.  It reads Q once at the memory's rate and
+// P once for every 16 columns, so its time grows with m n k; the block kernel's hardly does
+// up to 128 rows, but it pays for shares of k and a second launch.  Measured (us, few rows
+// against block; m n k in bytes of the multiplied elements): 8-bit 8192x28672 at m = 1 44
+// against 48, m = 8 (2^30.8) 54 / 48, m = 16 65 / 49; 28672x8192 at m = 8 59 / 61, 16
+// (2^31.8) 65 / 62, 24 77 / 62; gated 14336x4096 at m = 8 (2^30.8) 54 / 61, 24 70 / 62;
+// gated 4096x4096 at m = 32 (2^31) 23 / 25, 64 32 / 26.  Rows that are not whole chunks cost
+// the block kernel a copy and this one slower loads: 28672x8193 at m = 1 127 / 137, 8 157 /
+// 138; gated 4096x4097 at m = 16 (2^30) 42 / 50, 32 54 / 51.
+inline bool few_rows(int mode, int size, int m, int n, int k, bool whole)
 {
-    return ((size_t)2 * 2 * (size_t)M * (size_t)slope_pitch(F) + 255) / 256 * 256;
+    if (mode != kPlanInt8 && mode != kPlanGated) return false;
+    const double work = (double)m * n * k * size * (mode == kPlanGated ? 2 : 1);
+    return whole ? m <= 4 || (m <= 64 && work <= 0x1p31) : m <= 2 || (m <= 64 && work <= 0x1p30);
+}
+
+// mode, bytes of an element, rows and columns of the result, length of a sum; `whole`: the
+// operands are whole 16-byte chunks as they are
+inline ProductPlan plan_product(int mode, int size, int m, int n, int k, bool whole)
+{
+    ProductPlan p = {};
+    if (few_rows(mode, size, m, n, k, whole)) {
+        p.skinny = true;
+        return p;
+    }
+    p.fp = mode == kPlanGradW ? 8 : (m <= 64 ? 2 : (m <= 128 ? 4 : 8));
+    const int64_t cols = mode == kPlanGated ? 128 : 256;
+    const int64_t tiles = ((int64_t)m + 32 * p.fp - 1) / (32 * p.fp) * ((n + cols - 1) / cols);
+    const int per = 128 / size;
+    const int steps = (k + per - 1) / per * (mode == kPlanGradX ? 2 : 1);
+    int shares = 1;
+    if (mode != kPlanGradW && tiles > 0 && tiles < kComputeUnits) {
+        shares = (int)(kComputeUnits / tiles);
+        if (shares > steps / kShareSteps) shares = steps / kShareSteps;
+        if (shares < 1) shares = 1;
+    }
+    p.share_steps = steps > 0 ? (steps + shares - 1) / shares : 1;
+    p.shares = steps > 0 ? (steps + p.share_steps - 1) / p.share_steps : 1;
+    const int quads = (n + 3) / 4 * 4;
+    p.part_pitch = mode == kPlanGated ? 2 * quads : quads;
+    if (p.shares > 1) p.part_bytes = round256((size_t)p.shares * m * p.part_pitch * 4);
+    if (mode == kPlanInt8 || mode == kPlanGated) {
+        const size_t row = (size_t)chunk_pitch(k, size) * size;
+        p.p_bytes = round256((size_t)m * row);
+        p.q_bytes = round256((size_t)n * row * (mode == kPlanGated ? 2 : 1));
+    }
+    return p;
+}
+
+inline size_t rows_product_bytes(int mode, int size, int m, int n, int k, bool whole)
+{
+    const ProductPlan p = plan_product(mode, size, m, n, k, whole);
+    return p.part_bytes + (whole ? 0 : p.p_bytes + p.q_bytes);
+}
+
+// The gated gradient's scratch: d_gate and d_up, then what its two products need in turn --
+// copies of w_gate and w_up and the shares of grad_x, and a copy of x.
+struct VjpPlan {
+    size_t slopes, w_copy, part, x_copy;
+    size_t bytes(bool w_whole, bool x_whole, bool want_x, bool want_w) const
+    {
+        const size_t gx = want_x ? (w_whole ? 0 : 2 * w_copy) + part : 0, gw = want_w && !x_whole ? x_copy : 0;
+        return slopes + (gx > gw ? gx : gw);
+    }
+};
+inline VjpPlan plan_vjp(int M, int F, int K)
+{
+    VjpPlan v;
+    const size_t row = (size_t)chunk_pitch(K, 2) * 2;
+    v.slopes = round256((size_t)2 * 2 * M * slope_pitch(F));
+    v.w_copy = round256((size_t)F * row);
+    v.x_copy = round256((size_t)M * row);
+    v.part = plan_product(kPlanGradX, 2, M, K, F, true).part_bytes;
+    return v;
 }
 
 struct GatedCall {
@@ -47,9 +144,10 @@ qtcq_status launch_decode_matrix(int L, const CodeSel& code, bool tb, const uint
                                  void* w, int64_t ldw, float* scale, hipStream_t st);
 qtcq_status launch_matmul_int8(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* w, int64_t ldw,
                                const float* w_scale, int M, int N, int K, int dtype, void* y, int64_t ldy,
-                               hipStream_t st);
-qtcq_status launch_gated_forward(const GatedCall& c, hipStream_t st);
-qtcq_status launch_gated_vjp(const GatedVjpCall& c, void* ws, hipStream_t st);
+                               void* ws, size_t wsb, hipStream_t st);
+// these check the workspace against what the call's pointers and strides need
+qtcq_status launch_gated_forward(const GatedCall& c, void* ws, size_t wsb, hipStream_t st);
+qtcq_status launch_gated_vjp(const GatedVjpCall& c, void* ws, size_t wsb, hipStream_t st);
 
 }  // namespace host
 }  // namespace qtcq

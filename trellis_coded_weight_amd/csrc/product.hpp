@@ -1,0 +1,201 @@
+// product.hpp -- what the matrix products share, gfx950: the 8-bit product with token and
+// channel scales, the gated projections and the two products of their gradient.
+//
+// Every one of them is out[i][j] = sum_k P(i, k) Q(j, k) over one or two pairs of operands,
+// with an epilogue of its own:
+//   kInt8    P = a [M][K], Q = w [N][K]; out = acc * a_scale[i] * w_scale[j]
+//   kGated   P = x [M][K], Q = Wg and Wu [F][K], both in one workgroup; out = act(gate) * up
+//   kGradX   P = dg then du [M][F], Q(j, k) = Wg[k][j] then Wu[k][j]; one sum over both
+//   kGradW   P(i, k) = dg[k][i] (z = 0) or du[k][i] (z = 1), Q(j, k) = x[k][j]
+//
+// v_mfma_*_16x16x(64 bytes) on Q rows times P rows: lane l holds 16 bytes of Q row l % 16
+// and of P row l % 16 from byte 16 (l / 16) of a 64-byte step, and the result
+// D[4 (l / 16) + v][l % 16], v = 0..3: four consecutive columns j of the row i = l % 16,
+// stored together.  Sums are held in binary32 (int32 for kInt8, where they are exact:
+// K <= 131071).
+//
+// Two kernels share the work: few rows of P, rows on any element (skinny_product.hpp), and
+// any number of rows on whole 16-byte chunks (block_product.hpp).  Operands that are not
+// whole chunks go to the second through a copy with a padded pitch (pad_rows).
+#pragma once
+
+#include "dense.hpp"
+
+namespace qtcq {
+
+enum : int { kInt8 = 0, kGated = 1, kGradX = 2, kGradW = 3 };
+
+struct ProductArgs {
+    const void* p[2];        // operand P (kGradX, kGradW: dg and du)
+    const void* q[2];        // operand Q (kGated, kGradX: Wg and Wu)
+    int64_t ldp, ldq;        // their row strides, in elements
+    void* out[2];            // out (kGradW: both weight gradients)
+    int64_t ldo;
+    int m, n, k;             // rows and columns of out, length of one sum
+    int pk, qk;              // k of operands stored [row][k], with their zero padding
+    int pm, qn;              // rows of operands stored [k][row], with their padding
+    const float* p_scale;    // kInt8
+    const float* q_scale;
+    void* save[2];           // kGated: the projections, or NULL
+    int64_t lds;
+    void* part;              // sums of a share of k [splits][m][part_pitch], or NULL
+    int part_pitch;
+    int split_steps;         // steps of k of a share
+};
+
+template <typename T> struct Mfma;
+template <> struct Mfma<__bf16> {
+    typedef f32x4 Acc;
+    static __device__ __forceinline__ Acc mul(u32x4 a, u32x4 b, Acc c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
+                                                       c, 0, 0, 0);
+    }
+};
+template <> struct Mfma<_Float16> {
+    typedef f32x4 Acc;
+    static __device__ __forceinline__ Acc mul(u32x4 a, u32x4 b, Acc c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b),
+                                                      c, 0, 0, 0);
+    }
+};
+template <> struct Mfma<int8_t> {
+    typedef i32x4 Acc;
+    static __device__ __forceinline__ Acc mul(u32x4 a, u32x4 b, Acc c)
+    {
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b),
+                                                     c, 0, 0, 0);
+    }
+};
+
+// 16 bytes at p, which need only be aligned to their element
+template <typename T>
+__device__ __forceinline__ u32x4 load_loose(const T* p)
+{
+    struct __attribute__((packed, aligned(sizeof(T)))) Loose { u32x4 v; };
+    return reinterpret_cast<const Loose*>(p)->v;
+}
+
+// 16 bytes at p + at of a row with n elements, zero past its end
+template <typename T>
+__device__ __forceinline__ u32x4 load_chunk(const T* p, int at, int n)
+{
+    constexpr int E = 16 / (int)sizeof(T);
+    if (at + E <= n) return load_loose(p + at);
+    struct Parts { T e[E]; } o;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o.e[e] = at + e < n ? p[at + e] : (T)0;
+    return __builtin_bit_cast(u32x4, o);
+}
+
+// four consecutive outputs of a row, of which n are inside the matrix (stores need no
+// alignment beyond the element's here)
+template <typename O>
+__device__ __forceinline__ void store4(O* p, const float (&v)[4], int n)
+{
+    struct __attribute__((packed, aligned(sizeof(O)))) Four { O e[4]; };
+    if (n >= 4) {
+        *reinterpret_cast<Four*>(p) = Four{{from_f32<O>(v[0]), from_f32<O>(v[1]), from_f32<O>(v[2]), from_f32<O>(v[3])}};
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+        if (e < n) p[e] = from_f32<O>(v[e]);
+}
+
+// Four consecutive results of row `row` from column `col`, `left` of them inside the matrix:
+// s their sums (kGated: the gate's, and u the up's).
+template <typename O, int MODE, int ACT, typename Acc>
+__device__ __forceinline__ void finish4(const ProductArgs& a, int z, int row, int col, int left, const Acc& s, const Acc& u)
+{
+    float v[4];
+    if constexpr (MODE == kGated) {
+        const float gv[4] = {s[0], s[1], s[2], s[3]}, uv[4] = {u[0], u[1], u[2], u[3]};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = activate<ACT>(gv[e]) * uv[e];
+        if (a.save[0]) {
+            store4(static_cast<O*>(a.save[0]) + (int64_t)row * a.lds + col, gv, left);
+            store4(static_cast<O*>(a.save[1]) + (int64_t)row * a.lds + col, uv, left);
+        }
+    } else if constexpr (MODE == kInt8) {
+        const float ps = a.p_scale[row];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = (float)s[e] * ps * (e < left ? a.q_scale[col + e] : 0.0f);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = s[e];
+    }
+    store4(static_cast<O*>(a.out[z]) + (int64_t)row * a.ldo + col, v, left);
+}
+
+// The shares of k added in order, then the epilogue.  part [splits][m][part_pitch], four
+// columns a thread (kGated: the gate's sums, then the up's, part_pitch / 2 apart).
+//   grid.x covers m * (columns / 4) threads, block = 256.
+template <typename T, typename O, int MODE, int ACT>
+__global__ void __launch_bounds__(256)
+join_shares(ProductArgs a, int splits)
+{
+    typedef typename Mfma<T>::Acc Acc;
+    const int width = MODE == kGated ? a.part_pitch / 2 : a.part_pitch, per = width >> 2;
+    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x, row = t / per;
+    if (row >= a.m) return;
+    const int col = (int)(t - row * per) * 4;
+    const int64_t next = (int64_t)a.m * a.part_pitch >> 2, at = (row * a.part_pitch + col) >> 2;
+    const Acc* p = static_cast<const Acc*>(a.part) + at;
+    Acc s = {}, u = {};
+    for (int i = 0; i < splits; ++i) {
+        s += p[i * next];
+        if constexpr (MODE == kGated) u += p[i * next + (width >> 2)];
+    }
+    finish4<O, MODE, ACT>(a, 0, (int)row, col, a.n - col, s, u);
+}
+
+// Rows of `cols` elements, on any element, to rows of whole 16-byte chunks, zero past cols.
+//   grid.x covers rows * (pitch / E) threads, block = 256; pitch a multiple of E.
+template <typename T>
+__global__ void __launch_bounds__(256)
+pad_rows(const T* __restrict__ src, int64_t ld, int64_t rows, int cols, T* __restrict__ dst, int pitch)
+{
+    constexpr int E = 16 / (int)sizeof(T);
+    const int per = pitch / E;
+    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x, row = t / per;
+    if (row >= rows) return;
+    const int at = (int)(t - row * per) * E;
+    *reinterpret_cast<u32x4*>(dst + row * pitch + at) = load_chunk<T>(src + row * ld, at, cols);
+}
+
+// dg = dh u act'(g) and du = dh act(g), each formed in binary32 and rounded once to the
+// operands' type, the operand type of the matrix instructions that take them next.  The
+// rounding's relative 2^-9 (bf16) or 2^-12 (fp16) a term adds in squares over a sum, about
+// what the rounding of the gradient itself costs.  d [2][M][ldd]: columns from F to ldd
+// are written as zero.
+//   grid.x covers M * ldd / 8 chunks of 8 columns, block = 256; ldd a multiple of 8.
+template <typename T, int ACT>
+__global__ void __launch_bounds__(256)
+gated_slopes(const T* __restrict__ gate, const T* __restrict__ up, int64_t ldg, const T* __restrict__ gh, int64_t ldh,
+             int64_t M, int F, int ldd, T* __restrict__ dgate, T* __restrict__ dup)
+{
+    typedef T T8 __attribute__((ext_vector_type(8)));
+    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int per = ldd >> 3;
+    const int64_t row = c / per;
+    if (row >= M) return;
+    const int col = (int)(c - row * per) * 8;
+    const T8 g = __builtin_bit_cast(T8, load_chunk<T>(gate + row * ldg, col, F));
+    const T8 u = __builtin_bit_cast(T8, load_chunk<T>(up + row * ldg, col, F));
+    const T8 h = __builtin_bit_cast(T8, load_chunk<T>(gh + row * ldh, col, F));
+    T8 dg, du;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        float av, dv;
+        activate_grad<ACT>((float)g[e], av, dv);
+        const float hv = (float)h[e];
+        dg[e] = col + e < F ? from_f32<T>(hv * (float)u[e] * dv) : (T)0.0f;
+        du[e] = col + e < F ? from_f32<T>(hv * av) : (T)0.0f;
+    }
+    *reinterpret_cast<T8*>(dgate + row * ldd + col) = dg;
+    *reinterpret_cast<T8*>(dup + row * ldd + col) = du;
+}
+
+}  // namespace qtcq

@@ -1,0 +1,140 @@
+// product_launch.hpp -- which kernel a product takes (skinny_product.hpp or
+// block_product.hpp), its workspace and its launch, shared by the products' launch units.
+#pragma once
+
+#include "dense_host.hpp"
+#include "block_product.hpp"
+#include "skinny_product.hpp"
+
+namespace qtcq {
+namespace host {
+
+static_assert(kPlanGated == kGated && kPlanInt8 == kInt8 && kPlanGradX == kGradX && kPlanGradW == kGradW, "modes");
+
+// f(int_c<ACT>{})
+template <typename F>
+qtcq_status with_act(int act, F&& f)
+{
+    switch (act) {
+    case kActSilu: return f(int_c<kActSilu>{});
+    case kActGelu: return f(int_c<kActGelu>{});
+    case kActGeluTanh: return f(int_c<kActGeluTanh>{});
+    case kActRelu: return f(int_c<kActRelu>{});
+    default: return f(int_c<kActSigmoid>{});
+    }
+}
+
+// Few rows of P: 16 MI rows by 16 NJ columns a workgroup.  DEPTH blocks in flight fill the
+// registers that the sums leave.
+template <typename T, typename O, int MODE, int ACT, int MI, int NJ, bool ALIGNED>
+qtcq_status skinny_shape(const ProductArgs& a, hipStream_t st)
+{
+    constexpr int frags = 2 * (MI + (MODE == kGated ? 2 * NJ : NJ));
+    constexpr int DEPTH = frags <= 8 ? 4 : (frags <= 12 ? 3 : 2);
+    const int64_t n = (int64_t)blocks_for(a.m, 16 * MI) * blocks_for(a.n, 16 * NJ);
+    const dim3 grid((unsigned)n), block(SkinnyShape::kThreads);
+    hipLaunchKernelGGL((skinny_product<T, O, MODE, ACT, MI, NJ, DEPTH, ALIGNED>), grid, block, 0, st, a);
+    return launch_status();
+}
+
+template <typename T, typename O, int MODE, int ACT>
+qtcq_status skinny_go(const ProductArgs& a, bool whole, hipStream_t st)
+{
+    constexpr int WIDE = MODE == kGated ? 1 : 2;
+    // two groups of columns a workgroup, which halves the reads of P, where that leaves two
+    // workgroups a compute unit
+    const bool wide = a.n >= 16 * WIDE * 512;
+    return with_bool(whole, [&](auto al) {
+        constexpr bool ALIGNED = decltype(al)::value;
+        auto go = [&](auto mi) {
+            constexpr int MI = decltype(mi)::value;
+            return wide ? skinny_shape<T, O, MODE, ACT, MI, WIDE, ALIGNED>(a, st)
+                        : skinny_shape<T, O, MODE, ACT, MI, 1, ALIGNED>(a, st);
+        };
+        if (a.m <= 16) return go(int_c<1>{});
+        if (a.m <= 32) return go(int_c<2>{});
+        return go(int_c<4>{});
+    });
+}
+
+template <typename T, typename O, int MODE, int ACT, int FP>
+qtcq_status block_shape(ProductArgs a, const ProductPlan& p, hipStream_t st)
+{
+    const int64_t n = (int64_t)blocks_for(a.m, BlockShape::rows(FP)) * blocks_for(a.n, BlockShape::cols(MODE));
+    const dim3 grid((unsigned)n, (unsigned)p.shares, MODE == kGradW ? 2 : 1);
+    hipLaunchKernelGGL((block_product<T, O, MODE, ACT, FP>), grid, dim3(BlockShape::kThreads), 0, st, a);
+    if constexpr (MODE != kGradW)
+        if (p.shares > 1) {
+            const int64_t quads = (int64_t)a.m * (MODE == kGated ? p.part_pitch / 8 : p.part_pitch / 4);
+            hipLaunchKernelGGL((join_shares<T, O, MODE, ACT>), dim3(blocks_for(quads, 256)), dim3(256), 0, st, a, p.shares);
+        }
+    return launch_status();
+}
+
+// `part`: p.part_bytes of scratch
+template <typename T, typename O, int MODE, int ACT>
+qtcq_status block_go(ProductArgs a, const ProductPlan& p, void* part, hipStream_t st)
+{
+    a.part = p.shares > 1 ? part : nullptr;
+    a.part_pitch = p.part_pitch;
+    a.split_steps = p.share_steps;
+    if constexpr (MODE != kGradW) {
+        if (p.fp == 2) return block_shape<T, O, MODE, ACT, 2>(a, p, st);
+        if (p.fp == 4) return block_shape<T, O, MODE, ACT, 4>(a, p, st);
+    }
+    return block_shape<T, O, MODE, ACT, 8>(a, p, st);
+}
+
+// Rows that start on 16 bytes and whose last chunk is whole, `inner` elements long, at a
+// stride the block kernel's offsets hold.
+template <typename T>
+bool whole_chunks(const void* p, int64_t ld, int inner)
+{
+    constexpr int E = 16 / (int)sizeof(T);
+    return aligned16(p) && ld % E == 0 && inner % E == 0 && ld * (int64_t)sizeof(T) <= BlockShape::kMaxStride;
+}
+
+template <typename T>
+void pad_go(const void* src, int64_t ld, int64_t rows, int cols, void* dst, hipStream_t st)
+{
+    const int pitch = chunk_pitch(cols, (int)sizeof(T));
+    const int64_t n = rows * (pitch / (16 / (int)sizeof(T)));
+    if (n == 0) return;
+    hipLaunchKernelGGL(pad_rows<T>, dim3(blocks_for(n, 256)), dim3(256), 0, st, static_cast<const T*>(src), ld, rows,
+                       cols, static_cast<T*>(dst), pitch);
+}
+
+// kInt8 and kGated: both operands stored [row][k].
+template <typename T, typename O, int MODE, int ACT = 0>
+qtcq_status rows_product(ProductArgs a, void* ws, size_t wsb, hipStream_t st)
+{
+    constexpr int QS = MODE == kGated ? 2 : 1;
+    const bool pw = whole_chunks<T>(a.p[0], a.ldp, a.k);
+    const bool qw = whole_chunks<T>(a.q[0], a.ldq, a.k) && (QS == 1 || aligned16(a.q[1]));
+    const ProductPlan plan = plan_product(MODE, (int)sizeof(T), a.m, a.n, a.k, pw && qw);
+    if (plan.skinny) return skinny_go<T, O, MODE, ACT>(a, pw && qw, st);
+    const size_t pb = pw ? 0 : plan.p_bytes, qb = qw ? 0 : plan.q_bytes;
+    const size_t need = plan.part_bytes + pb + qb;
+    if (need > 0 && (!ws || !aligned16(ws) || wsb < need)) return QTCQ_ERR_WORKSPACE;
+    char* at = static_cast<char*>(ws) + plan.part_bytes;
+    a.pk = a.qk = a.k;
+    if (!pw) {
+        pad_go<T>(a.p[0], a.ldp, a.m, a.k, at, st);
+        a.p[0] = at;
+        a.ldp = a.pk = chunk_pitch(a.k, (int)sizeof(T));
+        at += pb;
+    }
+    if (!qw) {
+        a.qk = chunk_pitch(a.k, (int)sizeof(T));
+        for (int i = 0; i < QS; ++i) {
+            pad_go<T>(a.q[i], a.ldq, a.n, a.k, at, st);
+            a.q[i] = at;
+            at += (size_t)a.n * a.qk * sizeof(T);
+        }
+        a.ldq = a.qk;
+    }
+    return block_go<T, O, MODE, ACT>(a, plan, ws, st);
+}
+
+}  // namespace host
+}  // namespace qtcq

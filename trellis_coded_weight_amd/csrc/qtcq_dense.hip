@@ -1,6 +1,6 @@
 // qtcq_dense.hip -- the C ABI of the dense operators (include/qtcq.h, "Dense operators
-// around the codec"): argument validation; accepted calls go to launch_rows.hip and
-// launch_products.hip.
+// around the codec"): argument validation; accepted calls go to launch_rows.hip,
+// launch_int8.hip, launch_gated.hip and launch_gated_vjp.hip.
 #include "dense_host.hpp"
 
 namespace host = qtcq::host;
@@ -25,11 +25,15 @@ bool tiles_ok(int64_t rows, int64_t cols)
     return ((rows + 127) / 128) * ((cols + 63) / 64) <= kDenseMaxTiles;
 }
 
+bool gated_sizes_ok(int M, int F, int K)
+{
+    return M >= 0 && F >= 0 && K >= 0 && M <= kDenseMaxDim && F <= kHalfMaxRow && K <= kHalfMaxRow && tiles_ok(M, F);
+}
+
 bool vjp_sizes_ok(int M, int F, int K)
 {
     // the elementwise kernel's grid: one thread per 8 of M slope_pitch(F) elements
-    return M >= 0 && F >= 0 && K >= 0 && M <= kDenseMaxDim && F <= kDenseMaxDim && K <= kDenseMaxDim &&
-           (int64_t)M * slope_pitch(F) <= (int64_t)1 << 34 && tiles_ok(M, K) && tiles_ok(F, K);
+    return gated_sizes_ok(M, F, K) && (int64_t)M * slope_pitch(F) <= (int64_t)1 << 34 && tiles_ok(M, K) && tiles_ok(F, K);
 }
 
 }  // namespace
@@ -63,8 +67,15 @@ qtcq_status qtcq_decode_matrix(const uint32_t* bits, int M, int N, int L, int k,
     return host::launch_decode_matrix(L, cs, tailbiting != 0, bits, M, N, dtype, w, ldw, scale, as_stream(stream));
 }
 
+size_t qtcq_matmul_int8_workspace_bytes(int M, int N, int K, int whole_rows)
+{
+    if (M < 0 || N < 0 || K < 0 || M > kDenseMaxDim || N > kDenseMaxDim || K > kInt8MaxK || !tiles_ok(M, N)) return 0;
+    return rows_product_bytes(kPlanInt8, 1, M, N, K, whole_rows != 0);
+}
+
 qtcq_status qtcq_matmul_int8(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* w, int64_t ldw,
-                             const float* w_scale, int M, int N, int K, int dtype, void* y, int64_t ldy, void* stream)
+                             const float* w_scale, int M, int N, int K, int dtype, void* y, int64_t ldy, void* workspace,
+                             size_t workspace_bytes, void* stream)
 {
     if (M < 0 || N < 0 || K < 0 || lda < K || ldw < K || ldy < N) return QTCQ_ERR_INVALID_ARG;
     if (!float_type(dtype) || M > kDenseMaxDim || N > kDenseMaxDim || K > kInt8MaxK || !tiles_ok(M, N))
@@ -73,30 +84,36 @@ qtcq_status qtcq_matmul_int8(const int8_t* a, int64_t lda, const float* a_scale,
     if (!there(a, M, K, 1) || !there(w, N, K, 1) || !there(a_scale, M, 1, 4) || !there(w_scale, N, 1, 4) ||
         !there(y, M, N, type_size(dtype)))
         return QTCQ_ERR_INVALID_ARG;
-    return host::launch_matmul_int8(a, lda, a_scale, w, ldw, w_scale, M, N, K, dtype, y, ldy, as_stream(stream));
+    return host::launch_matmul_int8(a, lda, a_scale, w, ldw, w_scale, M, N, K, dtype, y, ldy, workspace, workspace_bytes,
+                                    as_stream(stream));
+}
+
+size_t qtcq_gated_workspace_bytes(int M, int F, int K, int whole_rows)
+{
+    if (!gated_sizes_ok(M, F, K)) return 0;
+    return rows_product_bytes(kPlanGated, 2, M, F, K, whole_rows != 0);
 }
 
 qtcq_status qtcq_gated_forward(const void* x, int64_t ldx, const void* w_gate, const void* w_up, int64_t ldw, int dtype,
                                int M, int F, int K, int activation, void* h, int64_t ldh, void* gate, void* up,
-                               int64_t ldg, void* stream)
+                               int64_t ldg, void* workspace, size_t workspace_bytes, void* stream)
 {
     if (M < 0 || F < 0 || K < 0 || ldx < K || ldw < K || ldh < F) return QTCQ_ERR_INVALID_ARG;
     if ((gate == nullptr) != (up == nullptr) || (gate && ldg < F)) return QTCQ_ERR_INVALID_ARG;
     if (!half_type(dtype) || activation < QTCQ_ACT_SILU || activation > QTCQ_ACT_SIGMOID) return QTCQ_ERR_UNSUPPORTED;
-    if (M > kDenseMaxDim || F > kDenseMaxDim || K > kDenseMaxDim || !tiles_ok(M, F)) return QTCQ_ERR_UNSUPPORTED;
+    if (!gated_sizes_ok(M, F, K)) return QTCQ_ERR_UNSUPPORTED;
     if (M == 0 || F == 0) return QTCQ_OK;
     if (!there(x, M, K, 2) || !there(w_gate, F, K, 2) || !there(w_up, F, K, 2) || !there(h, M, F, 2) ||
         !aligned_to(gate, 2) || !aligned_to(up, 2))
         return QTCQ_ERR_INVALID_ARG;
     const GatedCall c = {x, w_gate, w_up, ldx, ldw, dtype, M, F, K, activation, h, ldh, gate, up, ldg};
-    return host::launch_gated_forward(c, as_stream(stream));
+    return host::launch_gated_forward(c, workspace, workspace_bytes, as_stream(stream));
 }
 
-size_t qtcq_gated_vjp_workspace_bytes(int M, int F, int K)
+size_t qtcq_gated_vjp_workspace_bytes(int M, int F, int K, int whole_rows)
 {
     if (!vjp_sizes_ok(M, F, K)) return 0;
-    const size_t n = gated_vjp_bytes(M, F);
-    return n > 0 ? n : 256;
+    return plan_vjp(M, F, K).bytes(whole_rows != 0, whole_rows != 0, true, true);
 }
 
 qtcq_status qtcq_gated_vjp(const void* x, int64_t ldx, const void* w_gate, const void* w_up, int64_t ldw,
@@ -118,12 +135,10 @@ qtcq_status qtcq_gated_vjp(const void* x, int64_t ldx, const void* w_gate, const
         return QTCQ_ERR_INVALID_ARG;
     if (want_w && (!aligned_to(grad_w_gate, 2) || !aligned_to(grad_w_up, 2) || !there(x, M, K, 2)))
         return QTCQ_ERR_INVALID_ARG;
-    if (!workspace || !aligned16(workspace) || workspace_bytes < qtcq_gated_vjp_workspace_bytes(M, F, K))
-        return QTCQ_ERR_WORKSPACE;
     const GatedVjpCall c = {x, w_gate, w_up, gate, up, grad_h, ldx, ldw, ldg, ldgh, dtype, M, F, K, activation,
                             want_x ? grad_x : nullptr, want_w ? grad_w_gate : nullptr, want_w ? grad_w_up : nullptr,
                             ldgx, ldgw};
-    return host::launch_gated_vjp(c, workspace, as_stream(stream));
+    return host::launch_gated_vjp(c, workspace, workspace_bytes, as_stream(stream));
 }
 
 }  // extern "C"
