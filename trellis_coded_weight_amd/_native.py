@@ -258,16 +258,19 @@ def qtcq_decode_matvec_mfma_noalloc(bits: int, M: int, N: int, L: int, k: int, c
            "qtcq_decode_matvec_mfma_noalloc")
 
 
+# The dense operators' calls pass pointers as they are (an int, or None): ctypes converts
+# them by the signatures above.
+
 def qtcq_quantize_rows(x: int, dtype: int, rows: int, cols: int, ldx: int, q: int, ldq: int,
                        scale: int, stream: int = 0) -> None:
-    _check(_lib.qtcq_quantize_rows(_ptr(x), dtype, rows, cols, ldx, _ptr(q), ldq, _ptr(scale),
-                                   _ptr(stream)), "qtcq_quantize_rows")
+    _check(_lib.qtcq_quantize_rows(x, dtype, rows, cols, ldx, q, ldq, scale,
+                                   stream), "qtcq_quantize_rows")
 
 
 def qtcq_decode_matrix(bits: int, M: int, N: int, L: int, k: int, code: int, tailbiting: bool,
                        dtype: int, w: int, ldw: int, scale, stream: int = 0) -> None:
-    _check(_lib.qtcq_decode_matrix(_ptr(bits), M, N, L, k, code, 1 if tailbiting else 0, dtype,
-                                   _ptr(w), ldw, _ptr(scale), _ptr(stream)), "qtcq_decode_matrix")
+    _check(_lib.qtcq_decode_matrix(bits, M, N, L, k, code, 1 if tailbiting else 0, dtype,
+                                   w, ldw, scale, stream), "qtcq_decode_matrix")
 
 
 def qtcq_matmul_int8_workspace_bytes(M: int, N: int, K: int, whole_rows: bool) -> int:
@@ -277,9 +280,9 @@ def qtcq_matmul_int8_workspace_bytes(M: int, N: int, K: int, whole_rows: bool) -
 def qtcq_matmul_int8(a: int, lda: int, a_scale: int, w: int, ldw: int, w_scale: int, M: int,
                      N: int, K: int, dtype: int, y: int, ldy: int, workspace,
                      workspace_bytes: int, stream: int = 0) -> None:
-    _check(_lib.qtcq_matmul_int8(_ptr(a), lda, _ptr(a_scale), _ptr(w), ldw, _ptr(w_scale), M, N, K,
-                                 dtype, _ptr(y), ldy, _ptr(workspace), workspace_bytes,
-                                 _ptr(stream)), "qtcq_matmul_int8")
+    _check(_lib.qtcq_matmul_int8(a, lda, a_scale, w, ldw, w_scale, M, N, K,
+                                 dtype, y, ldy, workspace, workspace_bytes,
+                                 stream), "qtcq_matmul_int8")
 
 
 def qtcq_gated_workspace_bytes(M: int, F: int, K: int, whole_rows: bool) -> int:
@@ -289,9 +292,9 @@ def qtcq_gated_workspace_bytes(M: int, F: int, K: int, whole_rows: bool) -> int:
 def qtcq_gated_forward(x: int, ldx: int, w_gate: int, w_up: int, ldw: int, dtype: int, M: int,
                        F: int, K: int, activation: int, h: int, ldh: int, gate, up, ldg: int,
                        workspace, workspace_bytes: int, stream: int = 0) -> None:
-    _check(_lib.qtcq_gated_forward(_ptr(x), ldx, _ptr(w_gate), _ptr(w_up), ldw, dtype, M, F, K,
-                                   activation, _ptr(h), ldh, _ptr(gate), _ptr(up), ldg,
-                                   _ptr(workspace), workspace_bytes, _ptr(stream)),
+    _check(_lib.qtcq_gated_forward(x, ldx, w_gate, w_up, ldw, dtype, M, F, K,
+                                   activation, h, ldh, gate, up, ldg,
+                                   workspace, workspace_bytes, stream),
            "qtcq_gated_forward")
 
 
@@ -303,7 +306,7 @@ def qtcq_gated_vjp(x, ldx: int, w_gate, w_up, ldw: int, gate: int, up: int, ldg:
                    ldgh: int, dtype: int, M: int, F: int, K: int, activation: int, grad_x,
                    ldgx: int, grad_w_gate, grad_w_up, ldgw: int, workspace: int,
                    workspace_bytes: int, stream: int = 0) -> None:
-    _check(_lib.qtcq_gated_vjp(_ptr(x), ldx, _ptr(w_gate), _ptr(w_up), ldw, _ptr(gate), _ptr(up),
-                               ldg, _ptr(grad_h), ldgh, dtype, M, F, K, activation, _ptr(grad_x),
-                               ldgx, _ptr(grad_w_gate), _ptr(grad_w_up), ldgw, _ptr(workspace),
-                               workspace_bytes, _ptr(stream)), "qtcq_gated_vjp")
+    _check(_lib.qtcq_gated_vjp(x, ldx, w_gate, w_up, ldw, gate, up,
+                               ldg, grad_h, ldgh, dtype, M, F, K, activation, grad_x,
+                               ldgx, grad_w_gate, grad_w_up, ldgw, workspace,
+                               workspace_bytes, stream), "qtcq_gated_vjp")

@@ -30,7 +30,9 @@ def _code(code) -> int:
 
 
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    # the handle alone: building a torch Stream around it takes longer than the rest of a
+    # small call's checks together
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _on_current_device(x: torch.Tensor, name: str) -> None:
@@ -407,15 +409,16 @@ def _rows(x: torch.Tensor, name: str, dtypes, shape=None) -> int:
     if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dim() == 2 and x.dtype in dtypes):
         raise ValueError("%s must be a 2-D device tensor of %s"
                          % (name, " or ".join(str(d) for d in dtypes)))
-    _on_current_device(x, name)
+    if x.get_device() != torch.cuda.current_device():
+        _on_current_device(x, name)
     if shape is not None and tuple(x.shape) != tuple(shape):
         raise ValueError("%s must be %s" % (name, list(shape)))
-    rows, cols = x.shape
-    if rows == 0 or cols == 0:
+    cols = x.shape[1]
+    if x.is_contiguous():
         return cols
     if cols > 1 and x.stride(1) != 1:
         raise ValueError("%s must have contiguous rows" % name)
-    if rows == 1:
+    if x.shape[0] == 1:
         return cols
     if x.stride(0) < cols:
         raise ValueError("the rows of %s overlap" % name)
@@ -424,18 +427,22 @@ def _rows(x: torch.Tensor, name: str, dtypes, shape=None) -> int:
 
 def _scales(s: torch.Tensor, name: str, n: int) -> None:
     if not (isinstance(s, torch.Tensor) and s.is_cuda and s.dtype == torch.float32
-            and tuple(s.shape) == (n,) and s.is_contiguous()):
+            and s.dim() == 1 and s.shape[0] == n and s.is_contiguous()):
         raise ValueError("%s must be a contiguous float32 device tensor of %d values" % (name, n))
-    _on_current_device(s, name)
+    if s.get_device() != torch.cuda.current_device():
+        _on_current_device(s, name)
 
 
 def _whole_rows(*xs) -> bool:
     """Whether the kernels can read these operands in 16-byte chunks where they are
     (otherwise the workspace holds padded copies)."""
-    return all(x.data_ptr() % 16 == 0 and x.shape[1] * x.element_size() % 16 == 0
-               and (x.shape[0] < 2 or (x.stride(0) * x.element_size() % 16 == 0
-                                       and x.stride(0) * x.element_size() <= 1 << 22))
-               for x in xs)
+    for x in xs:
+        size = x.element_size()
+        if (x.data_ptr() | x.shape[1] * size) & 15:
+            return False
+        if x.shape[0] > 1 and (x.stride(0) * size & 15 or x.stride(0) * size > 1 << 22):
+            return False
+    return True
 
 
 def _workspace(workspace, nbytes: int, like: torch.Tensor):

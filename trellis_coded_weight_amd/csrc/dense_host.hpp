@@ -40,10 +40,6 @@ struct ProductPlan {
 
 // The compute units of the chip the tile and share counts are chosen for.
 constexpr int kComputeUnits = 256;
-// shares of k hold at least this many steps: a share's first loads and its sums' way
-// through memory cost about as much as six steps
-constexpr int kShareSteps = 8;
-
 // Whether the kernel for few rows takes a product.  It reads Q once at the memory's rate and
 // P once for every 16 columns, so its time grows with m n k; the block kernel's hardly does
 // up to 128 rows, but it pays for shares of k and a second launch.  Measured (us, few rows
@@ -69,26 +65,34 @@ inline ProductPlan plan_product(int mode, int size, int m, int n, int k, bool wh
         p.skinny = true;
         return p;
     }
-    p.fp = mode == kPlanGradW ? 8 : (m <= 64 ? 2 : (m <= 128 ? 4 : 8));
-    const int64_t cols = mode == kPlanGated ? 128 : 256;
-    const int64_t tiles = ((int64_t)m + 32 * p.fp - 1) / (32 * p.fp) * ((n + cols - 1) / cols);
-    const int per = 128 / size;
-    const int steps = (k + per - 1) / per * (mode == kPlanGradX ? 2 : 1);
-    int shares = 1;
-    if (mode != kPlanGradW && tiles > 0 && tiles < kComputeUnits) {
-        shares = (int)(kComputeUnits / tiles);
-        if (shares > steps / kShareSteps) shares = steps / kShareSteps;
-        if (shares < 1) shares = 1;
-    }
-    p.share_steps = steps > 0 ? (steps + shares - 1) / shares : 1;
-    p.shares = steps > 0 ? (steps + p.share_steps - 1) / p.share_steps : 1;
     const int quads = (n + 3) / 4 * 4;
     p.part_pitch = mode == kPlanGated ? 2 * quads : quads;
+    const int64_t cols = mode == kPlanGated ? 128 : 256;
+    const int per = 128 / size;
+    const int steps = (k + per - 1) / per * (mode == kPlanGradX ? 2 : 1);
+    // The tile's rows and the shares of k by the shortest estimate, in us: rounds of
+    // workgroups (one a compute unit) times a share's steps, each 0.7, 1.0 or 1.7 with 64, 128
+    // or 256 rows (8192x28672 at m = 2048: 616, 442 and 392 us in 4, 2 and 1 rounds of 224
+    // steps); shares cost a second launch, and their sums' way out and back at 4 TB/s.
+    // [k][row] tiles of P are 256 rows wide.
+    double best = 0;
+    for (int fp = mode == kPlanGradW ? 8 : 2; fp <= 8; fp *= 2) {
+        const int64_t tiles = ((int64_t)m + 32 * fp - 1) / (32 * fp) * ((n + cols - 1) / cols);
+        const double step = fp == 2 ? 0.7 : (fp == 4 ? 1.0 : 1.7);
+        int64_t most = mode == kPlanGradW || tiles == 0 ? 1 : kComputeUnits / tiles;
+        if (most > steps / 4) most = steps / 4;
+        for (int s = 1; s == 1 || s <= most; ++s) {
+            const int share = steps > 0 ? (steps + s - 1) / s : 1, shares = steps > 0 ? (steps + share - 1) / share : 1;
+            double t = (double)((tiles * shares + kComputeUnits - 1) / kComputeUnits) * (share + 2) * step;
+            if (shares > 1) t += 6.0 + 8.0 * shares * m * p.part_pitch / 4e6;
+            if (p.fp == 0 || t < best) best = t, p.fp = fp, p.shares = shares, p.share_steps = share;
+        }
+    }
     if (p.shares > 1) p.part_bytes = round256((size_t)p.shares * m * p.part_pitch * 4);
     if (mode == kPlanInt8 || mode == kPlanGated) {
         const size_t row = (size_t)chunk_pitch(k, size) * size;
         p.p_bytes = round256((size_t)m * row);
-        p.q_bytes = round256((size_t)n * row * (mode == kPlanGated ? 2 : 1));
+        p.q_bytes = round256((size_t)n * row) * (mode == kPlanGated ? 2 : 1);
     }
     return p;
 }

@@ -24,7 +24,7 @@ qtcq_status gated_vjp_impl(const GatedVjpCall& c, void* ws, size_t wsb, hipStrea
     const bool ww = whole_chunks<T>(c.w_gate, c.ldw, c.K) && aligned16(c.w_up), xw = whole_chunks<T>(c.x, c.ldx, c.K);
     const size_t need = v.bytes(ww, xw, c.grad_x != nullptr, c.grad_w_gate != nullptr);
     if (need > 0 && (!ws || !aligned16(ws) || wsb < need)) return QTCQ_ERR_WORKSPACE;
-    const int ldd = slope_pitch(c.F), pitch = chunk_pitch(c.K, (int)sizeof(T));
+    const int ldd = slope_pitch(c.F);
     T* dg = static_cast<T*>(ws);
     T* du = dg + (int64_t)c.M * ldd;
     char* more = static_cast<char*>(ws) + v.slopes;
@@ -41,14 +41,12 @@ qtcq_status gated_vjp_impl(const GatedVjpCall& c, void* ws, size_t wsb, hipStrea
         a.q[1] = c.w_up;
         a.ldq = c.ldw;
         a.qn = c.K;
-        if (!ww && c.F > 0) {
-            char* copy = more + v.part;
-            for (int i = 0; i < 2; ++i) {
-                pad_go<T>(a.q[i], c.ldw, c.F, c.K, copy, st);
-                a.q[i] = copy;
-                copy += v.w_copy;
-            }
-            a.ldq = a.qn = pitch;
+        if (!ww) {
+            char* at = more + v.part;
+            PadCopies<T> copies(c.K);
+            for (int i = 0; i < 2; ++i) a.q[i] = copies.add(a.q[i], c.ldw, c.F, &at);
+            a.ldq = a.qn = copies.a.pitch;
+            copies.go(st);
         }
         a.out[0] = c.grad_x;
         a.ldo = c.ldgx;
@@ -61,10 +59,12 @@ qtcq_status gated_vjp_impl(const GatedVjpCall& c, void* ws, size_t wsb, hipStrea
         a.q[0] = c.x;
         a.ldq = c.ldx;
         a.qn = c.K;
-        if (!xw && c.M > 0) {
-            pad_go<T>(c.x, c.ldx, c.M, c.K, more, st);
-            a.q[0] = more;
-            a.ldq = a.qn = pitch;
+        if (!xw) {
+            char* at = more;
+            PadCopies<T> copies(c.K);
+            a.q[0] = copies.add(c.x, c.ldx, c.M, &at);
+            a.ldq = a.qn = copies.a.pitch;
+            copies.go(st);
         }
         a.out[0] = c.grad_w_gate;
         a.out[1] = c.grad_w_up;

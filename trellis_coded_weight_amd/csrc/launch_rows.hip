@@ -43,16 +43,17 @@ qtcq_status decode_rows_impl(const uint32_t* bits, int M, int N, int dtype, void
                              const CodeArg& ca, hipStream_t st)
 {
     const dim3 grid((unsigned)(M / 16)), block(DecodeRowsShape::kThreads);
-    auto go = [&](auto out) {
-        hipLaunchKernelGGL((decode_rows<L, CODE, TB, decltype(out)::value>), grid, block, 0, st, bits, N / 16, w, ldw,
-                           scale, ca);
+    auto go = [&](auto out, auto hold) {
+        hipLaunchKernelGGL((decode_rows<L, CODE, TB, decltype(out)::value, decltype(hold)::value>), grid, block, 0, st,
+                           bits, N / 16, w, ldw, scale, ca);
         return launch_status();
     };
     switch (dtype) {
-    case QTCQ_I8: return go(int_c<0>{});
-    case QTCQ_BF16: return go(int_c<1>{});
-    case QTCQ_F16: return go(int_c<2>{});
-    default: return go(int_c<3>{});
+    // codes held between the passes: 32 registers for up to 4096 columns, 64 beyond
+    case QTCQ_I8: return N <= 16 * DecodeRowsShape::kTiles ? go(int_c<0>{}, int_c<1>{}) : go(int_c<0>{}, int_c<2>{});
+    case QTCQ_BF16: return go(int_c<1>{}, int_c<1>{});
+    case QTCQ_F16: return go(int_c<2>{}, int_c<1>{});
+    default: return go(int_c<3>{}, int_c<1>{});
     }
 }
 

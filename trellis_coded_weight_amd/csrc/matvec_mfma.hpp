@@ -49,7 +49,6 @@
 namespace qtcq {
 
 typedef _Float16 mv_half8 __attribute__((ext_vector_type(8)));
-typedef _Float16 mv_half2 __attribute__((ext_vector_type(2)));
 typedef float mv_float4 __attribute__((ext_vector_type(4)));
 
 struct MatvecMfmaShape {
@@ -136,42 +135,6 @@ matvec_split_x(const float* __restrict__ x, int N, int nkb, int batch, uint4* __
     }
     xs[(size_t)kf * 64 + l] = __builtin_bit_cast(uint4, h);
     if (l < 8) sc[(size_t)kf * 8 + l] = __builtin_ldexpf(1.0f, -s);
-}
-
-// A constant copied into a VGPR (opaque to the compiler, so it stays a VGPR operand).
-__device__ __forceinline__ uint32_t vgpr_u32(uint32_t c)
-{
-    uint32_t v;
-    asm("v_mov_b32 %0, %1" : "=v"(v) : "s"(c));
-    return v;
-}
-
-// Two windows' codes before their rescale, as one packed pair of fp16.
-//   kbias: fp16 -1534 in both halves, in a VGPR
-template <int CODE>
-__device__ __forceinline__ uint32_t code_raw_pair_f16(uint32_t w0, uint32_t w1, uint32_t kbias,
-                                                      const CodeArg& ca)
-{
-    if constexpr (CODE == kCodeXor) {
-        // palette values, exact in fp16 (so the round-toward-zero pack is exact)
-        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(code_xor(w0, ca), code_xor(w1, ca)));
-    } else if constexpr (CODE == kCode1Mad) {
-        // byte sums into both halves of an accumulator 0x64006400 (fp16 1024 twice):
-        // v_sad_u8 adds S0 to the low half, v_sad_hi_u8 adds S1 << 16, so the halves read
-        // 1024 + S0 and 1024 + S1 exactly (S <= 1020, no carry between them); one packed
-        // fp16 subtraction of 1534 gives S - 510
-        const uint32_t t0 = __builtin_amdgcn_sad_u8(lcg_step(w0), 0u, 0x64006400u);
-        const uint32_t t = __builtin_amdgcn_sad_hi_u8(lcg_step(w1), 0u, t0);
-        return __builtin_bit_cast(uint32_t, __builtin_bit_cast(mv_half2, t) + __builtin_bit_cast(mv_half2, kbias));
-    } else {
-        // the two halves of each (u & 0x8FFF8FFF) ^ 0x3B603B60, gathered as (lo0, lo1)
-        // and (hi0, hi1), added by one packed fp16 add (round to nearest even)
-        const uint32_t v0 = (lcg_step(w0) & 0x8FFF8FFFu) ^ 0x3B603B60u;
-        const uint32_t v1 = (lcg_step(w1) & 0x8FFF8FFFu) ^ 0x3B603B60u;
-        const uint32_t lo = __builtin_amdgcn_perm(v1, v0, 0x05040100u);
-        const uint32_t hi = __builtin_amdgcn_perm(v1, v0, 0x07060302u);
-        return __builtin_bit_cast(uint32_t, __builtin_bit_cast(mv_half2, hi) + __builtin_bit_cast(mv_half2, lo));
-    }
 }
 
 // grid.x = ceil((M / 16) / BANDS) (any grid.x >= 1 is correct: workgroup g takes band
@@ -337,7 +300,7 @@ decode_matvec_mfma(const uint32_t* __restrict__ bits, int M, int N,
                 const uint32_t w0 = (fw >> (32 - L - 4 * p)) & ((1u << L) - 1u);
                 const uint32_t w1 = (fw >> (30 - L - 4 * p)) & ((1u << L) - 1u);
                 if constexpr (TABLE) {
-                    const mv_half2 h = {tab16[w0], tab16[w1]};
+                    const code_half2 h = {tab16[w0], tab16[w1]};
                     a[p] = __builtin_bit_cast(uint32_t, h);
                 } else {
                     a[p] = code_raw_pair_f16<CODE>(w0, w1, kbias, ca);

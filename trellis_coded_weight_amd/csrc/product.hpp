@@ -151,18 +151,30 @@ join_shares(ProductArgs a, int splits)
     finish4<O, MODE, ACT>(a, 0, (int)row, col, a.n - col, s, u);
 }
 
-// Rows of `cols` elements, on any element, to rows of whole 16-byte chunks, zero past cols.
-//   grid.x covers rows * (pitch / E) threads, block = 256; pitch a multiple of E.
+// Up to three matrices of rows of `cols` elements, on any element, to rows of whole 16-byte
+// chunks, zero past cols, in one launch.
+//   grid.x: first[i + 1] - first[i] blocks of matrix i, each 256 chunks; block = 256;
+//   pitch a multiple of E.
+struct PadArgs {
+    const void* src[3];
+    void* dst[3];
+    int64_t ld[3], rows[3];
+    unsigned first[4];
+    int cols, pitch;
+};
+
 template <typename T>
 __global__ void __launch_bounds__(256)
-pad_rows(const T* __restrict__ src, int64_t ld, int64_t rows, int cols, T* __restrict__ dst, int pitch)
+pad_rows(PadArgs a)
 {
     constexpr int E = 16 / (int)sizeof(T);
-    const int per = pitch / E;
-    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x, row = t / per;
-    if (row >= rows) return;
+    const int i = blockIdx.x >= a.first[2] ? 2 : (blockIdx.x >= a.first[1] ? 1 : 0);
+    const int per = a.pitch / E;
+    const int64_t t = (int64_t)(blockIdx.x - a.first[i]) * 256 + threadIdx.x, row = t / per;
+    if (row >= a.rows[i]) return;
     const int at = (int)(t - row * per) * E;
-    *reinterpret_cast<u32x4*>(dst + row * pitch + at) = load_chunk<T>(src + row * ld, at, cols);
+    *reinterpret_cast<u32x4*>(static_cast<T*>(a.dst[i]) + row * a.pitch + at) =
+        load_chunk<T>(static_cast<const T*>(a.src[i]) + row * a.ld[i], at, a.cols);
 }
 
 // dg = dh u act'(g) and du = dh act(g), each formed in binary32 and rounded once to the

@@ -94,15 +94,32 @@ bool whole_chunks(const void* p, int64_t ld, int inner)
     return aligned16(p) && ld % E == 0 && inner % E == 0 && ld * (int64_t)sizeof(T) <= BlockShape::kMaxStride;
 }
 
+// Copies of operands with rows of whole chunks, gathered and then launched together.
 template <typename T>
-void pad_go(const void* src, int64_t ld, int64_t rows, int cols, void* dst, hipStream_t st)
-{
-    const int pitch = chunk_pitch(cols, (int)sizeof(T));
-    const int64_t n = rows * (pitch / (16 / (int)sizeof(T)));
-    if (n == 0) return;
-    hipLaunchKernelGGL(pad_rows<T>, dim3(blocks_for(n, 256)), dim3(256), 0, st, static_cast<const T*>(src), ld, rows,
-                       cols, static_cast<T*>(dst), pitch);
-}
+struct PadCopies {
+    PadArgs a = {};
+    int n = 0;
+    explicit PadCopies(int cols) { a.cols = cols, a.pitch = chunk_pitch(cols, (int)sizeof(T)); }
+    // the copy goes to *at, which moves past it; returns its place
+    const void* add(const void* src, int64_t ld, int64_t rows, char** at)
+    {
+        void* dst = *at;
+        const unsigned blocks = blocks_for(rows * (a.pitch / (16 / (int)sizeof(T))), 256);
+        a.src[n] = src;
+        a.dst[n] = dst;
+        a.ld[n] = ld;
+        a.rows[n] = rows;
+        a.first[n + 1] = a.first[n] + blocks;
+        *at += round256((size_t)rows * a.pitch * sizeof(T));
+        ++n;
+        return dst;
+    }
+    void go(hipStream_t st)
+    {
+        for (int i = n; i < 3; ++i) a.first[i + 1] = a.first[n];
+        if (a.first[n] > 0) hipLaunchKernelGGL(pad_rows<T>, dim3(a.first[n]), dim3(256), 0, st, a);
+    }
+};
 
 // kInt8 and kGated: both operands stored [row][k].
 template <typename T, typename O, int MODE, int ACT = 0>
@@ -113,26 +130,20 @@ qtcq_status rows_product(ProductArgs a, void* ws, size_t wsb, hipStream_t st)
     const bool qw = whole_chunks<T>(a.q[0], a.ldq, a.k) && (QS == 1 || aligned16(a.q[1]));
     const ProductPlan plan = plan_product(MODE, (int)sizeof(T), a.m, a.n, a.k, pw && qw);
     if (plan.skinny) return skinny_go<T, O, MODE, ACT>(a, pw && qw, st);
-    const size_t pb = pw ? 0 : plan.p_bytes, qb = qw ? 0 : plan.q_bytes;
-    const size_t need = plan.part_bytes + pb + qb;
+    const size_t need = plan.part_bytes + (pw ? 0 : plan.p_bytes) + (qw ? 0 : plan.q_bytes);
     if (need > 0 && (!ws || !aligned16(ws) || wsb < need)) return QTCQ_ERR_WORKSPACE;
     char* at = static_cast<char*>(ws) + plan.part_bytes;
+    PadCopies<T> copies(a.k);
     a.pk = a.qk = a.k;
     if (!pw) {
-        pad_go<T>(a.p[0], a.ldp, a.m, a.k, at, st);
-        a.p[0] = at;
-        a.ldp = a.pk = chunk_pitch(a.k, (int)sizeof(T));
-        at += pb;
+        a.p[0] = copies.add(a.p[0], a.ldp, a.m, &at);
+        a.ldp = a.pk = copies.a.pitch;
     }
     if (!qw) {
-        a.qk = chunk_pitch(a.k, (int)sizeof(T));
-        for (int i = 0; i < QS; ++i) {
-            pad_go<T>(a.q[i], a.ldq, a.n, a.k, at, st);
-            a.q[i] = at;
-            at += (size_t)a.n * a.qk * sizeof(T);
-        }
-        a.ldq = a.qk;
+        for (int i = 0; i < QS; ++i) a.q[i] = copies.add(a.q[i], a.ldq, a.n, &at);
+        a.ldq = a.qk = copies.a.pitch;
     }
+    copies.go(st);
     return block_go<T, O, MODE, ACT>(a, plan, ws, st);
 }
 

@@ -52,12 +52,13 @@ __device__ __forceinline__ int quant_tiny(float x, float s)
     return (int)t;
 }
 
+constexpr float kQuantMagic = 12582912.0f;                 // 1.5 * 2^23
+
 // the int8 of x in the low byte of the result (a row that is neither tiny nor zero)
 __device__ __forceinline__ uint32_t quant_bits(float x, const RowScale& o)
 {
-    constexpr float kMagic = 12582912.0f;                  // 1.5 * 2^23
-    const float u = __builtin_fmaf(x, o.r, kMagic);
-    const float q = u - kMagic;
+    const float u = __builtin_fmaf(x, o.r, kQuantMagic);
+    const float q = u - kQuantMagic;
     const float d = __builtin_fmaf(-q, o.s, x);
     uint32_t b = __builtin_bit_cast(uint32_t, u);
     if (__builtin_expect(!(__builtin_fabsf(d) < o.half), 0)) {
@@ -67,6 +68,24 @@ __device__ __forceinline__ uint32_t quant_bits(float x, const RowScale& o)
         if (e < -h || (e == -h && odd)) b -= 1u;
     }
     return b;
+}
+
+// The same of E values at once: one test of the largest residual for all of them.
+template <int E>
+__device__ __forceinline__ void quant_bits(const float (&x)[E], const RowScale& o, uint32_t (&b)[E])
+{
+    float worst = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const float u = __builtin_fmaf(x[e], o.r, kQuantMagic);
+        const float d = __builtin_fmaf(-(u - kQuantMagic), o.s, x[e]);
+        worst = __builtin_fmaxf(worst, __builtin_fabsf(d));
+        b[e] = __builtin_bit_cast(uint32_t, u);
+    }
+    if (__builtin_expect(!(worst < o.half), 0)) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) b[e] = quant_bits(x[e], o);
+    }
 }
 
 __device__ __forceinline__ uint32_t quant_any(float x, const RowScale& o)
@@ -92,6 +111,15 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t m)
         m = v > m ? v : m;
     }
     return m;
+}
+
+// The larger of |x| over both halves of 16-bit pairs, as 16-bit patterns (an infinity or NaN
+// is above every finite value).
+__device__ __forceinline__ uint32_t pair_max(uint32_t m, uint32_t pair)
+{
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, m),
+                                                                  __builtin_bit_cast(u16x2, pair & 0x7FFF7FFFu)));
 }
 
 struct QuantShape {
@@ -132,9 +160,14 @@ quantize_rows(const T* __restrict__ x, int64_t rows, int cols, int64_t ldx, int8
     uint32_t m = 0;
     auto take = [&](const Chunk& o) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const uint32_t a = abs_bits(to_f32(o.v[e]));
-            m = a > m ? a : m;
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t w = __builtin_bit_cast(u32x4, o)[e];
+            if constexpr (sizeof(T) == 2) {
+                m = pair_max(m, w);
+            } else {
+                const uint32_t a = w & 0x7FFFFFFFu;
+                m = a > m ? a : m;
+            }
         }
     };
 #pragma unroll
@@ -146,6 +179,10 @@ quantize_rows(const T* __restrict__ x, int64_t rows, int cols, int64_t ldx, int8
         }
     }
     for (int c = t + NCH * RT; c < nch; c += RT) take(load(c));
+    if constexpr (sizeof(T) == 2) {                    // the larger half, as binary32 bits
+        const uint32_t h = (m & 0xFFFFu) > (m >> 16) ? m & 0xFFFFu : m >> 16;
+        m = abs_bits(to_f32(__builtin_bit_cast(T, (uint16_t)h)));
+    }
     m = wave_max(m);
     if constexpr (RT > 64) {
         if ((tid & 63) == 0) red[tid >> 6] = m;
@@ -159,12 +196,14 @@ quantize_rows(const T* __restrict__ x, int64_t rows, int cols, int64_t ldx, int8
     int8_t* qr = q + row * ldq;
     auto store = [&](int c, const Chunk& o) {
         uint32_t b[E];
+        float v[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = to_f32(o.v[e]);
         if (__builtin_expect(sc.zero || sc.tiny, 0)) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) b[e] = quant_any(to_f32(o.v[e]), sc);
+            for (int e = 0; e < E; ++e) b[e] = quant_any(v[e], sc);
         } else {
-#pragma unroll
-            for (int e = 0; e < E; ++e) b[e] = quant_bits(to_f32(o.v[e]), sc);
+            quant_bits(v, sc, b);
         }
         if (VEC && (c + 1) * E <= n) {
             if constexpr (E == 8) {
@@ -195,28 +234,41 @@ quantize_rows(const T* __restrict__ x, int64_t rows, int cols, int64_t ldx, int8
 // stores of one row are contiguous.  Row r of a tile is stream bits [32 r, 32 r + 30 + L),
 // inside words r and r + 1 (word 16 of a tail-biting stream is word 0).
 //
-// int8 takes two passes over the band, the largest magnitude of each row first; the
-// words of the first 256 tiles stay in registers, others are read again (from L2).  The
-// largest value is found on the codes before their rescale (code_rescale is odd and
-// monotone).
+// int8 first finds the largest magnitude of each row, on the codes before their rescale
+// (exact in fp16; code_rescale is odd and monotone).  HOLD tiles a lane keep those codes in
+// registers for the second pass; tiles beyond HOLD * 256 are decoded again.
+//
+// The int8 of a code is that of its rescaled value c: with D the code's divisor, raw / (D s)
+// is within 2^-15 of c / s (three roundings of at most 127), so its nearest integer is the
+// int8 wherever it lies further than 2^-14 from a half step; the rest goes through c.
+//
+// At 2 bits in and 8 out the memory moves 235 million weights in 57 us; the decode's VALU
+// work, about 10 instructions a weight, is what takes longer.
 struct DecodeRowsShape {
     static constexpr int kThreads = 1024;
     static constexpr int kTiles = 256;       // tiles of a band in flight
 };
 
+template <int CODE>
+constexpr float code_divisor()
+{
+    return CODE == kCode1Mad ? 147.8f : (CODE == kCode3Inst ? 1.244f : 1.0f);
+}
+
 // OUT: 0 int8 + scale, 1 bf16, 2 fp16, 3 binary32.  grid.x = M / 16.
-template <int L, int CODE, bool TB, int OUT>
+template <int L, int CODE, bool TB, int OUT, int HOLD>
 __global__ void __launch_bounds__(DecodeRowsShape::kThreads)
 decode_rows(const uint32_t* __restrict__ bits, int NTJ, void* __restrict__ w, int64_t ldw,
             float* __restrict__ scale, CodeArg ca)
 {
-    constexpr int Wd = TB ? 16 : (L + 2 * 255 + 31) / 32;
+    constexpr int Wd = TB ? 16 : (L + 2 * 255 + 31) / 32, NT = DecodeRowsShape::kTiles;
     __shared__ uint32_t red[16][4];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r0 = 4 * (wave & 3), j0 = 64 * (wave >> 2) + lane;
     const int I = blockIdx.x;
     const uint32_t* band = bits + (int64_t)I * NTJ * Wd;
+    const uint32_t kbias = vgpr_u32(0xE5FEE5FEu);   // fp16 -1534 in both halves
 
     struct Words { uint32_t w[5]; };
     auto load = [&](int j) {
@@ -226,40 +278,52 @@ decode_rows(const uint32_t* __restrict__ bits, int NTJ, void* __restrict__ w, in
         for (int i = 0; i < 5; ++i) o.w[i] = p[TB ? ((r0 + i) & 15) : (r0 + i)];
         return o;
     };
-    // the 16 codes of row r0 + a before their rescale
-    auto raw_row = [&](const Words& o, int a, float* v) {
+    // the 16 codes of row r0 + a before their rescale, as fp16 pairs
+    struct Row { uint32_t h[8]; };
+    auto raw_row = [&](const Words& o, int a) {
         const uint32_t f0 = o.w[a], f1 = __builtin_amdgcn_alignbit(o.w[a], o.w[a + 1], 16);
+        Row v;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-            const uint32_t f = c < 8 ? f0 : f1;
-            v[c] = code_raw<CODE>((f >> (32 - L - 2 * (c & 7))) & ((1u << L) - 1u), ca);
+        for (int g = 0; g < 8; ++g) {
+            const uint32_t f = g < 4 ? f0 : f1;
+            v.h[g] = code_raw_pair_f16<CODE>((f >> (32 - L - 4 * (g & 3))) & ((1u << L) - 1u),
+                                             (f >> (30 - L - 4 * (g & 3))) & ((1u << L) - 1u), kbias, ca);
         }
+        return v;
     };
     const int64_t row0 = 16 * (int64_t)I + r0;
     if constexpr (OUT == 0) {
-        Words held = {};
-        float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        auto take = [&](const Words& o) {
+        Row held[HOLD][4];
+        uint32_t m[4] = {0u, 0u, 0u, 0u};
+        auto take = [&](const Row& v, int a) {
 #pragma unroll
-            for (int a = 0; a < 4; ++a) {
-                float v[16];
-                raw_row(o, a, v);
-#pragma unroll
-                for (int c = 0; c < 16; ++c) m[a] = __builtin_fmaxf(m[a], __builtin_fabsf(v[c]));
-            }
+            for (int g = 0; g < 8; ++g) m[a] = pair_max(m[a], v.h[g]);
         };
-        if (j0 < NTJ) {
-            held = load(j0);
-            take(held);
+#pragma unroll
+        for (int t = 0; t < HOLD; ++t) {
+            if (j0 + t * NT < NTJ) {
+                const Words o = load(j0 + t * NT);
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+                    held[t][a] = raw_row(o, a);
+                    take(held[t][a], a);
+                }
+            }
         }
-        for (int j = j0 + DecodeRowsShape::kTiles; j < NTJ; j += DecodeRowsShape::kTiles) take(load(j));
+        for (int j = j0 + HOLD * NT; j < NTJ; j += NT) {
+            const Words o = load(j);
+#pragma unroll
+            for (int a = 0; a < 4; ++a) take(raw_row(o, a), a);
+        }
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
-            const uint32_t mm = wave_max(__builtin_bit_cast(uint32_t, m[a]));
+            const uint32_t h = (m[a] & 0xFFFFu) > (m[a] >> 16) ? m[a] & 0xFFFFu : m[a] >> 16;
+            const uint32_t mm = wave_max(h);
             if (lane == 0) red[wave][a] = mm;
         }
         __syncthreads();
         RowScale sc[4];
+        float rho[4];
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
             uint32_t mm = 0;
@@ -269,38 +333,54 @@ decode_rows(const uint32_t* __restrict__ bits, int NTJ, void* __restrict__ w, in
                 mm = v > mm ? v : mm;
             }
             // the smallest nonzero code value of any code is far above kQuantTiny
-            sc[a] = row_scale(__builtin_bit_cast(uint32_t, code_rescale<CODE>(__builtin_bit_cast(float, mm))));
+            const float top = (float)__builtin_bit_cast(_Float16, (uint16_t)mm);
+            sc[a] = row_scale(__builtin_bit_cast(uint32_t, code_rescale<CODE>(top)));
+            rho[a] = sc[a].zero ? 0.0f : sc[a].r / code_divisor<CODE>();
             if (wave < 4 && lane == 0) scale[row0 + a] = sc[a].s;
         }
         int8_t* out = static_cast<int8_t*>(w) + row0 * ldw;
-        auto put = [&](int j, const Words& o) {
+        auto put = [&](int j, int a, const Row& row) {
+            uint32_t b[16];
+            float worst = 0.0f;
 #pragma unroll
-            for (int a = 0; a < 4; ++a) {
-                float v[16];
-                raw_row(o, a, v);
-                uint32_t p[4];
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    uint32_t b[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) b[e] = quant_bits(code_rescale<CODE>(v[4 * g + e]), sc[a]);
-                    p[g] = sc[a].zero ? 0u : pack4(b[0], b[1], b[2], b[3]);
-                }
-                const u32x4 pv = {p[0], p[1], p[2], p[3]};
-                *reinterpret_cast<u32x4*>(out + a * ldw + 16 * (int64_t)j) = pv;
+            for (int e = 0; e < 16; ++e) {
+                const float x = (float)__builtin_bit_cast(code_half2, row.h[e >> 1])[e & 1];
+                const float u = __builtin_fmaf(x, rho[a], kQuantMagic);
+                const float d = __builtin_fmaf(x, rho[a], -(u - kQuantMagic));
+                worst = __builtin_fmaxf(worst, __builtin_fabsf(d));
+                b[e] = __builtin_bit_cast(uint32_t, u);
             }
+            if (__builtin_expect(worst > 0.5f - 0x1p-14f, 0)) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    b[e] = quant_bits(code_rescale<CODE>((float)__builtin_bit_cast(code_half2, row.h[e >> 1])[e & 1]), sc[a]);
+            }
+            const u32x4 p = {pack4(b[0], b[1], b[2], b[3]), pack4(b[4], b[5], b[6], b[7]),
+                             pack4(b[8], b[9], b[10], b[11]), pack4(b[12], b[13], b[14], b[15])};
+            *reinterpret_cast<u32x4*>(out + a * ldw + 16 * (int64_t)j) = p;
         };
-        if (j0 < NTJ) put(j0, held);
-        for (int j = j0 + DecodeRowsShape::kTiles; j < NTJ; j += DecodeRowsShape::kTiles) put(j, load(j));
+#pragma unroll
+        for (int t = 0; t < HOLD; ++t) {
+            if (j0 + t * NT < NTJ) {
+#pragma unroll
+                for (int a = 0; a < 4; ++a) put(j0 + t * NT, a, held[t][a]);
+            }
+        }
+        for (int j = j0 + HOLD * NT; j < NTJ; j += NT) {
+            const Words o = load(j);
+#pragma unroll
+            for (int a = 0; a < 4; ++a) put(j, a, raw_row(o, a));
+        }
     } else {
-        for (int j = j0; j < NTJ; j += DecodeRowsShape::kTiles) {
+        for (int j = j0; j < NTJ; j += NT) {
             const Words o = load(j);
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
+                const Row row = raw_row(o, a);
                 float v[16];
-                raw_row(o, a, v);
 #pragma unroll
-                for (int c = 0; c < 16; ++c) v[c] = code_rescale<CODE>(v[c]);
+                for (int e = 0; e < 16; ++e)
+                    v[e] = code_rescale<CODE>((float)__builtin_bit_cast(code_half2, row.h[e >> 1])[e & 1]);
                 const int64_t at = (row0 + a) * ldw + 16 * (int64_t)j;
                 if constexpr (OUT == 3) {
 #pragma unroll
@@ -314,12 +394,12 @@ decode_rows(const uint32_t* __restrict__ bits, int NTJ, void* __restrict__ w, in
                         if constexpr (OUT == 1) {
                             bf16x8 p;
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) p[e] = (__bf16)v[8 * g + e];
+                            for (int e = 0; e < 8; ++e) p[e] = from_f32<__bf16>(v[8 * g + e]);
                             reinterpret_cast<bf16x8*>(static_cast<__bf16*>(w) + at)[g] = p;
                         } else {
                             f16x8 p;
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) p[e] = (_Float16)v[8 * g + e];
+                            for (int e = 0; e < 8; ++e) p[e] = from_f32<_Float16>(v[8 * g + e]);
                             reinterpret_cast<f16x8*>(static_cast<_Float16*>(w) + at)[g] = p;
                         }
                     }
