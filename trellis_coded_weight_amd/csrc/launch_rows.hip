@@ -42,10 +42,10 @@ template <int L, int CODE, bool TB>
 qtcq_status decode_rows_impl(const uint32_t* bits, int M, int N, int dtype, void* w, int64_t ldw, float* scale,
                              const CodeArg& ca, hipStream_t st)
 {
-    const dim3 grid((unsigned)(M / 16)), block(DecodeRowsShape::kThreads);
+    const dim3 grid((unsigned)(M / 4)), block(DecodeRowsShape::kThreads);
     auto go = [&](auto out, auto hold) {
         hipLaunchKernelGGL((decode_rows<L, CODE, TB, decltype(out)::value, decltype(hold)::value>), grid, block, 0, st,
-                           bits, N / 16, w, ldw, scale, ca);
+                           bits, M / 16, N / 16, w, ldw, scale, ca);
         return launch_status();
     };
     switch (dtype) {

@@ -228,11 +228,13 @@ quantize_rows(const T* __restrict__ x, int64_t rows, int cols, int64_t ldx, int8
 
 // ---- streams to rows ----------------------------------------------------------------------
 // W [M][N] from its tile streams (tile (I, J) is sequence I (N/16) + J, weight 16 r + c of
-// a tile is row 16 I + r, column 16 J + c).  One workgroup of 16 waves per band of 16 rows:
-// wave w decodes rows 4 (w & 3) .. + 3 of tiles 64 (w >> 2) + lane, + 256, ...: a lane reads
-// the five stream words of its four rows and writes whole tile rows, so that a wave's
-// stores of one row are contiguous.  Row r of a tile is stream bits [32 r, 32 r + 30 + L),
-// inside words r and r + 1 (word 16 of a tail-biting stream is word 0).
+// a tile is row 16 I + r, column 16 J + c).  One workgroup of 4 waves per quarter of a band
+// of 16 rows: wave w decodes the four rows of tiles 64 w + lane, + 256, ...: a lane reads the
+// five stream words of its rows and writes whole tile rows, so that a wave's stores of one
+// row are contiguous.  Row r of a tile is stream bits [32 r, 32 r + 30 + L), inside words r
+// and r + 1 (word 16 of a tail-biting stream is word 0).  The quarters of a band share its
+// streams' lines, so they run on one XCD: workgroups go round the 8 XCDs, and workgroup b of
+// each 32 takes quarter b / 8 of band b % 8.
 //
 // int8 first finds the largest magnitude of each row, on the codes before their rescale
 // (exact in fp16; code_rescale is odd and monotone).  HOLD tiles a lane keep those codes in
@@ -245,7 +247,7 @@ quantize_rows(const T* __restrict__ x, int64_t rows, int cols, int64_t ldx, int8
 // At 2 bits in and 8 out the memory moves 235 million weights in 57 us; the decode's VALU
 // work, about 10 instructions a weight, is what takes longer.
 struct DecodeRowsShape {
-    static constexpr int kThreads = 1024;
+    static constexpr int kThreads = 256;
     static constexpr int kTiles = 256;       // tiles of a band in flight
 };
 
@@ -255,18 +257,20 @@ constexpr float code_divisor()
     return CODE == kCode1Mad ? 147.8f : (CODE == kCode3Inst ? 1.244f : 1.0f);
 }
 
-// OUT: 0 int8 + scale, 1 bf16, 2 fp16, 3 binary32.  grid.x = M / 16.
+// OUT: 0 int8 + scale, 1 bf16, 2 fp16, 3 binary32.  grid.x = 4 bands.
 template <int L, int CODE, bool TB, int OUT, int HOLD>
 __global__ void __launch_bounds__(DecodeRowsShape::kThreads)
-decode_rows(const uint32_t* __restrict__ bits, int NTJ, void* __restrict__ w, int64_t ldw,
+decode_rows(const uint32_t* __restrict__ bits, int bands, int NTJ, void* __restrict__ w, int64_t ldw,
             float* __restrict__ scale, CodeArg ca)
 {
     constexpr int Wd = TB ? 16 : (L + 2 * 255 + 31) / 32, NT = DecodeRowsShape::kTiles;
-    __shared__ uint32_t red[16][4];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r0 = 4 * (wave & 3), j0 = 64 * (wave >> 2) + lane;
-    const int I = blockIdx.x;
+    __shared__ uint32_t red[4][4];
+    const int lane = threadIdx.x & 63, j0 = threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // whole groups of 8 bands by quarters, the bands after them in order
+    const int b = blockIdx.x, grouped = bands >> 3 << 3;
+    const int I = b < 4 * grouped ? (b >> 5) * 8 + (b & 7) : b >> 2;
+    const int r0 = 4 * (b < 4 * grouped ? (b >> 3) & 3 : b & 3);
     const uint32_t* band = bits + (int64_t)I * NTJ * Wd;
     const uint32_t kbias = vgpr_u32(0xE5FEE5FEu);   // fp16 -1534 in both halves
 
@@ -329,14 +333,14 @@ decode_rows(const uint32_t* __restrict__ bits, int NTJ, void* __restrict__ w, in
             uint32_t mm = 0;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const uint32_t v = red[4 * g + (wave & 3)][a];
+                const uint32_t v = red[g][a];
                 mm = v > mm ? v : mm;
             }
             // the smallest nonzero code value of any code is far above kQuantTiny
             const float top = (float)__builtin_bit_cast(_Float16, (uint16_t)mm);
             sc[a] = row_scale(__builtin_bit_cast(uint32_t, code_rescale<CODE>(top)));
             rho[a] = sc[a].zero ? 0.0f : sc[a].r / code_divisor<CODE>();
-            if (wave < 4 && lane == 0) scale[row0 + a] = sc[a].s;
+            if (threadIdx.x == 0) scale[row0 + a] = sc[a].s;
         }
         int8_t* out = static_cast<int8_t*>(w) + row0 * ldw;
         auto put = [&](int j, int a, const Row& row) {
