@@ -264,25 +264,79 @@ block_product(ProductArgs a)
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
 
+    // a lane's results: rows row0 + 16 i, four columns from col0 + 16 j
+    typedef typename MM::Acc Acc;
     constexpr int NJ = MODE == kGated ? 2 : 4;
+    const int row0 = i0 + wm * FP * 16 + (lane & 15);
+    const int col0 = j0 + (MODE == kGated ? wn * 32 : wn * 64) + 4 * (lane >> 4);
+    if (MODE != kGradW && a.part) {
 #pragma unroll
-    for (int i = 0; i < FP; ++i) {
-        const int row = i0 + (wm * FP + i) * 16 + (lane & 15);
-        if (row >= a.m) continue;
+        for (int i = 0; i < FP; ++i) {
+            const int row = row0 + i * 16;
+            if (row >= a.m) continue;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const int col = j0 + (MODE == kGated ? wn * 32 : wn * 64) + j * 16 + 4 * (lane >> 4);
-            const int left = a.n - col;
-            if (left <= 0) continue;
-            if (MODE != kGradW && a.part) {
-                typedef typename MM::Acc Acc;
+            for (int j = 0; j < NJ; ++j) {
+                const int col = col0 + j * 16;
+                if (col >= a.n) continue;
                 Acc* p = static_cast<Acc*>(a.part) + ((((int64_t)blockIdx.y * a.m + row) * a.part_pitch + col) >> 2);
                 p[0] = acc[i][j];
                 if constexpr (MODE == kGated) p[a.part_pitch >> 3] = acc[i][j + 2];
-            } else {
-                finish4<O, MODE, ACT>(a, z, row, col, left, acc[i][j], acc[i][MODE == kGated ? j + 2 : j]);
             }
         }
+    } else if (sizeof(O) == 2 && i0 + BlockShape::rows(FP) <= a.m && j0 + COLS <= a.n) {
+        // A whole tile of 16-bit results goes out through LDS, in whole rows of the tile
+        // (a wave's own results are 32-byte pieces of 16 rows).  Rows are 16 bytes apart in
+        // banks.
+        constexpr int RB = COLS * 2, PITCH = RB + 16, LR = RB / 16, RW = 64 / LR;   // lanes a row, rows a wave
+        static_assert(BlockShape::rows(FP) * PITCH <= (int)sizeof(lds), "the tile fits LDS");
+        float qs[NJ][4] = {};
+        if constexpr (MODE == kInt8) {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) qs[j][e] = a.q_scale[col0 + j * 16 + e];
+        }
+        struct __attribute__((aligned(8))) Four { O e[4]; };
+        struct __attribute__((packed, aligned(2))) Loose { u32x4 v; };
+        auto put = [&](void* base, int64_t ld, auto value) {
+            landed(std::integral_constant<int, 0>{});     // LDS is no longer read or loaded
+#pragma unroll
+            for (int i = 0; i < FP; ++i) {
+                const float ps = MODE == kInt8 ? a.p_scale[row0 + i * 16] : 0.0f;
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    Four f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f.e[e] = from_f32<O>(value(i, j, e, ps));
+                    *reinterpret_cast<Four*>(lds + (row0 - i0 + i * 16) * PITCH + (col0 - j0 + j * 16) * 2) = f;
+                }
+            }
+            __syncthreads();
+            const int r = RW * wave + lane / LR, c = lane % LR;
+            O* o = static_cast<O*>(base) + (int64_t)(i0 + r) * ld + j0 + c * 8;
+#pragma unroll
+            for (int h = 0; h < BlockShape::rows(FP) / (8 * RW); ++h) {
+                reinterpret_cast<Loose*>(o)->v = *reinterpret_cast<const u32x4*>(lds + (r + h * 8 * RW) * PITCH + c * 16);
+                o += 8 * RW * ld;
+            }
+        };
+        put(a.out[z], a.ldo, [&](int i, int j, int e, float ps) {
+            if constexpr (MODE == kGated) return activate<ACT>(acc[i][j][e]) * acc[i][j + 2][e];
+            if constexpr (MODE == kInt8) return (float)acc[i][j][e] * ps * qs[j][e];
+            return (float)acc[i][j][e];
+        });
+        if constexpr (MODE == kGated)
+            if (a.save[0]) {
+                put(a.save[0], a.lds, [&](int i, int j, int e, float) { return acc[i][j][e]; });
+                put(a.save[1], a.lds, [&](int i, int j, int e, float) { return acc[i][j + 2][e]; });
+            }
+    } else {
+#pragma unroll
+        for (int i = 0; i < FP; ++i)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                if (row0 + i * 16 < a.m && col0 + j * 16 < a.n)
+                    finish_at<O, MODE, ACT>(a, z, row0 + i * 16, col0 + j * 16, acc[i][j], acc[i][MODE == kGated ? j + 2 : j]);
     }
 }
 

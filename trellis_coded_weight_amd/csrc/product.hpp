@@ -104,11 +104,12 @@ __device__ __forceinline__ void store4(O* p, const float (&v)[4], int n)
         if (e < n) p[e] = from_f32<O>(v[e]);
 }
 
-// Four consecutive results of row `row` from column `col`, `left` of them inside the matrix:
-// s their sums (kGated: the gate's, and u the up's).
+// Four consecutive results of row `row` from column `col` (those inside the matrix), from
+// their sums s (kGated: the gate's, and u the up's).
 template <typename O, int MODE, int ACT, typename Acc>
-__device__ __forceinline__ void finish4(const ProductArgs& a, int z, int row, int col, int left, const Acc& s, const Acc& u)
+__device__ __forceinline__ void finish_at(const ProductArgs& a, int z, int row, int col, const Acc& s, const Acc& u)
 {
+    const int left = a.n - col;
     float v[4];
     if constexpr (MODE == kGated) {
         const float gv[4] = {s[0], s[1], s[2], s[3]}, uv[4] = {u[0], u[1], u[2], u[3]};
@@ -148,7 +149,7 @@ join_shares(ProductArgs a, int splits)
         s += p[i * next];
         if constexpr (MODE == kGated) u += p[i * next + (width >> 2)];
     }
-    finish4<O, MODE, ACT>(a, 0, (int)row, col, a.n - col, s, u);
+    finish_at<O, MODE, ACT>(a, 0, (int)row, col, s, u);
 }
 
 // Up to three matrices of rows of `cols` elements, on any element, to rows of whole 16-byte

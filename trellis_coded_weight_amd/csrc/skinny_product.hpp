@@ -135,8 +135,8 @@ skinny_product(ProductArgs a)
                 s += red[w][f][lane];
                 if constexpr (MODE == kGated) u += red[w][f + NJ][lane];
             }
-            const int row = i0 + i * 16 + r, col = j0 + j * 16 + 4 * c, left = a.n - col;
-            if (row < a.m && left > 0) finish4<O, MODE, ACT>(a, 0, row, col, left, s, u);
+            const int row = i0 + i * 16 + r, col = j0 + j * 16 + 4 * c;
+            if (row < a.m && col < a.n) finish_at<O, MODE, ACT>(a, 0, row, col, s, u);
         }
     }
 }
