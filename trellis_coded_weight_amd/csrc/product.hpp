@@ -69,26 +69,6 @@ template <> struct Mfma<int8_t> {
     }
 };
 
-// 16 bytes at p, which need only be aligned to their element
-template <typename T>
-__device__ __forceinline__ u32x4 load_loose(const T* p)
-{
-    struct __attribute__((packed, aligned(sizeof(T)))) Loose { u32x4 v; };
-    return reinterpret_cast<const Loose*>(p)->v;
-}
-
-// 16 bytes at p + at of a row with n elements, zero past its end
-template <typename T>
-__device__ __forceinline__ u32x4 load_chunk(const T* p, int at, int n)
-{
-    constexpr int E = 16 / (int)sizeof(T);
-    if (at + E <= n) return load_loose(p + at);
-    struct Parts { T e[E]; } o;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o.e[e] = at + e < n ? p[at + e] : (T)0;
-    return __builtin_bit_cast(u32x4, o);
-}
-
 // four consecutive outputs of a row, of which n are inside the matrix (stores need no
 // alignment beyond the element's here)
 template <typename O>

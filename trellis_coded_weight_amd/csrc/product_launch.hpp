@@ -41,9 +41,11 @@ template <typename T, typename O, int MODE, int ACT>
 qtcq_status skinny_go(const ProductArgs& a, bool whole, hipStream_t st)
 {
     constexpr int WIDE = MODE == kGated ? 1 : 2;
-    // two groups of columns a workgroup, which halves the reads of P, where that leaves two
-    // workgroups a compute unit
-    const bool wide = a.n >= 16 * WIDE * 512;
+    // Two groups of columns a workgroup halve the reads of P; worth it once P has rows to
+    // read, where that leaves two workgroups a compute unit (us, one group against two:
+    // 8-bit 28672x8192 at m = 4 46.5 / 55.9, 16384x4096 at m = 16 19.6 / 16.7, m = 32 28.1 /
+    // 21.4).
+    const bool wide = a.m > 8 && a.n >= 16 * WIDE * 512;
     return with_bool(whole, [&](auto al) {
         constexpr bool ALIGNED = decltype(al)::value;
         auto go = [&](auto mi) {

@@ -128,10 +128,11 @@ struct QuantShape {
 
 // One row per RT threads (64: a wave a row; 256: a workgroup a row).  E elements of T in
 // 16 bytes; a thread holds NCH such chunks of its row in registers between the two
-// passes, and rows longer than RT * NCH chunks are read a second time.  VEC: rows start
-// on 16 bytes, whole chunks are loaded and stored at once; otherwise element by element.
+// passes, and rows longer than RT * NCH chunks are read a second time.  Rows may start on
+// any element (neither loads nor stores need more alignment); a row's last chunk, if it is
+// not whole, goes element by element.
 //   grid.x = ceil(rows / (256 / RT)), block = 256
-template <typename T, int RT, int NCH, bool VEC>
+template <typename T, int RT, int NCH>
 __global__ void __launch_bounds__(QuantShape::kThreads)
 quantize_rows(const T* __restrict__ x, int64_t rows, int cols, int64_t ldx, int8_t* __restrict__ q, int64_t ldq,
               float* __restrict__ scale)
@@ -146,16 +147,7 @@ quantize_rows(const T* __restrict__ x, int64_t rows, int cols, int64_t ldx, int8
     const int nch = (n + E - 1) / E;
 
     struct Chunk { T v[E]; };
-    auto load = [&](int c) {
-        Chunk o;
-        if (VEC && (c + 1) * E <= n) {
-            o = __builtin_bit_cast(Chunk, *reinterpret_cast<const u32x4*>(xr + (int64_t)c * E));
-        } else {
-#pragma unroll
-            for (int e = 0; e < E; ++e) o.v[e] = c * E + e < n ? xr[c * E + e] : (T)0.0f;
-        }
-        return o;
-    };
+    auto load = [&](int c) { return __builtin_bit_cast(Chunk, load_chunk<T>(xr, c * E, n)); };
     Chunk held[NCH];
     uint32_t m = 0;
     auto take = [&](const Chunk& o) {
@@ -205,17 +197,16 @@ quantize_rows(const T* __restrict__ x, int64_t rows, int cols, int64_t ldx, int8
         } else {
             quant_bits(v, sc, b);
         }
-        if (VEC && (c + 1) * E <= n) {
-            if constexpr (E == 8) {
-                const u32x2 p = {pack4(b[0], b[1], b[2], b[3]), pack4(b[4], b[5], b[6], b[7])};
-                *reinterpret_cast<u32x2*>(qr + (int64_t)c * E) = p;
-            } else {
-                *reinterpret_cast<uint32_t*>(qr + (int64_t)c * E) = pack4(b[0], b[1], b[2], b[3]);
-            }
+        int8_t* p = qr + (int64_t)c * E;
+        if ((c + 1) * E <= n) {
+            struct __attribute__((packed)) Loose { uint32_t w[E / 4]; } l;
+#pragma unroll
+            for (int g = 0; g < E / 4; ++g) l.w[g] = pack4(b[4 * g], b[4 * g + 1], b[4 * g + 2], b[4 * g + 3]);
+            *reinterpret_cast<Loose*>(p) = l;
         } else {
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                if (c * E + e < n) qr[c * E + e] = (int8_t)b[e];
+                if (c * E + e < n) p[e] = (int8_t)b[e];
         }
     };
 #pragma unroll
