@@ -23,7 +23,7 @@
 // the count of loads in flight the same.
 //
 // Where the tiles of out are fewer than the compute units, k is cut into shares of
-// split_steps steps (grid.y); each writes its sums in 32 bits, and join_shares adds them in
+// split_steps steps; each writes its sums in 32 bits, and join_shares adds them in
 // order.
 //
 // LDS holds an operand in one of two layouts, both written by the loads in whole kilobytes
@@ -66,13 +66,18 @@ struct BlockShape {
 typedef __attribute__((address_space(3))) char lds_char;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// The tile of workgroup `b` of `n`: consecutive workgroups go round the 8 XCDs, so XCD x
-// takes a contiguous run of tiles; runs go down groups of 8 tile rows, column by column,
-// so that an XCD's concurrent tiles share operands in its L2.
-__device__ __forceinline__ void block_tile(int b, int tiles_m, int tiles_n, int& ti, int& tj)
+// The share of k and the tile of workgroup `b` of shares * tiles.  Consecutive workgroups go
+// round the 8 XCDs, so XCD x takes a contiguous run of them: whole shares where there are
+// several, whose tiles read the same rows of P (8-bit 77x8192x28672 46.3 us, with each
+// share's tiles dealt round the XCDs 48.5), and within a share runs that go down groups of
+// 8 tile rows, column by column, so that an XCD's concurrent tiles share operands in its L2
+// (groups of 2, 4 and 8 are alike on the large products).
+__device__ __forceinline__ void block_tile(int b, int shares, int tiles_m, int tiles_n, int& share, int& ti, int& tj)
 {
-    const int n = tiles_m * tiles_n, x = b & 7, q = n >> 3, r = n & 7;
-    const int t = x * q + (x < r ? x : r) + (b >> 3);
+    const int tiles = tiles_m * tiles_n, n = shares * tiles, x = b & 7, q = n >> 3, r = n & 7;
+    int t = x * q + (x < r ? x : r) + (b >> 3);
+    share = t / tiles;
+    t -= share * tiles;
     constexpr int G = 8;
     const int per = G * tiles_n, g = t / per, first = g * G;
     const int rows = tiles_m - first < G ? tiles_m - first : G;
@@ -81,7 +86,7 @@ __device__ __forceinline__ void block_tile(int b, int tiles_m, int tiles_n, int&
     tj = in / rows;
 }
 
-// grid.x = tiles, grid.y = shares of k, grid.z = 2 for kGradW; block = 512.  FP = 8 for
+// grid.x = shares * tiles, grid.z = 2 for kGradW; block = 512.  FP = 8 for
 // kGradW, whose P is stored [k][row].
 template <typename T, typename O, int MODE, int ACT, int FP>
 __global__ void __launch_bounds__(BlockShape::kThreads)
@@ -101,14 +106,15 @@ block_product(ProductArgs a)
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
-    int ti, tj;
-    block_tile(blockIdx.x, (a.m + BlockShape::rows(FP) - 1) / BlockShape::rows(FP), (a.n + COLS - 1) / COLS, ti, tj);
+    int share, ti, tj;
+    block_tile(blockIdx.x, a.shares, (a.m + BlockShape::rows(FP) - 1) / BlockShape::rows(FP), (a.n + COLS - 1) / COLS,
+               share, ti, tj);
     const int i0 = ti * BlockShape::rows(FP), j0 = tj * COLS;
     const int z = MODE == kGradW ? blockIdx.z : 0;
     const int steps1 = (a.k + KS - 1) / KS;
     const int steps = MODE == kGradX ? 2 * steps1 : steps1;
     // this workgroup's share of the steps
-    const int s0 = blockIdx.y * a.split_steps, s1 = s0 + a.split_steps < steps ? s0 + a.split_steps : steps;
+    const int s0 = share * a.split_steps, s1 = s0 + a.split_steps < steps ? s0 + a.split_steps : steps;
     const int64_t ldp = a.ldp * SZ, ldq = a.ldq * SZ;     // in bytes
 
     // where a lane's chunks come from: row-of-k tiles, row 64 h + 8 wave + lane / 8;
@@ -278,7 +284,7 @@ block_product(ProductArgs a)
             for (int j = 0; j < NJ; ++j) {
                 const int col = col0 + j * 16;
                 if (col >= a.n) continue;
-                Acc* p = static_cast<Acc*>(a.part) + ((((int64_t)blockIdx.y * a.m + row) * a.part_pitch + col) >> 2);
+                Acc* p = static_cast<Acc*>(a.part) + ((((int64_t)share * a.m + row) * a.part_pitch + col) >> 2);
                 p[0] = acc[i][j];
                 if constexpr (MODE == kGated) p[a.part_pitch >> 3] = acc[i][j + 2];
             }

@@ -8,7 +8,7 @@ namespace {
 template <typename T>
 qtcq_status slopes(const GatedVjpCall& c, int ldd, T* dg, T* du, hipStream_t st)
 {
-    const dim3 grid(blocks_for((int64_t)c.M * (ldd / 8), 256)), block(256);
+    const dim3 grid((unsigned)RowGrid{ldd / 8}.blocks(c.M)), block(256);
     return with_act(c.act, [&](auto act) {
         hipLaunchKernelGGL((gated_slopes<T, decltype(act)::value>), grid, block, 0, st,
                            static_cast<const T*>(c.gate), static_cast<const T*>(c.up), c.ldg,

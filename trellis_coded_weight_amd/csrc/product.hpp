@@ -40,7 +40,7 @@ struct ProductArgs {
     int64_t lds;
     void* part;              // sums of a share of k [splits][m][part_pitch], or NULL
     int part_pitch;
-    int split_steps;         // steps of k of a share
+    int shares, split_steps; // shares of k, and the steps of each
 };
 
 template <typename T> struct Mfma;
@@ -110,22 +110,47 @@ __device__ __forceinline__ void finish_at(const ProductArgs& a, int z, int row, 
     store4(static_cast<O*>(a.out[z]) + (int64_t)row * a.ldo + col, v, left);
 }
 
+// Threads over the rows of a matrix, `per` pieces a row, in blocks of 256: whole rows in a
+// block, or a row over several blocks (an index division a block, not a 64-bit one a
+// thread).
+struct RowGrid {
+    int per;
+    __host__ __device__ int wide() const { return (per + 255) / 256; }        // blocks a row
+    __host__ __device__ int rows() const { return per < 256 ? 256 / per : 1; }  // rows a block
+    int64_t blocks(int64_t n) const { return per > 0 ? (n + rows() - 1) / rows() * wide() : 0; }
+    // this thread's row and piece in block b; false for a thread without one
+    __device__ __forceinline__ bool at(unsigned b, int64_t& row, int& piece) const
+    {
+        if (per < 256) {
+            const int r = threadIdx.x / per;
+            row = (int64_t)b * rows() + r;
+            piece = threadIdx.x - r * per;
+            return r < rows();
+        }
+        const unsigned w = wide(), r = b / w;
+        row = r;
+        piece = (int)(b - r * w) * 256 + threadIdx.x;
+        return piece < per;
+    }
+};
+
 // The shares of k added in order, then the epilogue.  part [splits][m][part_pitch], four
 // columns a thread (kGated: the gate's sums, then the up's, part_pitch / 2 apart).
-//   grid.x covers m * (columns / 4) threads, block = 256.
+//   grid.x = RowGrid{columns / 4}.blocks(m), block = 256.
 template <typename T, typename O, int MODE, int ACT>
 __global__ void __launch_bounds__(256)
-join_shares(ProductArgs a, int splits)
+join_shares(ProductArgs a)
 {
     typedef typename Mfma<T>::Acc Acc;
-    const int width = MODE == kGated ? a.part_pitch / 2 : a.part_pitch, per = width >> 2;
-    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x, row = t / per;
-    if (row >= a.m) return;
-    const int col = (int)(t - row * per) * 4;
+    const int width = MODE == kGated ? a.part_pitch / 2 : a.part_pitch;
+    int64_t row;
+    int col;
+    if (!RowGrid{width >> 2}.at(blockIdx.x, row, col) || row >= a.m) return;
+    col *= 4;
     const int64_t next = (int64_t)a.m * a.part_pitch >> 2, at = (row * a.part_pitch + col) >> 2;
     const Acc* p = static_cast<const Acc*>(a.part) + at;
     Acc s = {}, u = {};
-    for (int i = 0; i < splits; ++i) {
+    for (int i = 0; i < a.shares; ++i) {
         s += p[i * next];
         if constexpr (MODE == kGated) u += p[i * next + (width >> 2)];
     }
@@ -134,13 +159,12 @@ join_shares(ProductArgs a, int splits)
 
 // Up to three matrices of rows of `cols` elements, on any element, to rows of whole 16-byte
 // chunks, zero past cols, in one launch.
-//   grid.x: first[i + 1] - first[i] blocks of matrix i, each 256 chunks; block = 256;
-//   pitch a multiple of E.
+//   matrix i: blocks first[i] .. first[i + 1] - 1 (RowGrid over its chunks), which any
+//   grid.x takes in turn; block = 256; pitch a multiple of E.
 struct PadArgs {
     const void* src[3];
     void* dst[3];
-    int64_t ld[3], rows[3];
-    unsigned first[4];
+    int64_t ld[3], rows[3], first[4];
     int cols, pitch;
 };
 
@@ -149,13 +173,15 @@ __global__ void __launch_bounds__(256)
 pad_rows(PadArgs a)
 {
     constexpr int E = 16 / (int)sizeof(T);
-    const int i = blockIdx.x >= a.first[2] ? 2 : (blockIdx.x >= a.first[1] ? 1 : 0);
-    const int per = a.pitch / E;
-    const int64_t t = (int64_t)(blockIdx.x - a.first[i]) * 256 + threadIdx.x, row = t / per;
-    if (row >= a.rows[i]) return;
-    const int at = (int)(t - row * per) * E;
-    *reinterpret_cast<u32x4*>(static_cast<T*>(a.dst[i]) + row * a.pitch + at) =
-        load_chunk<T>(static_cast<const T*>(a.src[i]) + row * a.ld[i], at, a.cols);
+    const RowGrid g{a.pitch / E};
+    for (int64_t b = blockIdx.x; b < a.first[3]; b += gridDim.x) {
+        const int i = b >= a.first[2] ? 2 : (b >= a.first[1] ? 1 : 0);
+        int64_t row;
+        int at;
+        if (!g.at((unsigned)(b - a.first[i]), row, at) || row >= a.rows[i]) continue;
+        *reinterpret_cast<u32x4*>(static_cast<T*>(a.dst[i]) + row * a.pitch + at * E) =
+            load_chunk<T>(static_cast<const T*>(a.src[i]) + row * a.ld[i], at * E, a.cols);
+    }
 }
 
 // dg = dh u act'(g) and du = dh act(g), each formed in binary32 and rounded once to the
@@ -163,18 +189,17 @@ pad_rows(PadArgs a)
 // rounding's relative 2^-9 (bf16) or 2^-12 (fp16) a term adds in squares over a sum, about
 // what the rounding of the gradient itself costs.  d [2][M][ldd]: columns from F to ldd
 // are written as zero.
-//   grid.x covers M * ldd / 8 chunks of 8 columns, block = 256; ldd a multiple of 8.
+//   grid.x = RowGrid{ldd / 8}.blocks(M), block = 256; ldd a multiple of 8.
 template <typename T, int ACT>
 __global__ void __launch_bounds__(256)
 gated_slopes(const T* __restrict__ gate, const T* __restrict__ up, int64_t ldg, const T* __restrict__ gh, int64_t ldh,
              int64_t M, int F, int ldd, T* __restrict__ dgate, T* __restrict__ dup)
 {
     typedef T T8 __attribute__((ext_vector_type(8)));
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int per = ldd >> 3;
-    const int64_t row = c / per;
-    if (row >= M) return;
-    const int col = (int)(c - row * per) * 8;
+    int64_t row;
+    int col;
+    if (!RowGrid{ldd >> 3}.at(blockIdx.x, row, col) || row >= M) return;
+    col *= 8;
     const T8 g = __builtin_bit_cast(T8, load_chunk<T>(gate + row * ldg, col, F));
     const T8 u = __builtin_bit_cast(T8, load_chunk<T>(up + row * ldg, col, F));
     const T8 h = __builtin_bit_cast(T8, load_chunk<T>(gh + row * ldh, col, F));

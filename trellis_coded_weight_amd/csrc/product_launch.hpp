@@ -63,12 +63,12 @@ template <typename T, typename O, int MODE, int ACT, int FP>
 qtcq_status block_shape(ProductArgs a, const ProductPlan& p, hipStream_t st)
 {
     const int64_t n = (int64_t)blocks_for(a.m, BlockShape::rows(FP)) * blocks_for(a.n, BlockShape::cols(MODE));
-    const dim3 grid((unsigned)n, (unsigned)p.shares, MODE == kGradW ? 2 : 1);
+    const dim3 grid((unsigned)(n * p.shares), 1, MODE == kGradW ? 2 : 1);
     hipLaunchKernelGGL((block_product<T, O, MODE, ACT, FP>), grid, dim3(BlockShape::kThreads), 0, st, a);
     if constexpr (MODE != kGradW)
         if (p.shares > 1) {
-            const int64_t quads = (int64_t)a.m * (MODE == kGated ? p.part_pitch / 8 : p.part_pitch / 4);
-            hipLaunchKernelGGL((join_shares<T, O, MODE, ACT>), dim3(blocks_for(quads, 256)), dim3(256), 0, st, a, p.shares);
+            const RowGrid g{MODE == kGated ? p.part_pitch / 8 : p.part_pitch / 4};
+            hipLaunchKernelGGL((join_shares<T, O, MODE, ACT>), dim3((unsigned)g.blocks(a.m)), dim3(256), 0, st, a);
         }
     return launch_status();
 }
@@ -79,6 +79,7 @@ qtcq_status block_go(ProductArgs a, const ProductPlan& p, void* part, hipStream_
 {
     a.part = p.shares > 1 ? part : nullptr;
     a.part_pitch = p.part_pitch;
+    a.shares = p.shares;
     a.split_steps = p.share_steps;
     if constexpr (MODE != kGradW) {
         if (p.fp == 2) return block_shape<T, O, MODE, ACT, 2>(a, p, st);
@@ -106,12 +107,11 @@ struct PadCopies {
     const void* add(const void* src, int64_t ld, int64_t rows, char** at)
     {
         void* dst = *at;
-        const unsigned blocks = blocks_for(rows * (a.pitch / (16 / (int)sizeof(T))), 256);
         a.src[n] = src;
         a.dst[n] = dst;
         a.ld[n] = ld;
         a.rows[n] = rows;
-        a.first[n + 1] = a.first[n] + blocks;
+        a.first[n + 1] = a.first[n] + RowGrid{a.pitch / (16 / (int)sizeof(T))}.blocks(rows);
         *at += round256((size_t)rows * a.pitch * sizeof(T));
         ++n;
         return dst;
@@ -119,7 +119,9 @@ struct PadCopies {
     void go(hipStream_t st)
     {
         for (int i = n; i < 3; ++i) a.first[i + 1] = a.first[n];
-        if (a.first[n] > 0) hipLaunchKernelGGL(pad_rows<T>, dim3(a.first[n]), dim3(256), 0, st, a);
+        constexpr int64_t most = 1 << 20;
+        if (a.first[n] > 0)
+            hipLaunchKernelGGL(pad_rows<T>, dim3((unsigned)(a.first[n] < most ? a.first[n] : most)), dim3(256), 0, st, a);
     }
 };
 
