@@ -387,7 +387,7 @@ qtcq_status qtcq_decode_matvec_mfma_noalloc(const uint32_t* bits, int M, int N, 
  *    and the next row are neither read into a result nor written.
  *  - Outputs must not overlap inputs or each other.
  *  - Rows, columns and inner lengths are at most 2^24 (F and K of the gated products 2^21),
- *    and a result at most 2^23 tiles of 128 rows by 64 columns (QTCQ_ERR_UNSUPPORTED
+ *    and a result at most 2^22 tiles of 128 rows by 64 columns (QTCQ_ERR_UNSUPPORTED
  *    beyond).  A length of zero is allowed everywhere: an empty result is a no-op, an empty
  *    sum gives zeros.
  *  - The products take a device workspace, 16-byte aligned, whose contents on entry are

@@ -23,8 +23,8 @@
 // the count of loads in flight the same.
 //
 // Where the tiles of out are fewer than the compute units, k is cut into shares of
-// split_steps steps; each writes its sums in 32 bits, and join_shares adds them in
-// order.
+// share_steps steps; each writes its sums in 32 bits, and join_shares adds them
+// in order.
 //
 // LDS holds an operand in one of two layouts, both written by the loads in whole kilobytes
 // of consecutive lanes, so the order inside a tile is chosen by which chunk of memory each
@@ -114,7 +114,7 @@ block_product(ProductArgs a)
     const int steps1 = (a.k + KS - 1) / KS;
     const int steps = MODE == kGradX ? 2 * steps1 : steps1;
     // this workgroup's share of the steps
-    const int s0 = share * a.split_steps, s1 = s0 + a.split_steps < steps ? s0 + a.split_steps : steps;
+    const int s0 = share * a.share_steps, s1 = s0 + a.share_steps < steps ? s0 + a.share_steps : steps;
     const int64_t ldp = a.ldp * SZ, ldq = a.ldq * SZ;     // in bytes
 
     // where a lane's chunks come from: row-of-k tiles, row 64 h + 8 wave + lane / 8;
@@ -235,10 +235,11 @@ block_product(ProductArgs a)
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(decltype(n)::value) : "memory");
         __builtin_amdgcn_sched_barrier(0);
     };
-    // The order of loads: P0 Q0 P1 Q1 ... where the rings are equally long; with one more
-    // place for P (FP = 8) P is a step ahead, P0 Q0 P1 Q1 P2 Q2 ... with Q(s) and P(s + 1)
-    // started together.  `after`: the loads that follow those of step 0 in the prologue,
-    // `newer`: those that follow step s + 1's when step s waits for them.
+    // The order of loads: P0 Q0 P1 Q1 ... where the rings are equally long, the last two
+    // started in step s being P(s + NPP) Q(s + NPQ); with one more place for P (FP = 8)
+    // the prologue ends in P2, and step s starts Q(s + 2) P(s + 3).  `after`: the loads
+    // that follow those of step 0 in the prologue, `newer`: those that follow step s + 1's
+    // when step s waits for them.
     constexpr bool AHEAD = NPP > NPQ;
     static_assert(NPP == NPQ || NPP == NPQ + 1, "ring lengths");
     constexpr int after = (NPP - 1) * LP + (NPQ - 1) * LQ;

@@ -15,8 +15,9 @@ constexpr int kDenseMaxDim = 1 << 24;
 constexpr int kHalfMaxRow = 1 << 21;
 // 2^14 K, the largest magnitude of a sum of K products of 8-bit integers, below 2^31
 constexpr int kInt8MaxK = 131071;
-// the largest grid of 128-wide tiles of 256 threads a launch can hold
-constexpr int64_t kDenseMaxTiles = (int64_t)1 << 23;
+// results of at most this many pieces of 8192 elements (the smallest tile of the block
+// kernel): its threads stay below the 2^32 of a launch
+constexpr int64_t kDenseMaxTiles = (int64_t)1 << 22;
 
 // whole 16-byte chunks, in elements
 inline int chunk_pitch(int cols, int size) { return (cols + 16 / size - 1) / (16 / size) * (16 / size); }
@@ -40,6 +41,7 @@ struct ProductPlan {
 
 // The compute units of the chip the tile and share counts are chosen for.
 constexpr int kComputeUnits = 256;
+
 // Whether the kernel for few rows takes a product.  It reads Q once at the memory's rate and
 // P once for every 16 columns, so its time grows with m n k; the block kernel's hardly does
 // up to 128 rows, but it pays for shares of k and a second launch.  Measured (us, few rows

@@ -38,9 +38,9 @@ struct ProductArgs {
     const float* q_scale;
     void* save[2];           // kGated: the projections, or NULL
     int64_t lds;
-    void* part;              // sums of a share of k [splits][m][part_pitch], or NULL
+    void* part;              // the shares' sums [shares][m][part_pitch], or NULL
     int part_pitch;
-    int shares, split_steps; // shares of k, and the steps of each
+    int shares, share_steps; // shares of k, and the steps of each
 };
 
 template <typename T> struct Mfma;
@@ -134,7 +134,7 @@ struct RowGrid {
     }
 };
 
-// The shares of k added in order, then the epilogue.  part [splits][m][part_pitch], four
+// The shares of k added in order, then the epilogue.  part [shares][m][part_pitch], four
 // columns a thread (kGated: the gate's sums, then the up's, part_pitch / 2 apart).
 //   grid.x = RowGrid{columns / 4}.blocks(m), block = 256.
 template <typename T, typename O, int MODE, int ACT>

@@ -80,7 +80,7 @@ qtcq_status block_go(ProductArgs a, const ProductPlan& p, void* part, hipStream_
     a.part = p.shares > 1 ? part : nullptr;
     a.part_pitch = p.part_pitch;
     a.shares = p.shares;
-    a.split_steps = p.share_steps;
+    a.share_steps = p.share_steps;
     if constexpr (MODE != kGradW) {
         if (p.fp == 2) return block_shape<T, O, MODE, ACT, 2>(a, p, st);
         if (p.fp == 4) return block_shape<T, O, MODE, ACT, 4>(a, p, st);
