@@ -29,10 +29,11 @@ def _code(code) -> int:
     return int(code)
 
 
-def _stream() -> int:
+def _stream(device: int | None = None) -> int:
     # the handle alone: building a torch Stream around it takes longer than the rest of a
     # small call's checks together
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None
+                                              else device)
 
 
 def _on_current_device(x: torch.Tensor, name: str) -> None:
@@ -403,13 +404,13 @@ ACTIVATIONS = {"silu": nat.QTCQ_ACT_SILU, "gelu": nat.QTCQ_ACT_GELU,
                "sigmoid": nat.QTCQ_ACT_SIGMOID}
 
 
-def _rows(x: torch.Tensor, name: str, dtypes, shape=None) -> int:
-    """A 2-D device tensor of rows that do not overlap, each contiguous (a slice of columns
-    of a wider matrix too).  Returns its row stride."""
+def _rows(x: torch.Tensor, name: str, dtypes, device: int, shape=None) -> int:
+    """A 2-D tensor on the current device (its index: device) of rows that do not overlap,
+    each contiguous (a slice of columns of a wider matrix too).  Returns its row stride."""
     if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dim() == 2 and x.dtype in dtypes):
         raise ValueError("%s must be a 2-D device tensor of %s"
                          % (name, " or ".join(str(d) for d in dtypes)))
-    if x.get_device() != torch.cuda.current_device():
+    if x.get_device() != device:
         _on_current_device(x, name)
     if shape is not None and tuple(x.shape) != tuple(shape):
         raise ValueError("%s must be %s" % (name, list(shape)))
@@ -425,24 +426,23 @@ def _rows(x: torch.Tensor, name: str, dtypes, shape=None) -> int:
     return x.stride(0)
 
 
-def _scales(s: torch.Tensor, name: str, n: int) -> None:
+def _scales(s: torch.Tensor, name: str, n: int, device: int) -> None:
     if not (isinstance(s, torch.Tensor) and s.is_cuda and s.dtype == torch.float32
             and s.dim() == 1 and s.shape[0] == n and s.is_contiguous()):
         raise ValueError("%s must be a contiguous float32 device tensor of %d values" % (name, n))
-    if s.get_device() != torch.cuda.current_device():
+    if s.get_device() != device:
         _on_current_device(s, name)
 
 
-def _whole_rows(*xs) -> bool:
-    """Whether the kernels can read these operands in 16-byte chunks where they are
-    (otherwise the workspace holds padded copies)."""
-    for x in xs:
-        size = x.element_size()
-        if (x.data_ptr() | x.shape[1] * size) & 15:
+def _whole_rows(pointers: int, cols: int, size: int, *strides: int) -> bool:
+    """Whether the kernels can read operands of `cols` columns in 16-byte chunks where they
+    are (otherwise the workspace holds padded copies): their pointers ORed together, the
+    bytes of an element, their row strides."""
+    for ld in strides:
+        cols |= ld
+        if ld * size > 1 << 22:
             return False
-        if x.shape[0] > 1 and (x.stride(0) * size & 15 or x.stride(0) * size > 1 << 22):
-            return False
-    return True
+    return (pointers | cols * size) & 15 == 0
 
 
 def _workspace(workspace, nbytes: int, like: torch.Tensor):
@@ -464,12 +464,13 @@ def _activation(name) -> int:
 def quantize_rows(x: torch.Tensor):
     """Rows of x ([R][C] float32, bfloat16 or float16) to 8-bit integers with one scale a
     row.  Returns (q [R][C] int8, scale [R] float32); x is about q * scale[:, None]."""
-    ldx = _rows(x, "x", (torch.float32, torch.bfloat16, torch.float16))
+    dev = torch.cuda.current_device()
+    ldx = _rows(x, "x", (torch.float32, torch.bfloat16, torch.float16), dev)
     R, C = x.shape
-    q = torch.empty((R, C), dtype=torch.int8, device=x.device)
-    scale = torch.empty(R, dtype=torch.float32, device=x.device)
+    q = torch.empty_like(x, dtype=torch.int8, memory_format=torch.contiguous_format)
+    scale = x.new_empty(R, dtype=torch.float32)
     nat.qtcq_quantize_rows(x.data_ptr(), DTYPES[x.dtype], R, C, ldx, q.data_ptr(), C,
-                           scale.data_ptr(), _stream())
+                           scale.data_ptr(), _stream(dev))
     return q, scale
 
 
@@ -487,8 +488,8 @@ def decode_matrix(bits: torch.Tensor, M: int, N: int, L: int = 16, k: int = 2, c
             and bits.numel() == (M // 16) * (N // 16) * W):
         raise ValueError("bits must hold (M/16)*(N/16) contiguous streams of %d words" % W)
     _on_current_device(bits, "bits")
-    w = torch.empty((M, N), dtype=dtype, device=bits.device)
-    scale = torch.empty(M, dtype=torch.float32, device=bits.device) if dtype == torch.int8 else None
+    w = bits.new_empty((M, N), dtype=dtype)
+    scale = bits.new_empty(M, dtype=torch.float32) if dtype == torch.int8 else None
     nat.qtcq_decode_matrix(bits.data_ptr(), M, N, L, k, _code(code), tailbiting, DTYPES[dtype],
                            w.data_ptr(), N, None if scale is None else scale.data_ptr(), _stream())
     return w if scale is None else (w, scale)
@@ -510,30 +511,33 @@ def matmul_int8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale
     and needed."""
     if dtype not in (torch.float32, torch.bfloat16, torch.float16):
         raise ValueError("dtype must be float32, bfloat16 or float16")
-    lda = _rows(a, "a", (torch.int8,))
-    ldw = _rows(w, "w", (torch.int8,))
+    dev = torch.cuda.current_device()
+    lda = _rows(a, "a", (torch.int8,), dev)
+    ldw = _rows(w, "w", (torch.int8,), dev)
     (M, K), N = a.shape, w.shape[0]
     if w.shape[1] != K:
         raise ValueError("w must have the columns of a")
-    _scales(a_scale, "a_scale", M)
-    _scales(w_scale, "w_scale", N)
-    need = nat.qtcq_matmul_int8_workspace_bytes(M, N, K, _whole_rows(a, w))
+    _scales(a_scale, "a_scale", M, dev)
+    _scales(w_scale, "w_scale", N, dev)
+    ap, wp = a.data_ptr(), w.data_ptr()
+    need = nat.qtcq_matmul_int8_workspace_bytes(M, N, K, _whole_rows(ap | wp, K, 1, lda, ldw))
     _keep, ws, ws_bytes = _workspace(workspace, need, a)
-    y = torch.empty((M, N), dtype=dtype, device=a.device)
-    nat.qtcq_matmul_int8(a.data_ptr(), lda, a_scale.data_ptr(), w.data_ptr(), ldw,
-                         w_scale.data_ptr(), M, N, K, DTYPES[dtype], y.data_ptr(), N, ws, ws_bytes,
-                         _stream())
+    y = a.new_empty((M, N), dtype=dtype)
+    nat.qtcq_matmul_int8(ap, lda, a_scale.data_ptr(), wp, ldw, w_scale.data_ptr(), M, N, K,
+                         DTYPES[dtype], y.data_ptr(), N, ws, ws_bytes, _stream(dev))
     return y
 
 
-def _gated_inputs(x, w_gate, w_up):
-    ldx = _rows(x, "x", (torch.bfloat16, torch.float16))
-    ldw = _rows(w_gate, "w_gate", (x.dtype,))
+def _gated_inputs(x, w_gate, w_up, dev):
+    """(ldx, ldw, whether x, w_gate and w_up are whole 16-byte chunks)"""
+    ldx = _rows(x, "x", (torch.bfloat16, torch.float16), dev)
+    ldw = _rows(w_gate, "w_gate", (x.dtype,), dev)
     if w_gate.shape[1] != x.shape[1]:
         raise ValueError("w_gate must have the columns of x")
-    if _rows(w_up, "w_up", (x.dtype,), w_gate.shape) != ldw:
+    if _rows(w_up, "w_up", (x.dtype,), dev, w_gate.shape) != ldw:
         raise ValueError("w_up must have the row stride of w_gate")
-    return ldx, ldw
+    return ldx, ldw, _whole_rows(x.data_ptr() | w_gate.data_ptr() | w_up.data_ptr(), x.shape[1], 2,
+                                 ldx, ldw)
 
 
 def gated_workspace(M: int, F: int, K: int, whole_rows: bool = False) -> torch.Tensor:
@@ -550,16 +554,17 @@ def gated(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, activation:
     for gated_vjp.  `workspace` (gated_workspace(M, F, K)) is allocated when not given and
     needed."""
     act = _activation(activation)
-    ldx, ldw = _gated_inputs(x, w_gate, w_up)
+    dev = torch.cuda.current_device()
+    ldx, ldw, whole = _gated_inputs(x, w_gate, w_up, dev)
     (M, K), F = x.shape, w_gate.shape[0]
-    need = nat.qtcq_gated_workspace_bytes(M, F, K, _whole_rows(x, w_gate, w_up))
+    need = nat.qtcq_gated_workspace_bytes(M, F, K, whole)
     _keep, ws, ws_bytes = _workspace(workspace, need, x)
-    h = torch.empty((M, F), dtype=x.dtype, device=x.device)
+    h = x.new_empty((M, F))
     gate, up = (torch.empty_like(h), torch.empty_like(h)) if save else (None, None)
     nat.qtcq_gated_forward(x.data_ptr(), ldx, w_gate.data_ptr(), w_up.data_ptr(), ldw,
                            DTYPES[x.dtype], M, F, K, act, h.data_ptr(), F,
                            gate.data_ptr() if save else None, up.data_ptr() if save else None, F,
-                           ws, ws_bytes, _stream())
+                           ws, ws_bytes, _stream(dev))
     return (h, gate, up) if save else h
 
 
@@ -578,20 +583,21 @@ def gated_vjp(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, gate: t
     where not wanted; `workspace` (gated_vjp_workspace(M, F, K)) is allocated when not
     given."""
     act = _activation(activation)
-    ldx, ldw = _gated_inputs(x, w_gate, w_up)
+    dev = torch.cuda.current_device()
+    ldx, ldw, whole = _gated_inputs(x, w_gate, w_up, dev)
     (M, K), F = x.shape, w_gate.shape[0]
-    ldg = _rows(gate, "gate", (x.dtype,), (M, F))
-    if _rows(up, "up", (x.dtype,), (M, F)) != ldg:
+    ldg = _rows(gate, "gate", (x.dtype,), dev, (M, F))
+    if _rows(up, "up", (x.dtype,), dev, (M, F)) != ldg:
         raise ValueError("up must have the row stride of gate")
-    ldgh = _rows(grad_h, "grad_h", (x.dtype,), (M, F))
-    need = nat.qtcq_gated_vjp_workspace_bytes(M, F, K, _whole_rows(x, w_gate, w_up))
+    ldgh = _rows(grad_h, "grad_h", (x.dtype,), dev, (M, F))
+    need = nat.qtcq_gated_vjp_workspace_bytes(M, F, K, whole)
     _keep, ws, ws_bytes = _workspace(workspace, need, x)
-    grad_x = torch.empty((M, K), dtype=x.dtype, device=x.device) if want_x else None
-    grad_wg, grad_wu = ((torch.empty((F, K), dtype=x.dtype, device=x.device) for _ in range(2))
-                        if want_w else (None, None))
+    grad_x = x.new_empty((M, K)) if want_x else None
+    grad_wg, grad_wu = (x.new_empty((F, K)), x.new_empty((F, K))) if want_w else (None, None)
     nat.qtcq_gated_vjp(x.data_ptr(), ldx, w_gate.data_ptr(), w_up.data_ptr(), ldw, gate.data_ptr(),
                        up.data_ptr(), ldg, grad_h.data_ptr(), ldgh, DTYPES[x.dtype], M, F, K, act,
                        None if grad_x is None else grad_x.data_ptr(), K,
                        None if grad_wg is None else grad_wg.data_ptr(),
-                       None if grad_wu is None else grad_wu.data_ptr(), K, ws, ws_bytes, _stream())
+                       None if grad_wu is None else grad_wu.data_ptr(), K, ws, ws_bytes,
+                       _stream(dev))
     return grad_x, grad_wg, grad_wu
