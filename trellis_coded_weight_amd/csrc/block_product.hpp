@@ -86,14 +86,19 @@ __device__ __forceinline__ void block_tile(int b, int shares, int tiles_m, int t
     tj = in / rows;
 }
 
-// grid.x = shares * tiles, grid.z = 2 for kGradW; block = 512.  FP = 8 for
-// kGradW, whose P is stored [k][row].
+// LDS of a workgroup.
+constexpr int block_lds_bytes(int fp)
+{
+    return BlockShape::p_places(fp) * BlockShape::rows(fp) * BlockShape::kStep + BlockShape::q_places(fp) * BlockShape::kTile;
+}
+
+// Workgroup b of shares * tiles (kGradW: of 2 * tiles, the gate's gradient first); lds has
+// block_lds_bytes(FP).  FP = 8 for kGradW, whose P is stored [k][row].
 template <typename T, typename O, int MODE, int ACT, int FP>
-__global__ void __launch_bounds__(BlockShape::kThreads)
-block_product(ProductArgs a)
+__device__ __forceinline__ void block_tile_product(const ProductArgs& a, int b, char* lds)
 {
     typedef Mfma<T> MM;
-    constexpr int R = BlockShape::kRows, TQ = BlockShape::kTile, TP = BlockShape::rows(FP) * BlockShape::kStep;
+    constexpr int TQ = BlockShape::kTile, TP = BlockShape::rows(FP) * BlockShape::kStep;
     constexpr int NPP = BlockShape::p_places(FP), NPQ = BlockShape::q_places(FP);
     constexpr int LP = FP / 2, LQ = 4;                   // loads of a half tile by one wave
     constexpr int SZ = (int)sizeof(T);
@@ -101,20 +106,19 @@ block_product(ProductArgs a)
     constexpr bool PT = MODE == kGradW, QT = MODE == kGradX || MODE == kGradW;
     constexpr int COLS = BlockShape::cols(MODE);
     static_assert(!PT || FP == 8, "[k][row] tiles are 256 rows wide");
-    __shared__ __align__(1024) char lds[NPP * TP + NPQ * TQ];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
     int share, ti, tj;
-    block_tile(blockIdx.x, a.shares, (a.m + BlockShape::rows(FP) - 1) / BlockShape::rows(FP), (a.n + COLS - 1) / COLS,
-               share, ti, tj);
+    block_tile(b, MODE == kGradW ? 2 : a.shares, (a.m + BlockShape::rows(FP) - 1) / BlockShape::rows(FP),
+               (a.n + COLS - 1) / COLS, share, ti, tj);
     const int i0 = ti * BlockShape::rows(FP), j0 = tj * COLS;
-    const int z = MODE == kGradW ? blockIdx.z : 0;
+    const int z = MODE == kGradW ? share : 0;
     const int steps1 = (a.k + KS - 1) / KS;
     const int steps = MODE == kGradX ? 2 * steps1 : steps1;
     // this workgroup's share of the steps
-    const int s0 = share * a.share_steps, s1 = s0 + a.share_steps < steps ? s0 + a.share_steps : steps;
+    const int s0 = MODE == kGradW ? 0 : share * a.share_steps, s1 = s0 + a.share_steps < steps ? s0 + a.share_steps : steps;
     const int64_t ldp = a.ldp * SZ, ldq = a.ldq * SZ;     // in bytes
 
     // where a lane's chunks come from: row-of-k tiles, row 64 h + 8 wave + lane / 8;
@@ -295,7 +299,7 @@ block_product(ProductArgs a)
         // (a wave's own results are 32-byte pieces of 16 rows).  Rows are 16 bytes apart in
         // banks.
         constexpr int RB = COLS * 2, PITCH = RB + 16, LR = RB / 16, RW = 64 / LR;   // lanes a row, rows a wave
-        static_assert(BlockShape::rows(FP) * PITCH <= (int)sizeof(lds), "the tile fits LDS");
+        static_assert(BlockShape::rows(FP) * PITCH <= block_lds_bytes(FP), "the tile fits LDS");
         float qs[NJ][4] = {};
         if constexpr (MODE == kInt8) {
 #pragma unroll
@@ -345,6 +349,30 @@ block_product(ProductArgs a)
                 if (row0 + i * 16 < a.m && col0 + j * 16 < a.n)
                     finish_at<O, MODE, ACT>(a, z, row0 + i * 16, col0 + j * 16, acc[i][j], acc[i][MODE == kGated ? j + 2 : j]);
     }
+}
+
+// grid.x = shares * tiles (kGradW: 2 * tiles); block = 512.
+template <typename T, typename O, int MODE, int ACT, int FP>
+__global__ void __launch_bounds__(BlockShape::kThreads)
+block_product(ProductArgs a)
+{
+    __shared__ __align__(1024) char lds[block_lds_bytes(FP)];
+    block_tile_product<T, O, MODE, ACT, FP>(a, blockIdx.x, lds);
+}
+
+// Both products of the gated gradient in one launch, the first nx workgroups grad_x's: they
+// share no result, and small ones fill the chip together.
+//   grid.x = nx + 2 * tiles of the weight gradients; block = 512.
+template <typename T, int FP>
+__global__ void __launch_bounds__(BlockShape::kThreads)
+gradient_products(ProductArgs x, ProductArgs w, int nx)
+{
+    __shared__ __align__(1024) char lds[block_lds_bytes(8) > block_lds_bytes(FP) ? block_lds_bytes(8) : block_lds_bytes(FP)];
+    const int b = blockIdx.x;
+    if (b < nx)
+        block_tile_product<T, T, kGradX, 0, FP>(x, b, lds);
+    else
+        block_tile_product<T, T, kGradW, 0, 8>(w, b - nx, lds);
 }
 
 }  // namespace qtcq

@@ -105,14 +105,13 @@ inline size_t rows_product_bytes(int mode, int size, int m, int n, int k, bool w
     return p.part_bytes + (whole ? 0 : p.p_bytes + p.q_bytes);
 }
 
-// The gated gradient's scratch: d_gate and d_up, then what its two products need in turn --
-// copies of w_gate and w_up and the shares of grad_x, and a copy of x.
+// The gated gradient's scratch: d_gate and d_up, the shares of grad_x, copies of w_gate and
+// w_up, and of x.
 struct VjpPlan {
-    size_t slopes, w_copy, part, x_copy;
+    size_t slopes, part, w_copy, x_copy;
     size_t bytes(bool w_whole, bool x_whole, bool want_x, bool want_w) const
     {
-        const size_t gx = want_x ? (w_whole ? 0 : 2 * w_copy) + part : 0, gw = want_w && !x_whole ? x_copy : 0;
-        return slopes + (gx > gw ? gx : gw);
+        return slopes + (want_x ? part + (w_whole ? 0 : 2 * w_copy) : 0) + (want_w && !x_whole ? x_copy : 0);
     }
 };
 inline VjpPlan plan_vjp(int M, int F, int K)

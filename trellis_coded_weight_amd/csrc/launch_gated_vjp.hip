@@ -30,49 +30,69 @@ qtcq_status gated_vjp_impl(const GatedVjpCall& c, void* ws, size_t wsb, hipStrea
     char* more = static_cast<char*>(ws) + v.slopes;
     if (c.M > 0 && c.F > 0)
         if (const qtcq_status s = slopes<T>(c, ldd, dg, du, st); s != QTCQ_OK) return s;
-    ProductArgs a = {};
-    a.p[0] = dg;
-    a.p[1] = du;
-    a.ldp = a.pk = a.pm = ldd;
-    a.n = c.K;
+    // both products from the slopes and, where the rows are not whole chunks, from copies
+    ProductArgs ax = {};
+    ax.p[0] = dg;
+    ax.p[1] = du;
+    ax.ldp = ax.pk = ax.pm = ldd;
+    ax.n = ax.qn = c.K;
+    ProductArgs aw = ax;
+    PadCopies<T> copies(c.K);
+    const ProductPlan plan = plan_product(kPlanGradX, (int)sizeof(T), c.M, c.K, c.F, true);
+    char* at = more + v.part;
     if (c.grad_x) {
-        const ProductPlan plan = plan_product(kPlanGradX, (int)sizeof(T), c.M, c.K, c.F, true);
-        a.q[0] = c.w_gate;
-        a.q[1] = c.w_up;
-        a.ldq = c.ldw;
-        a.qn = c.K;
+        ax.q[0] = c.w_gate;
+        ax.q[1] = c.w_up;
+        ax.ldq = c.ldw;
         if (!ww) {
-            char* at = more + v.part;
-            PadCopies<T> copies(c.K);
-            for (int i = 0; i < 2; ++i) a.q[i] = copies.add(a.q[i], c.ldw, c.F, &at);
-            a.ldq = a.qn = copies.a.pitch;
-            copies.go(st);
+            for (int i = 0; i < 2; ++i) ax.q[i] = copies.add(ax.q[i], c.ldw, c.F, &at);
+            ax.ldq = ax.qn = copies.a.pitch;
         }
-        a.out[0] = c.grad_x;
-        a.ldo = c.ldgx;
-        a.m = c.M;
-        a.k = c.F;
-        if (const qtcq_status s = block_go<T, T, kGradX, 0>(a, plan, more, st); s != QTCQ_OK) return s;
+        ax.out[0] = c.grad_x;
+        ax.ldo = c.ldgx;
+        ax.m = c.M;
+        ax.k = c.F;
+        use_plan(ax, plan, more);
+    } else {
+        at = more;
     }
     if (c.grad_w_gate) {
-        const ProductPlan plan = plan_product(kPlanGradW, (int)sizeof(T), c.F, c.K, c.M, true);
-        a.q[0] = c.x;
-        a.ldq = c.ldx;
-        a.qn = c.K;
+        aw.q[0] = c.x;
+        aw.ldq = c.ldx;
         if (!xw) {
-            char* at = more;
-            PadCopies<T> copies(c.K);
-            a.q[0] = copies.add(c.x, c.ldx, c.M, &at);
-            a.ldq = a.qn = copies.a.pitch;
-            copies.go(st);
+            aw.q[0] = copies.add(c.x, c.ldx, c.M, &at);
+            aw.ldq = aw.qn = copies.a.pitch;
         }
-        a.out[0] = c.grad_w_gate;
-        a.out[1] = c.grad_w_up;
-        a.ldo = c.ldgw;
-        a.m = c.F;
-        a.k = c.M;
-        return block_go<T, T, kGradW, 0>(a, plan, nullptr, st);
+        aw.out[0] = c.grad_w_gate;
+        aw.out[1] = c.grad_w_up;
+        aw.ldo = c.ldgw;
+        aw.m = c.F;
+        aw.k = c.M;
+        use_plan(aw, plan_product(kPlanGradW, (int)sizeof(T), c.F, c.K, c.M, true), nullptr);
     }
+    copies.go(st);
+    if (!c.grad_w_gate) return block_go<T, T, kGradX, 0>(ax, plan.fp, st);
+    if (!c.grad_x) return block_go<T, T, kGradW, 0>(aw, 8, st);
+    // One launch for both where they are small enough to fill the chip together (us, one launch
+    // against two: 64x4096x1024 25 / 34, 700x5000x1280 64 / 70, 120x14336x4096 143 / 155,
+    // 512x14336x4096 280 / 282; 2048x8192x2048 282 / 277, 4096x14336x4096 1620 / 1611).  The
+    // results are the same bits.
+    if ((double)c.M * c.F * c.K > 0x1p34) {
+        if (const qtcq_status s = block_go<T, T, kGradX, 0>(ax, plan.fp, st); s != QTCQ_OK) return s;
+        return block_go<T, T, kGradW, 0>(aw, 8, st);
+    }
+    const int64_t nx = block_groups<kGradX>(ax, plan.fp), n = nx + block_groups<kGradW>(aw, 8);
+    auto go = [&](auto fp) {
+        hipLaunchKernelGGL((gradient_products<T, decltype(fp)::value>), dim3((unsigned)n), dim3(BlockShape::kThreads), 0,
+                           st, ax, aw, (int)nx);
+    };
+    if (plan.fp == 2)
+        go(int_c<2>{});
+    else if (plan.fp == 4)
+        go(int_c<4>{});
+    else
+        go(int_c<8>{});
+    join_go<T, T, kGradX, 0>(ax, st);
     return launch_status();
 }
 

@@ -59,33 +59,53 @@ qtcq_status skinny_go(const ProductArgs& a, bool whole, hipStream_t st)
     });
 }
 
-template <typename T, typename O, int MODE, int ACT, int FP>
-qtcq_status block_shape(ProductArgs a, const ProductPlan& p, hipStream_t st)
+// workgroups of a product
+template <int MODE>
+int64_t block_groups(const ProductArgs& a, int fp)
 {
-    const int64_t n = (int64_t)blocks_for(a.m, BlockShape::rows(FP)) * blocks_for(a.n, BlockShape::cols(MODE));
-    const dim3 grid((unsigned)(n * p.shares), 1, MODE == kGradW ? 2 : 1);
-    hipLaunchKernelGGL((block_product<T, O, MODE, ACT, FP>), grid, dim3(BlockShape::kThreads), 0, st, a);
-    if constexpr (MODE != kGradW)
-        if (p.shares > 1) {
-            const RowGrid g{MODE == kGated ? p.part_pitch / 8 : p.part_pitch / 4};
-            hipLaunchKernelGGL((join_shares<T, O, MODE, ACT>), dim3((unsigned)g.blocks(a.m)), dim3(256), 0, st, a);
-        }
-    return launch_status();
+    return (int64_t)blocks_for(a.m, BlockShape::rows(fp)) * blocks_for(a.n, BlockShape::cols(MODE)) *
+           (MODE == kGradW ? 2 : a.shares);
 }
 
-// `part`: p.part_bytes of scratch
 template <typename T, typename O, int MODE, int ACT>
-qtcq_status block_go(ProductArgs a, const ProductPlan& p, void* part, hipStream_t st)
+void join_go(const ProductArgs& a, hipStream_t st)
+{
+    if (a.shares < 2) return;
+    const RowGrid g{MODE == kGated ? a.part_pitch / 8 : a.part_pitch / 4};
+    hipLaunchKernelGGL((join_shares<T, O, MODE, ACT>), dim3((unsigned)g.blocks(a.m)), dim3(256), 0, st, a);
+}
+
+// the plan's shares into the arguments; `part`: p.part_bytes of scratch
+inline void use_plan(ProductArgs& a, const ProductPlan& p, void* part)
 {
     a.part = p.shares > 1 ? part : nullptr;
     a.part_pitch = p.part_pitch;
     a.shares = p.shares;
     a.share_steps = p.share_steps;
-    if constexpr (MODE != kGradW) {
-        if (p.fp == 2) return block_shape<T, O, MODE, ACT, 2>(a, p, st);
-        if (p.fp == 4) return block_shape<T, O, MODE, ACT, 4>(a, p, st);
+}
+
+template <typename T, typename O, int MODE, int ACT, int FP>
+void block_shape(const ProductArgs& a, hipStream_t st)
+{
+    hipLaunchKernelGGL((block_product<T, O, MODE, ACT, FP>), dim3((unsigned)block_groups<MODE>(a, FP)),
+                       dim3(BlockShape::kThreads), 0, st, a);
+}
+
+template <typename T, typename O, int MODE, int ACT>
+qtcq_status block_go(const ProductArgs& a, int fp, hipStream_t st)
+{
+    if constexpr (MODE == kGradW) {
+        block_shape<T, O, MODE, ACT, 8>(a, st);
+    } else {
+        if (fp == 2)
+            block_shape<T, O, MODE, ACT, 2>(a, st);
+        else if (fp == 4)
+            block_shape<T, O, MODE, ACT, 4>(a, st);
+        else
+            block_shape<T, O, MODE, ACT, 8>(a, st);
+        join_go<T, O, MODE, ACT>(a, st);
     }
-    return block_shape<T, O, MODE, ACT, 8>(a, p, st);
+    return launch_status();
 }
 
 // Rows that start on 16 bytes and whose last chunk is whole, `inner` elements long, at a
@@ -148,7 +168,8 @@ qtcq_status rows_product(ProductArgs a, void* ws, size_t wsb, hipStream_t st)
         a.ldq = a.qk = copies.a.pitch;
     }
     copies.go(st);
-    return block_go<T, O, MODE, ACT>(a, plan, ws, st);
+    use_plan(a, plan, ws);
+    return block_go<T, O, MODE, ACT>(a, plan.fp, st);
 }
 
 }  // namespace host
