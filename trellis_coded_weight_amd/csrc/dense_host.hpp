@@ -42,7 +42,7 @@ struct ProductPlan {
 // The compute units of the chip the tile and share counts are chosen for.
 constexpr int kComputeUnits = 256;
 
-// Whether the kernel for few rows takes a product.  It reads Q once at the memory's rate and
+// Whether the kernel for few rows, at most 64, takes a product.  It reads Q once at the memory's rate and
 // P once for every 16 columns, so its time grows with m n k; the block kernel's hardly does
 // up to 128 rows, but it pays for shares of k and a second launch.  Measured (us, few rows
 // against block; m n k in bytes of the multiplied elements): 8-bit 8192x28672 at m = 1 44

@@ -31,8 +31,7 @@ qtcq_status skinny_shape(const ProductArgs& a, hipStream_t st)
 {
     constexpr int frags = 2 * (MI + (MODE == kGated ? 2 * NJ : NJ));
     constexpr int DEPTH = frags <= 8 ? 4 : (frags <= 12 ? 3 : 2);
-    const int64_t n = (int64_t)blocks_for(a.m, 16 * MI) * blocks_for(a.n, 16 * NJ);
-    const dim3 grid((unsigned)n), block(SkinnyShape::kThreads);
+    const dim3 grid(blocks_for(a.n, 16 * NJ)), block(SkinnyShape::kThreads);
     hipLaunchKernelGGL((skinny_product<T, O, MODE, ACT, MI, NJ, DEPTH, ALIGNED>), grid, block, 0, st, a);
     return launch_status();
 }

@@ -1,7 +1,7 @@
 // skinny_product.hpp -- the 8-bit product and the gated projections for few rows of P
 // (tokens), where reading Q (the weights) once is the work, gfx950.
 //
-// A workgroup of 8 waves takes MI groups of 16 rows of P and NJ groups of 16 rows of Q
+// A workgroup of 8 waves takes all rows of P, MI groups of 16, and NJ groups of 16 rows of Q
 // (kGated: NJ of Wg and NJ of Wu); its waves share k: wave w takes the 128-byte blocks w,
 // w + 8, ... of every row, so that a workgroup reads each row in kilobytes.  Operands go from
 // memory to registers in the matrix instructions' layout -- lane l holds 16 bytes of row
@@ -23,10 +23,10 @@ struct SkinnyShape {
     static constexpr int kThreads = 512;
     static constexpr int kWaves = kThreads / 64;
     static constexpr int kBlock = 128;        // bytes of k a wave takes at a time
-    static constexpr int kRound = 8;          // fragments reduced at once (64 KB of LDS)
+    static constexpr int kMaxFrags = 8;       // fragments of sums a wave (64 KB of LDS)
 };
 
-// grid.x = column tiles x chunks of 16 MI rows (chunks fastest); block = 512.
+// a.m <= 16 MI.  grid.x = ceil(a.n / (16 NJ)), block = 512.
 template <typename T, typename O, int MODE, int ACT, int MI, int NJ, int DEPTH, bool ALIGNED>
 __global__ void __launch_bounds__(SkinnyShape::kThreads)
 skinny_product(ProductArgs a)
@@ -37,19 +37,17 @@ skinny_product(ProductArgs a)
     constexpr int NQ = MODE == kGated ? 2 * NJ : NJ;      // groups of Q: gate first, then up
     constexpr int KB = SkinnyShape::kBlock / SZ;          // k of a block
     constexpr int F = MI * NQ;                            // fragments of sums
-    constexpr int G = F < SkinnyShape::kRound ? F : SkinnyShape::kRound;
-    static_assert(F % G == 0 && G % NQ == 0, "whole rounds of whole row groups");
-    __shared__ Acc red[NW][G][64];
+    static_assert(F <= SkinnyShape::kMaxFrags, "a wave finishes one fragment");
+    __shared__ Acc red[NW][F][64];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int chunks = (a.m + 16 * MI - 1) / (16 * MI);
-    const int i0 = (int)(blockIdx.x % chunks) * 16 * MI, j0 = (int)(blockIdx.x / chunks) * 16 * NJ;
+    const int j0 = blockIdx.x * 16 * NJ;
     const int64_t ldp = a.ldp * SZ, ldq = a.ldq * SZ;
     const int kb = a.k * SZ;                              // bytes of a row
     const int r = lane & 15, c = lane >> 4;
 
-    // rows i0.. of P and j0.. of Q through descriptors that end with the matrix
+    // all rows of P and rows j0.. of Q through descriptors that end with the matrix
     auto rsrc = [&](const void* p, int64_t ld, int row0, int nrows, int rows) {
         const int n = nrows - row0 < rows ? nrows - row0 : rows;
         return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(static_cast<const char*>(p) + row0 * ld), (short)0,
@@ -57,7 +55,7 @@ skinny_product(ProductArgs a)
     };
     __amdgpu_buffer_rsrc_t rp, rq[2];
     if constexpr (ALIGNED) {
-        rp = rsrc(a.p[0], ldp, i0, a.m, 16 * MI);
+        rp = rsrc(a.p[0], ldp, 0, a.m, 16 * MI);
         rq[0] = rsrc(a.q[0], ldq, j0, a.n, 16 * NJ);
         rq[1] = rsrc(a.q[MODE == kGated], ldq, j0, a.n, 16 * NJ);
     }
@@ -87,7 +85,7 @@ skinny_product(ProductArgs a)
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) o.q[h][j] = chunk(a.q[j >= NJ], a.ldq, j0 + (j % NJ) * 16 + r, a.n);
 #pragma unroll
-                for (int i = 0; i < MI; ++i) o.p[h][i] = chunk(a.p[0], a.ldp, i0 + i * 16 + r, a.m);
+                for (int i = 0; i < MI; ++i) o.p[h][i] = chunk(a.p[0], a.ldp, i * 16 + r, a.m);
             }
         }
     };
@@ -115,29 +113,25 @@ skinny_product(ProductArgs a)
         }
     }
 
-    // sums of the waves, G fragments at a time: wave w finishes fragment w of the round
-    // (kGated: gate fragment w and the up fragment beside it)
+    // sums of the waves in order: wave w finishes fragment w (kGated: gate fragment w and the
+    // up fragment beside it; fragments are numbered gate groups, then up groups, of each
+    // row group)
 #pragma unroll
-    for (int f0 = 0; f0 < F; f0 += G) {
-        if (f0 > 0) __syncthreads();
+    for (int f = 0; f < F; ++f) red[wave][f][lane] = acc[f / NQ][f % NQ];
+    __syncthreads();
+    constexpr int DONE = MODE == kGated ? F / 2 : F;
+    if (wave < DONE) {
+        const int f = MODE == kGated ? wave / NJ * NQ + wave % NJ : wave;
+        const int i = f / NQ, j = f % NQ;
+        Acc s = red[0][f][lane], u = {};
+        if constexpr (MODE == kGated) u = red[0][f + NJ][lane];
 #pragma unroll
-        for (int f = 0; f < G; ++f) red[wave][f][lane] = acc[(f0 + f) / NQ][(f0 + f) % NQ];
-        __syncthreads();
-        constexpr int DONE = MODE == kGated ? G / 2 : G;
-        if (wave < DONE) {
-            // kGated: fragments are numbered gate groups, then up groups, of each row group
-            const int f = MODE == kGated ? wave / NJ * NQ + wave % NJ : wave;
-            const int i = (f0 + f) / NQ, j = (f0 + f) % NQ;
-            Acc s = red[0][f][lane], u = {};
-            if constexpr (MODE == kGated) u = red[0][f + NJ][lane];
-#pragma unroll
-            for (int w = 1; w < NW; ++w) {
-                s += red[w][f][lane];
-                if constexpr (MODE == kGated) u += red[w][f + NJ][lane];
-            }
-            const int row = i0 + i * 16 + r, col = j0 + j * 16 + 4 * c;
-            if (row < a.m && col < a.n) finish_at<O, MODE, ACT>(a, 0, row, col, s, u);
+        for (int w = 1; w < NW; ++w) {
+            s += red[w][f][lane];
+            if constexpr (MODE == kGated) u += red[w][f + NJ][lane];
         }
+        const int row = i * 16 + r, col = j0 + j * 16 + 4 * c;
+        if (row < a.m && col < a.n) finish_at<O, MODE, ACT>(a, 0, row, col, s, u);
     }
 }
 
