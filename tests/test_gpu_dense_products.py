@@ -456,6 +456,85 @@ def test_dense_chain_in_a_graph(api, M, F, K):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("M,F,K", [(2, 70, 333), (90, 130, 2999), (300, 75, 1001)])
+def test_odd_rows_in_a_graph(api, M, F, K):
+    """Rows that are copied into the workspace first, and shares of k, captured and replayed."""
+    import torch
+    from test_gpu_graphs import capture
+    t = torch.float16
+    args = list(vjp_inputs(M, F, K, t, 1))
+    a, w = ints(M, K, 8), ints(F, K, 9)
+    sa, sw = scales(M, 10), scales(F, 11)
+
+    def step():
+        return (api.matmul_int8(a, sa, w, sw), api.gated(*args[:3])) + api.gated_vjp(*args)
+
+    say("odd rows in a graph %dx%dx%d" % (M, F, K))
+    graph, out = capture(step)
+    for rep in range(3):
+        for x, y in zip(args, vjp_inputs(M, F, K, t, 20 + rep)):
+            x.copy_(y)
+        a.copy_(ints(M, K, 30 + rep))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(out, step()):
+            assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("M,F,K", [(100, 64, 4096), (100, 70, 4099)])
+def test_given_workspaces(api, M, F, K):
+    """A workspace of the caller's gives the same bits and serves one call after another; one
+    that is too small, or not on 16 bytes, is refused."""
+    import torch
+    t = torch.bfloat16
+    args = vjp_inputs(M, F, K, t, 1)
+    a, w = ints(M, K, 8), ints(F, K, 9)
+    sa, sw = scales(M, 10), scales(F, 11)
+    w8, wg, wv = api.matmul_int8_workspace(M, F, K), api.gated_workspace(M, F, K), api.gated_vjp_workspace(M, F, K)
+    one = torch.empty(max(x.numel() for x in (w8, wg, wv)) + 16, dtype=torch.uint8, device="cuda")
+    say("given workspaces %dx%dx%d" % (M, F, K))
+    want = (api.matmul_int8(a, sa, w, sw), api.gated(*args[:3])) + api.gated_vjp(*args)
+    for ws in ((w8, wg, wv), (one[:-16],) * 3):
+        for x in ws:
+            x.fill_(0xFF)                                        # what is in it does not matter
+        got = (api.matmul_int8(a, sa, w, sw, workspace=ws[0]), api.gated(*args[:3], workspace=ws[1])) + \
+            api.gated_vjp(*args, workspace=ws[2])
+        torch.cuda.synchronize()
+        for x, y in zip(want, got):
+            assert torch.equal(x, y)
+    for bad in (one[:64], one[8:]):
+        for call in (lambda: api.matmul_int8(a, sa, w, sw, workspace=bad), lambda: api.gated(*args[:3], workspace=bad),
+                     lambda: api.gated_vjp(*args, workspace=bad)):
+            with pytest.raises(RuntimeError, match="workspace"):
+                call()
+
+
+@pytest.mark.parametrize("stride", [1 << 21, (1 << 21) + 8])
+def test_rows_far_apart(api, stride):
+    """Rows 4 MB apart, the most that is read where it is, and a little more, which is copied."""
+    import torch
+    t = torch.bfloat16
+    M, F, K = 130, 260, 72
+
+    def apart(v, ld):
+        o = torch.empty_strided(v.shape, (ld, 1), dtype=v.dtype, device="cuda")
+        o.copy_(v)
+        return o
+
+    say("rows far apart, stride %d" % stride)
+    x, wg, wu, gate, up, gh = vjp_inputs(M, F, K, t, 1)
+    far = (apart(x, stride), apart(wg, stride), apart(wu, stride))
+    assert torch.equal(api.gated(*far), api.gated(x, wg, wu))
+    for a, b in zip(api.gated_vjp(*far, gate, up, gh), api.gated_vjp(x, wg, wu, gate, up, gh)):
+        assert torch.equal(a, b)
+    a, w = ints(M, 64, 8), ints(F, 64, 9)
+    sa, sw = scales(M, 10), scales(F, 11)
+    y = api.matmul_int8(apart(a, 2 * stride), sa, apart(w, 2 * stride), sw)
+    torch.cuda.synchronize()
+    assert torch.equal(y, api.matmul_int8(a, sa, w, sw))
+
+
 def test_dense_chains_on_two_streams(api):
     """Two chains at once on streams of their own, each with its own workspace."""
     import torch
