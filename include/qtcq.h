@@ -415,6 +415,9 @@ typedef enum {
     QTCQ_ACT_SIGMOID = 4
 } qtcq_activation;
 
+/* Added to the activation of qtcq_gated_vjp: d_gate and d_up are rounded once to dtype. */
+#define QTCQ_ACT_ROUND_SLOPES 0x100
+
 /* Rows to 8-bit integers, one scale a row (activations a token a row, weights a channel a
  * row).  scale[r] = fl32(max_c |x[r][c]| / 127); q[r][c] is x[r][c] / scale[r] rounded to
  * the nearest integer, halves to even, of the exact quotient, within [-127, 127].  A row
@@ -483,10 +486,14 @@ size_t qtcq_gated_vjp_workspace_bytes(int M, int F, int K, int whole_rows);
 
 /* Gradients of the gated projections from grad_h = dLoss/dh.  With
  *   d_gate = grad_h up act'(gate),   d_up = grad_h act(gate)
- * (in binary32, each rounded once to dtype: in fp16 values beyond 65504 become infinite
- * there, and values below 2^-14 lose precision, so scale the loss as usual),
+ * in binary32,
  *   grad_x = d_gate w_gate + d_up w_up,  grad_w_gate = d_gate^T x,  grad_w_up = d_up^T x,
- * sums in binary32, each result rounded once to dtype.
+ * sums in binary32, each result rounded once to dtype.  For the products d_gate and d_up
+ * are held as the sums of two values of dtype each, within 2^-15 (bf16) or 2^-21 (fp16) of
+ * them; in fp16 also within 2^-25 absolute, and values beyond 131008 become infinite, so
+ * scale the loss as usual.  activation | QTCQ_ACT_ROUND_SLOPES has them rounded once to
+ * dtype: half the matrix work, an error of about sqrt(2) times that of the results' own
+ * rounding, and in fp16 infinities from 65520 up.
  *   x, w_gate, w_up, dtype, M, F, K, activation : as qtcq_gated_forward
  *   gate, up     [M][F] as qtcq_gated_forward saved them, row stride ldg
  *   grad_h       [M][F] of dtype, row stride ldgh

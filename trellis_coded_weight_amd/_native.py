@@ -36,6 +36,7 @@ QTCQ_ACT_GELU = 1
 QTCQ_ACT_GELU_TANH = 2
 QTCQ_ACT_RELU = 3
 QTCQ_ACT_SIGMOID = 4
+QTCQ_ACT_ROUND_SLOPES = 0x100
 
 
 class QtcqError(RuntimeError):

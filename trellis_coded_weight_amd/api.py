@@ -577,12 +577,15 @@ def gated_vjp_workspace(M: int, F: int, K: int, whole_rows: bool = False) -> tor
 
 def gated_vjp(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, gate: torch.Tensor,
               up: torch.Tensor, grad_h: torch.Tensor, activation: str = "silu",
-              want_x: bool = True, want_w: bool = True, workspace: torch.Tensor | None = None):
+              want_x: bool = True, want_w: bool = True, workspace: torch.Tensor | None = None,
+              round_slopes: bool = False):
     """Gradients of sum(grad_h * h) for h of gated(x, w_gate, w_up), with the gate and up
     that it saved.  Returns (grad_x [M][K], grad_w_gate [F][K], grad_w_up [F][K]), None
     where not wanted; `workspace` (gated_vjp_workspace(M, F, K)) is allocated when not
-    given."""
-    act = _activation(activation)
+    given.  round_slopes: the gradients of the two projections are rounded to the type of x
+    ahead of the products, which halves their work and adds about as much error as the
+    rounding of the results."""
+    act = _activation(activation) | (nat.QTCQ_ACT_ROUND_SLOPES if round_slopes else 0)
     dev = torch.cuda.current_device()
     ldx, ldw, whole = _gated_inputs(x, w_gate, w_up, dev)
     (M, K), F = x.shape, w_gate.shape[0]

@@ -117,8 +117,11 @@ __device__ __forceinline__ void block_tile_product(const ProductArgs& a, int b, 
     const int z = MODE == kGradW ? share : 0;
     const int steps1 = (a.k + KS - 1) / KS;
     const int steps = MODE == kGradX ? 2 * steps1 : steps1;
-    // this workgroup's share of the steps
-    const int s0 = MODE == kGradW ? 0 : share * a.share_steps, s1 = s0 + a.share_steps < steps ? s0 + a.share_steps : steps;
+    // this workgroup's share of the steps; where P is in two pieces each of them is taken
+    // twice, with the one and then the other (Q's half tile then comes from the L2)
+    const int twice = MODE == kGradX || MODE == kGradW ? a.pieces - 1 : 0;
+    const int first = MODE == kGradW ? 0 : share * a.share_steps;
+    const int s0 = first << twice, s1 = (first + a.share_steps < steps ? first + a.share_steps : steps) << twice;
     const int64_t ldp = a.ldp * SZ, ldq = a.ldq * SZ;     // in bytes
 
     // where a lane's chunks come from: row-of-k tiles, row 64 h + 8 wave + lane / 8;
@@ -169,9 +172,9 @@ __device__ __forceinline__ void block_tile_product(const ProductArgs& a, int b, 
     auto stage_p = [&](int s, int i) {
         char* dst = lds + i * TP;
         const bool there = s < s1;
-        const int seg = MODE == kGradX && s >= steps1 ? 1 : 0;
-        const int k0 = (s - seg * steps1) * KS;
-        const void* p = a.p[MODE == kGradW ? z : seg];
+        const int t = s >> twice, seg = MODE == kGradX && t >= steps1 ? 1 : 0;
+        const int k0 = (t - seg * steps1) * KS;
+        const T* p = static_cast<const T*>(a.p[MODE == kGradW ? z : seg]) + ((s & twice) ? a.piece_step : 0);
         if constexpr (PT)
             stage_cols(there, p, ldp, i0, a.pm, k0, dst);
         else
@@ -180,8 +183,8 @@ __device__ __forceinline__ void block_tile_product(const ProductArgs& a, int b, 
     auto stage_q = [&](int s, int i) {
         char* dst = lds + NPP * TP + i * TQ;
         const bool there = s < s1;
-        const int seg = MODE == kGradX && s >= steps1 ? 1 : 0;
-        const int k0 = (s - seg * steps1) * KS;
+        const int t = s >> twice, seg = MODE == kGradX && t >= steps1 ? 1 : 0;
+        const int k0 = (t - seg * steps1) * KS;
         if constexpr (MODE == kGated) {
             stage_rows(there, a.q[0], ldq, j0, a.n, a.qk, k0, dst, std::integral_constant<int, 2>{});
             stage_rows(there, a.q[1], ldq, j0, a.n, a.qk, k0, dst + TQ / 2, std::integral_constant<int, 2>{});

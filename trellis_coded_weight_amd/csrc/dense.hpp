@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace qtcq {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -29,6 +31,34 @@ __device__ __forceinline__ T from_f32(float v)
 {
     if constexpr (sizeof(T) == 2) asm volatile("" : "+v"(v));
     return (T)v;
+}
+
+// v as the sum of two values of T, both of v's sign: hi is the largest one below |v| in
+// magnitude, lo the rest, rounded.  Their sum is within 2^-15 (bf16) or 2^-21 (fp16, and
+// 2^-25 absolute) of v, and a v of up to 131008 stays finite in fp16.  hi stays below |v| also
+// where v itself is a value of T, so that lo is not 0 where hi is not: an infinite factor
+// then gives v's infinity twice and not inf + 0 * inf.  (Not so for |v| under 2^-110 in bf16,
+// 2^-23 in fp16.)  0, infinities and NaN are both parts.
+template <typename T>
+__device__ __forceinline__ void two_parts(float v, T& hi, T& lo)
+{
+    const uint32_t b = __builtin_bit_cast(uint32_t, v), mag = b & 0x7FFFFFFFu;
+    const float below = __builtin_bit_cast(float, mag - 1u);
+    float h;
+    if constexpr (std::is_same_v<T, __bf16>) {
+        h = __builtin_bit_cast(float, (mag - 1u) & 0xFFFF0000u);
+    } else {
+        // 2^-24 below |v| at least, half of which would round to a lo of 0; then toward zero:
+        // the mantissa's upper 10 bits, or whole multiples of 2^-24 under 2^-14
+        float u = __builtin_fminf(below, __builtin_bit_cast(float, mag) - 0x1p-24f);
+        u = __builtin_fminf(__builtin_fmaxf(u, 0.0f), 65504.0f);
+        h = u >= 0x1p-14f ? __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, u) & 0xFFFFE000u)
+                          : __builtin_truncf(u * 0x1p24f) * 0x1p-24f;
+    }
+    const bool whole = mag == 0u || mag >= 0x7F800000u;
+    h = whole ? v : __builtin_copysignf(h, v);
+    hi = (T)h;
+    lo = whole ? hi : from_f32<T>(v - h);
 }
 
 // 16 bytes at p, which need only be aligned to their element

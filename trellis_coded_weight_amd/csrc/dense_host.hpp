@@ -105,8 +105,8 @@ inline size_t rows_product_bytes(int mode, int size, int m, int n, int k, bool w
     return p.part_bytes + (whole ? 0 : p.p_bytes + p.q_bytes);
 }
 
-// The gated gradient's scratch: d_gate and d_up, the shares of grad_x, copies of w_gate and
-// w_up, and of x.
+// The gated gradient's scratch: d_gate and d_up in one or two parts, the shares of grad_x,
+// copies of w_gate and w_up, and of x.
 struct VjpPlan {
     size_t slopes, part, w_copy, x_copy;
     size_t bytes(bool w_whole, bool x_whole, bool want_x, bool want_w) const
@@ -114,11 +114,11 @@ struct VjpPlan {
         return slopes + (want_x ? part + (w_whole ? 0 : 2 * w_copy) : 0) + (want_w && !x_whole ? x_copy : 0);
     }
 };
-inline VjpPlan plan_vjp(int M, int F, int K)
+inline VjpPlan plan_vjp(int M, int F, int K, int pieces)
 {
     VjpPlan v;
     const size_t row = (size_t)chunk_pitch(K, 2) * 2;
-    v.slopes = round256((size_t)2 * 2 * M * slope_pitch(F));
+    v.slopes = round256((size_t)2 * 2 * pieces * M * slope_pitch(F));
     v.w_copy = round256((size_t)F * row);
     v.x_copy = round256((size_t)M * row);
     v.part = plan_product(kPlanGradX, 2, M, K, F, true).part_bytes;
@@ -139,6 +139,7 @@ struct GatedVjpCall {
     const void *x, *w_gate, *w_up, *gate, *up, *grad_h;
     int64_t ldx, ldw, ldg, ldgh;
     int dtype, M, F, K, act;
+    int pieces;              // parts that d_gate and d_up are held in
     void *grad_x, *grad_w_gate, *grad_w_up;
     int64_t ldgx, ldgw;
 };

@@ -12,7 +12,8 @@ qtcq_status slopes(const GatedVjpCall& c, int ldd, T* dg, T* du, hipStream_t st)
     return with_act(c.act, [&](auto act) {
         hipLaunchKernelGGL((gated_slopes<T, decltype(act)::value>), grid, block, 0, st,
                            static_cast<const T*>(c.gate), static_cast<const T*>(c.up), c.ldg,
-                           static_cast<const T*>(c.grad_h), c.ldgh, c.M, c.F, ldd, dg, du);
+                           static_cast<const T*>(c.grad_h), c.ldgh, c.M, c.F, ldd, dg, du, c.pieces,
+                           (int64_t)2 * c.M * ldd);
         return launch_status();
     });
 }
@@ -20,7 +21,7 @@ qtcq_status slopes(const GatedVjpCall& c, int ldd, T* dg, T* du, hipStream_t st)
 template <typename T>
 qtcq_status gated_vjp_impl(const GatedVjpCall& c, void* ws, size_t wsb, hipStream_t st)
 {
-    const VjpPlan v = plan_vjp(c.M, c.F, c.K);
+    const VjpPlan v = plan_vjp(c.M, c.F, c.K, c.pieces);
     const bool ww = whole_chunks<T>(c.w_gate, c.ldw, c.K) && aligned16(c.w_up), xw = whole_chunks<T>(c.x, c.ldx, c.K);
     const size_t need = v.bytes(ww, xw, c.grad_x != nullptr, c.grad_w_gate != nullptr);
     if (need > 0 && (!ws || !aligned16(ws) || wsb < need)) return QTCQ_ERR_WORKSPACE;
@@ -35,6 +36,8 @@ qtcq_status gated_vjp_impl(const GatedVjpCall& c, void* ws, size_t wsb, hipStrea
     ax.p[0] = dg;
     ax.p[1] = du;
     ax.ldp = ax.pk = ax.pm = ldd;
+    ax.pieces = c.pieces;
+    ax.piece_step = (int64_t)2 * c.M * ldd;
     ax.n = ax.qn = c.K;
     ProductArgs aw = ax;
     PadCopies<T> copies(c.K);

@@ -7,6 +7,8 @@
 //   kGated   P = x [M][K], Q = Wg and Wu [F][K], both in one workgroup; out = act(gate) * up
 //   kGradX   P = dg then du [M][F], Q(j, k) = Wg[k][j] then Wu[k][j]; one sum over both
 //   kGradW   P(i, k) = dg[k][i] (z = 0) or du[k][i] (z = 1), Q(j, k) = x[k][j]
+// dg and du are the sums of two parts each (gated_slopes), whose products with Q are added
+// one after the other, or one part, where the caller has them rounded.
 //
 // v_mfma_*_16x16x(64 bytes) on Q rows times P rows: lane l holds 16 bytes of Q row l % 16
 // and of P row l % 16 from byte 16 (l / 16) of a 64-byte step, and the result
@@ -41,6 +43,8 @@ struct ProductArgs {
     void* part;              // the shares' sums [shares][m][part_pitch], or NULL
     int part_pitch;
     int shares, share_steps; // shares of k, and the steps of each
+    int pieces;              // kGradX, kGradW: parts that P is the sum of, 1 or 2,
+    int64_t piece_step;      // and the elements from one to the next
 };
 
 template <typename T> struct Mfma;
@@ -184,16 +188,17 @@ pad_rows(PadArgs a)
     }
 }
 
-// dg = dh u act'(g) and du = dh act(g), each formed in binary32 and rounded once to the
-// operands' type, the operand type of the matrix instructions that take them next.  The
-// rounding's relative 2^-9 (bf16) or 2^-12 (fp16) a term adds in squares over a sum, about
-// what the rounding of the gradient itself costs.  d [2][M][ldd]: columns from F to ldd
-// are written as zero.
+// dg = dh u act'(g) and du = dh act(g), each formed in binary32.  The matrix instructions
+// that take them next have 16-bit operands, so each is written as two parts (two_parts), or,
+// with one piece, rounded once to the operands' type: its relative 2^-8 (bf16) or 2^-11 (fp16)
+// at most a term adds in squares over a sum, about what the rounding of the gradient itself
+// costs.  d [pieces][2][M][ldd], dgate and dup in the first piece; columns from F to ldd are
+// written as zero.
 //   grid.x = RowGrid{ldd / 8}.blocks(M), block = 256; ldd a multiple of 8.
 template <typename T, int ACT>
 __global__ void __launch_bounds__(256)
 gated_slopes(const T* __restrict__ gate, const T* __restrict__ up, int64_t ldg, const T* __restrict__ gh, int64_t ldh,
-             int64_t M, int F, int ldd, T* __restrict__ dgate, T* __restrict__ dup)
+             int64_t M, int F, int ldd, T* __restrict__ dgate, T* __restrict__ dup, int pieces, int64_t piece_step)
 {
     typedef T T8 __attribute__((ext_vector_type(8)));
     int64_t row;
@@ -203,17 +208,28 @@ gated_slopes(const T* __restrict__ gate, const T* __restrict__ up, int64_t ldg, 
     const T8 g = __builtin_bit_cast(T8, load_chunk<T>(gate + row * ldg, col, F));
     const T8 u = __builtin_bit_cast(T8, load_chunk<T>(up + row * ldg, col, F));
     const T8 h = __builtin_bit_cast(T8, load_chunk<T>(gh + row * ldh, col, F));
-    T8 dg, du;
+    T8 dg, du, dg2, du2;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         float av, dv;
         activate_grad<ACT>((float)g[e], av, dv);
         const float hv = (float)h[e];
-        dg[e] = col + e < F ? from_f32<T>(hv * (float)u[e] * dv) : (T)0.0f;
-        du[e] = col + e < F ? from_f32<T>(hv * av) : (T)0.0f;
+        const float gv = col + e < F ? hv * (float)u[e] * dv : 0.0f, uv = col + e < F ? hv * av : 0.0f;
+        T hi, lo;
+        two_parts(gv, hi, lo);
+        dg[e] = pieces == 2 ? hi : from_f32<T>(gv);
+        dg2[e] = lo;
+        two_parts(uv, hi, lo);
+        du[e] = pieces == 2 ? hi : from_f32<T>(uv);
+        du2[e] = lo;
     }
-    *reinterpret_cast<T8*>(dgate + row * ldd + col) = dg;
-    *reinterpret_cast<T8*>(dup + row * ldd + col) = du;
+    const int64_t at = row * ldd + col;
+    *reinterpret_cast<T8*>(dgate + at) = dg;
+    *reinterpret_cast<T8*>(dup + at) = du;
+    if (pieces == 2) {
+        *reinterpret_cast<T8*>(dgate + piece_step + at) = dg2;
+        *reinterpret_cast<T8*>(dup + piece_step + at) = du2;
+    }
 }
 
 }  // namespace qtcq

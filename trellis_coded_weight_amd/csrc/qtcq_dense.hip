@@ -113,7 +113,7 @@ qtcq_status qtcq_gated_forward(const void* x, int64_t ldx, const void* w_gate, c
 size_t qtcq_gated_vjp_workspace_bytes(int M, int F, int K, int whole_rows)
 {
     if (!vjp_sizes_ok(M, F, K)) return 0;
-    return plan_vjp(M, F, K).bytes(whole_rows != 0, whole_rows != 0, true, true);
+    return plan_vjp(M, F, K, 2).bytes(whole_rows != 0, whole_rows != 0, true, true);
 }
 
 qtcq_status qtcq_gated_vjp(const void* x, int64_t ldx, const void* w_gate, const void* w_up, int64_t ldw,
@@ -125,6 +125,8 @@ qtcq_status qtcq_gated_vjp(const void* x, int64_t ldx, const void* w_gate, const
     if ((grad_w_gate == nullptr) != (grad_w_up == nullptr)) return QTCQ_ERR_INVALID_ARG;
     if (grad_x && (ldw < K || ldgx < K)) return QTCQ_ERR_INVALID_ARG;
     if (grad_w_gate && (ldx < K || ldgw < K)) return QTCQ_ERR_INVALID_ARG;
+    const int pieces = activation >= 0 && (activation & QTCQ_ACT_ROUND_SLOPES) ? 1 : 2;
+    if (pieces == 1) activation &= ~QTCQ_ACT_ROUND_SLOPES;
     if (!half_type(dtype) || activation < QTCQ_ACT_SILU || activation > QTCQ_ACT_SIGMOID) return QTCQ_ERR_UNSUPPORTED;
     if (!vjp_sizes_ok(M, F, K)) return QTCQ_ERR_UNSUPPORTED;
     // what is left to write: grad_x [M][K], the weight gradients [F][K]
@@ -135,7 +137,7 @@ qtcq_status qtcq_gated_vjp(const void* x, int64_t ldx, const void* w_gate, const
         return QTCQ_ERR_INVALID_ARG;
     if (want_w && (!aligned_to(grad_w_gate, 2) || !aligned_to(grad_w_up, 2) || !there(x, M, K, 2)))
         return QTCQ_ERR_INVALID_ARG;
-    const GatedVjpCall c = {x, w_gate, w_up, gate, up, grad_h, ldx, ldw, ldg, ldgh, dtype, M, F, K, activation,
+    const GatedVjpCall c = {x, w_gate, w_up, gate, up, grad_h, ldx, ldw, ldg, ldgh, dtype, M, F, K, activation, pieces,
                             want_x ? grad_x : nullptr, want_w ? grad_w_gate : nullptr, want_w ? grad_w_up : nullptr,
                             ldgx, ldgw};
     return host::launch_gated_vjp(c, workspace, workspace_bytes, as_stream(stream));
