@@ -81,13 +81,26 @@ __device__ __forceinline__ u32x4 load_chunk(const T* p, int at, int n)
     return __builtin_bit_cast(u32x4, o);
 }
 
-// 1 / (1 + exp(-g)) from the hardware's exp2 and reciprocal (one unit in the last place
-// each; the rounding of g log2 e adds |g| 2^-24 relative): far below the roundings of the
-// 16-bit operands and results, and a seventh of the instructions of the full-precision
-// ones.  exp2 overflows to infinity for g below -88.7, which gives 0.
+// sigmoid(g) = 1 / (1 + exp(-g)) and its complement sigmoid(-g), from the hardware's exp2 and
+// reciprocal (one unit in the last place each; the rounding of g log2 e adds a few |g| 2^-24
+// relative): far below the roundings of the 16-bit operands and results, and a seventh of the
+// instructions of the full-precision ones.  With e = exp(-|g|) the larger of the two is
+// 1 / (1 + e) and the smaller e / (1 + e), so neither is a difference that loses its digits,
+// and nothing overflows.  e is the square of exp(-|g| / 2), as the hardware's exp2 flushes
+// results below 2^-126 to 0, which g sigmoid(g) may still exceed; it is 0 itself below 2^-149.
+__device__ __forceinline__ void sigmoids_f32(float g, float& s, float& c)
+{
+    const float h = __builtin_amdgcn_exp2f(-0.72134752044448170f * __builtin_fabsf(g)), e = h * h;
+    const float r = __builtin_amdgcn_rcpf(1.0f + e), t = e * r;
+    s = g < 0.0f ? t : r;
+    c = g < 0.0f ? r : t;
+}
+
 __device__ __forceinline__ float sigmoid_f32(float g)
 {
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * g));
+    float s, c;
+    sigmoids_f32(g, s, c);
+    return s;
 }
 
 constexpr float kGeluTanhC = 1.5957691216057308f;        // 2 sqrt(2 / pi)
@@ -104,33 +117,34 @@ __device__ __forceinline__ float activate(float g)
     return sigmoid_f32(g);
 }
 
-// act(g) and act'(g).  A saturated sigmoid times a large g: 1 - s is exactly 0 for g > 17,
-// and s underflows to 0 before g (1 - s) can matter.
+// act(g) and act'(g).  A saturated sigmoid times a large g: its complement underflows to 0
+// before their product can matter.
 template <int ACT>
 __device__ __forceinline__ void activate_grad(float g, float& a, float& d)
 {
+    float s, c;
     if constexpr (ACT == kActSilu) {
-        const float s = sigmoid_f32(g);
+        sigmoids_f32(g, s, c);
         a = g * s;
-        d = s * (1.0f + g * (1.0f - s));
+        d = s * (1.0f + g * c);
     } else if constexpr (ACT == kActGelu) {
-        const float c = 0.5f * erfcf(-0.7071067811865476f * g);
+        c = 0.5f * erfcf(-0.7071067811865476f * g);
         a = g * c;
         d = c + g * (0.3989422804014327f * expf(-0.5f * g * g));
     } else if constexpr (ACT == kActGeluTanh) {
-        const float s = sigmoid_f32(g * (kGeluTanhC + kGeluTanhC3 * g * g));
+        sigmoids_f32(g * (kGeluTanhC + kGeluTanhC3 * g * g), s, c);
         a = g * s;
         // g^2 s (1 - s): the polynomial's slope multiplies s (1 - s) before g, so that a
         // large |g| meets an exact 0
-        const float t = s * (1.0f - s);
+        const float t = s * c;
         d = t == 0.0f ? s : s + g * t * (kGeluTanhC + 3.0f * kGeluTanhC3 * g * g);
     } else if constexpr (ACT == kActRelu) {
         a = g < 0.0f ? 0.0f : g;
         d = g > 0.0f ? 1.0f : (g == g ? 0.0f : g);
     } else {
-        const float s = sigmoid_f32(g);
+        sigmoids_f32(g, s, c);
         a = s;
-        d = s * (1.0f - s);
+        d = s * c;
     }
 }
 
