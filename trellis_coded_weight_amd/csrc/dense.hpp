@@ -118,10 +118,13 @@ __device__ __forceinline__ float activate(float g)
 }
 
 // act(g) and act'(g).  A saturated sigmoid times a large g: its complement underflows to 0
-// before their product can matter.
+// before their product can matter.  An infinite g, which may be a finite one that the type it
+// was saved in does not hold, has the limits of both: the slope is taken at the largest
+// finite g of its sign, and so is act at -infinity.
 template <int ACT>
-__device__ __forceinline__ void activate_grad(float g, float& a, float& d)
+__device__ __forceinline__ void activate_grad(float gate, float& a, float& d)
 {
+    const float g = __builtin_fabsf(gate) == __builtin_inff() ? __builtin_copysignf(0x1.fffffep127f, gate) : gate;
     float s, c;
     if constexpr (ACT == kActSilu) {
         sigmoids_f32(g, s, c);
@@ -146,6 +149,7 @@ __device__ __forceinline__ void activate_grad(float g, float& a, float& d)
         a = s;
         d = s * c;
     }
+    if constexpr (ACT != kActSigmoid) a = gate == __builtin_inff() ? gate : a;
 }
 
 }  // namespace qtcq
