@@ -552,10 +552,14 @@ def gated(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, activation:
     """h [M][F] = act(x w_gate^T) * (x w_up^T) for x [M][K] and w_gate, w_up [F][K], all
     bfloat16 or all float16.  With save, returns (h, gate, up): the two projections too,
     for gated_vjp.  `workspace` (gated_workspace(M, F, K)) is allocated when not given and
-    needed."""
+    needed.  Autograd does not see the call, so inputs that require gradients are refused
+    while it records (torch.no_grad() or detached inputs, and gated_vjp for the gradients)."""
     act = _activation(activation)
     dev = torch.cuda.current_device()
     ldx, ldw, whole = _gated_inputs(x, w_gate, w_up, dev)
+    if torch.is_grad_enabled() and (x.requires_grad or w_gate.requires_grad or w_up.requires_grad):
+        raise ValueError("gated does not record gradients: call it under torch.no_grad() or with "
+                         "detached inputs, and gated_vjp for the gradients")
     (M, K), F = x.shape, w_gate.shape[0]
     need = nat.qtcq_gated_workspace_bytes(M, F, K, whole)
     _keep, ws, ws_bytes = _workspace(workspace, need, x)
