@@ -140,12 +140,11 @@ __device__ __forceinline__ void block_tile_product(const ProductArgs& a, int b, 
     };
     // 16 bytes a lane from r + off to LDS at dst + 16 lane.  Written out because the compiler
     // would wait for all such loads ahead of every ds_read_b64_tr_b16; `landed` below waits
-    // for the ones that matter.  It has no output register: the data goes to LDS.  (The
-    // compiler keeps no value in m0: it sets it where it uses it.)
+    // for the ones that matter.  It has no output register: the data goes to LDS.
     auto to_lds = [&](u32x4 r, const char* dst, int off) {
         const uint32_t at = (uint32_t)reinterpret_cast<uintptr_t>((lds_char*)dst);
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                     ::"s"(at), "v"(off), "s"(r) : "memory");
+                     ::"s"(at), "v"(off), "s"(r) : "m0", "memory");
     };
     // HR groups of 64 rows (of k) from row0 of `base` [nrows][k] into dst; nothing but zeros
     // if this step is not there
