@@ -14,8 +14,14 @@ qtcq_status quantize_impl(const void* x, int64_t rows, int cols, int64_t ldx, in
     constexpr int E = 16 / (int)sizeof(T);
     auto go = [&](auto rt, auto nch) {
         constexpr int RT = decltype(rt)::value, NCH = decltype(nch)::value;
-        hipLaunchKernelGGL((quantize_rows<T, RT, NCH>), dim3(blocks_for(rows, QuantShape::kThreads / RT)),
-                           dim3(QuantShape::kThreads), 0, st, static_cast<const T*>(x), rows, cols, ldx, q, ldq, scale);
+        // as many rows a launch as keep its threads below 2^32
+        constexpr int64_t most = ((int64_t)1 << 31) / RT;
+        for (int64_t r = 0; r < rows; r += most) {
+            const int64_t n = rows - r < most ? rows - r : most;
+            hipLaunchKernelGGL((quantize_rows<T, RT, NCH>), dim3(blocks_for(n, QuantShape::kThreads / RT)),
+                               dim3(QuantShape::kThreads), 0, st, static_cast<const T*>(x) + r * ldx, n, cols, ldx,
+                               q + r * ldq, ldq, scale + r);
+        }
         return launch_status();
     };
     // A wave a row needs no barrier, a workgroup a row keeps longer rows in registers (us, wave
