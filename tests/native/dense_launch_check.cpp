@@ -7,6 +7,7 @@
 //   int8 DTYPE M N K ALIGNED
 //   gated DTYPE M F K ALIGNED ACT
 //   vjp DTYPE M F K ALIGNED ACT
+//   kernels        (the names of all kernels, in the form of launches with no grid)
 // (ALIGNED 0: operands one element off 16 bytes.)  Each answers with its status and, a
 // line each, its launches: mangled name, grid.x, block.x, and for quantize_rows the rows and
 // the three pointers it was given.
@@ -80,7 +81,10 @@ int main()
     while (std::cin >> op) {
         long long d = 0, m = 0, n = 0, k = 0, al = 1, act = 0;
         int s = -1;
-        if (op == "quantize") {
+        if (op == "kernels") {
+            for (const auto& it : kernels()) std::printf("%s 0 0\n", it.second.c_str());
+            s = 0;
+        } else if (op == "quantize") {
             std::cin >> d >> m >> n;
             s = qtcq_quantize_rows(at(1ull << 40, 1, 0), (int)d, m, (int)n, n, (int8_t*)at(2ull << 40, 1, 0), n,
                                    (float*)at(3ull << 40, 1, 0), nullptr);

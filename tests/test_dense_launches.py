@@ -2,10 +2,12 @@
 every launch has blocks and stays below 2^32 threads, the most a launch holds, and rows that
 need more go in several.  No GPU needed."""
 import os
+import re
 
 import pytest
 
 import dense_launches
+import dense_variants
 
 F32, BF16, F16, I8 = 0, 1, 2, 3
 
@@ -57,3 +59,24 @@ def test_every_grid_fits_a_launch(recorder):
             grid, block = int(words[1]), int(words[2])
             assert 0 < grid and grid * block < 1 << 32, (call, words)
     assert accepted > len(calls) // 4
+
+
+def test_sizes_that_reach_every_product_kernel(recorder):
+    """The lists of dense_variants.py launch every kernel that the products are built as."""
+    families = ("skinny_product", "block_product", "join_shares", "pad_rows", "gated_slopes", "gradient_products")
+    built = {w[0] for w in dense_launches.record(recorder, ["kernels"])[0][1] if any(f in w[0] for f in families)}
+    assert len(built) > 150
+    reached, shares = set(), set()
+    for call, (status, launches) in zip(dense_variants.calls(), dense_launches.record(recorder, dense_variants.calls())):
+        assert status == 0 and launches, call
+        names = [w[0] for w in launches]
+        reached |= set(names)
+        joined = any("join_shares" in n for n in names)
+        for n in names:
+            # the operator and the tile height, 32 times the last template argument
+            m = re.search(r"block_product.*Li([012])ELi\dELi([248])E|gradient_products.*Li([248])E", n)
+            if m:
+                shares.add((m[1] or "2", m[2] or m[3], joined))
+    assert not built - reached, sorted(built - reached)
+    # each height of each operator's tiles on whole sums and on shares
+    assert len(shares) == 3 * 3 * 2, sorted(shares)
