@@ -80,3 +80,14 @@ def test_sizes_that_reach_every_product_kernel(recorder):
     assert not built - reached, sorted(built - reached)
     # each height of each operator's tiles on whole sums and on shares
     assert len(shares) == 3 * 3 * 2, sorted(shares)
+
+
+def test_few_rows_go_where_they_are_faster(recorder):
+    """Sizes measured with both kernels: the kernel for few rows or the block kernel."""
+    few = ["int8 1 1 8192 28672 1", "gated 1 8 14336 4096 1 0", "gated 1 32 4096 4096 1 0", "int8 1 1 28672 8193 0",
+           "gated 1 16 4096 4097 0 0"]
+    block = ["int8 1 16 8192 28672 1", "int8 1 16 28672 8192 1", "gated 1 24 14336 4096 1 0",
+             "gated 1 64 4096 4096 1 0", "int8 1 8 28672 8193 0", "gated 1 32 4096 4097 0 0"]
+    for calls, kernel in ((few, "skinny_product"), (block, "block_product")):
+        for call, (status, launches) in zip(calls, dense_launches.record(recorder, calls)):
+            assert status == 0 and any(kernel in w[0] for w in launches), call

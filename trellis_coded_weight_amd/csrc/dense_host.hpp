@@ -45,17 +45,18 @@ constexpr int kComputeUnits = 256;
 // Whether the kernel for few rows, at most 64, takes a product.  It reads Q once at the memory's rate and
 // P once for every 16 columns, so its time grows with m n k; the block kernel's hardly does
 // up to 128 rows, but it pays for shares of k and a second launch.  Measured (us, few rows
-// against block; m n k in bytes of the multiplied elements): 8-bit 8192x28672 at m = 1 44
-// against 48, m = 8 (2^30.8) 54 / 48, m = 16 65 / 49; 28672x8192 at m = 8 59 / 61, 16
-// (2^31.8) 65 / 62, 24 77 / 62; gated 14336x4096 at m = 8 (2^30.8) 54 / 61, 24 70 / 62;
-// gated 4096x4096 at m = 32 (2^31) 23 / 25, 64 32 / 26.  Rows that are not whole chunks cost
-// the block kernel a copy and this one slower loads: 28672x8193 at m = 1 127 / 137, 8 157 /
-// 138; gated 4096x4097 at m = 16 (2^30) 42 / 50, 32 54 / 51.
+// against block; m n k in bytes of the multiplied elements): 8-bit 8192x28672 at m = 1 44.5
+// against 49.1, m = 8 (2^30.8) 51.8 / 48.2, m = 16 63.8 / 48.1; 28672x8192 at m = 8 52.7 /
+// 52.2, 16 (2^31.8) 64.7 / 53.0; gated 14336x4096 at m = 8 (2^30.8) 51.5 / 51.9, 24 69.6 /
+// 53.4; gated 4096x4096 at m = 32 (2^31) 22.8 / 23.0, 64 30.5 / 25.2.  Rows that are not whole
+// chunks cost the block kernel a copy and this one slower loads: 28672x8193 at m = 1 106.8 /
+// 143.9, 8 (2^30.8) 160.8 / 145.1; gated 4096x4097 at m = 16 (just past 2^30) 41.3 / 46.6, 32
+// 53.2 / 48.0.
 inline bool few_rows(int mode, int size, int m, int n, int k, bool whole)
 {
     if (mode != kPlanInt8 && mode != kPlanGated) return false;
     const double work = (double)m * n * k * size * (mode == kPlanGated ? 2 : 1);
-    return whole ? m <= 4 || (m <= 64 && work <= 0x1p31) : m <= 2 || (m <= 64 && work <= 0x1p30);
+    return whole ? m <= 4 || (m <= 64 && work <= 0x1p31) : m <= 2 || (m <= 64 && work <= 0x1.1p30);
 }
 
 // mode, bytes of an element, rows and columns of the result, length of a sum; `whole`: the
