@@ -1,6 +1,8 @@
 """Torch-facing convenience layer over the C ABI: allocates outputs and workspaces as
 CUDA (HIP) tensors and calls the entry points on the current stream.  Only argument
-marshalling happens here; every step of the path runs in the HIP kernels.
+marshalling happens here; every step of the path runs in the HIP kernels.  Autograd
+records none of these calls: gradients come from the calls that compute them (bcjr_vjp,
+gated_vjp).
 """
 from __future__ import annotations
 

@@ -1,8 +1,8 @@
 """Build the gfx950 HIP library libqtcq.so in-tree with hipcc.
 
 The library is the C-ABI units (csrc/qtcq.hip, and csrc/qtcq_dense.hip for the dense
-operators) and one launch unit per kernel family (csrc/launch_*.hip).  Each is compiled to an object on its own, in parallel, and the
-objects are linked into the shared library.
+operators) and one launch unit per kernel family (csrc/launch_*.hip).  Each is compiled to
+an object on its own, in parallel, and the objects are linked into the shared library.
 
 Flags that matter for results:
   -ffp-contract=off       the path cost is a chain of separately rounded sub, square,

@@ -75,8 +75,8 @@ inline ProductPlan plan_product(int mode, int size, int m, int n, int k, bool wh
     const int steps = (k + per - 1) / per * (mode == kPlanGradX ? 2 : 1);
     // The tile's rows and the shares of k by the shortest estimate, in us: rounds of
     // workgroups (one a compute unit) times a share's steps, each 0.7, 1.0 or 1.7 with 64, 128
-    // or 256 rows (8192x28672 at m = 2048: 616, 442 and 392 us in 4, 2 and 1 rounds of 224
-    // steps); shares cost a second launch, and their sums' way out and back at 4 TB/s.
+    // or 256 rows (8-bit 8192x28672 at m = 2048: 616, 435 and 390 us in 4, 2 and 1 rounds of
+    // 224 steps); shares cost a second launch, and their sums' way out and back at 4 TB/s.
     // [k][row] tiles of P are 256 rows wide.
     double best = 0;
     for (int fp = mode == kPlanGradW ? 8 : 2; fp <= 8; fp *= 2) {
@@ -106,7 +106,7 @@ inline size_t rows_product_bytes(int mode, int size, int m, int n, int k, bool w
     return p.part_bytes + (whole ? 0 : p.p_bytes + p.q_bytes);
 }
 
-// The gated gradient's scratch: d_gate and d_up in one or two parts, the shares of grad_x,
+// The gated gradient's scratch: d_gate and d_up, one after the other, in one or two parts, the shares of grad_x,
 // copies of w_gate and w_up, and of x.
 struct VjpPlan {
     size_t slopes, part, w_copy, x_copy;

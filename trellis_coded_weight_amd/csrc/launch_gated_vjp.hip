@@ -77,9 +77,9 @@ qtcq_status gated_vjp_impl(const GatedVjpCall& c, void* ws, size_t wsb, hipStrea
     if (!c.grad_w_gate) return block_go<T, T, kGradX, 0>(ax, plan.fp, st);
     if (!c.grad_x) return block_go<T, T, kGradW, 0>(aw, 8, st);
     // One launch for both where they are small enough to fill the chip together (us, one launch
-    // against two: 64x4096x1024 25 / 34, 700x5000x1280 64 / 70, 120x14336x4096 143 / 155,
-    // 512x14336x4096 280 / 282; 2048x8192x2048 282 / 277, 4096x14336x4096 1620 / 1611).  The
-    // results are the same bits.
+    // against two: 64x4096x1024 32.6 / 41.4, 700x5000x1280 105 / 110, 120x14336x4096 183 / 186;
+    // on slopes of one part 28.9 / 36.1, 74 / 77, 147 / 157); beyond that the two are within 3%
+    // (512x14336x4096 476 / 492, 4096x14336x4096 3260 both).  The results are the same bits.
     if ((double)c.M * c.F * c.K > 0x1p34) {
         if (const qtcq_status s = block_go<T, T, kGradX, 0>(ax, plan.fp, st); s != QTCQ_OK) return s;
         return block_go<T, T, kGradW, 0>(aw, 8, st);

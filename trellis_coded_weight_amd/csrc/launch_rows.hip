@@ -25,8 +25,8 @@ qtcq_status quantize_impl(const void* x, int64_t rows, int cols, int64_t ldx, in
         return launch_status();
     };
     // A wave a row needs no barrier, a workgroup a row keeps longer rows in registers (us, wave
-    // against workgroup, bf16: 65536x1024 31 / 56, 65536x2048 75 / 87, 8192x4096 23 / 18,
-    // 16384x8192 104 / 75).
+    // against workgroup, bf16: 65536x1024 38 / 72, 65536x2048 76 / 86, 8192x4096 25 / 20,
+    // 16384x8192 108 / 74).
     const int chunks = (cols + E - 1) / E;
     if (chunks <= 64) return go(int_c<64>{}, int_c<1>{});
     if (chunks <= 256) return go(int_c<64>{}, int_c<4>{});
@@ -46,7 +46,8 @@ qtcq_status decode_rows_impl(const uint32_t* bits, int M, int N, int dtype, void
     };
     switch (dtype) {
     // codes held between the passes: 32 registers for up to 4096 columns, 64 beyond (3INST,
-    // us, 32 against 64: 4096x4096 14.1 / 14.3, 28672x8192 117 / 103)
+    // us, 32 against 64: 4096x4096 14.1 / 14.0, 28672x8192 115 / 107).  Columns past 4096 or
+    // 8192 of a row are decoded twice (4096x14336 47 / 45, 8192x28672 150 / 146).
     case QTCQ_I8: return N <= 16 * DecodeRowsShape::kTiles ? go(int_c<0>{}, int_c<1>{}) : go(int_c<0>{}, int_c<2>{});
     case QTCQ_BF16: return go(int_c<1>{}, int_c<1>{});
     case QTCQ_F16: return go(int_c<2>{}, int_c<1>{});

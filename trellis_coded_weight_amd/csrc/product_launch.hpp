@@ -39,18 +39,18 @@ qtcq_status skinny_shape(const ProductArgs& a, hipStream_t st)
 template <typename T, typename O, int MODE, int ACT>
 qtcq_status skinny_go(const ProductArgs& a, bool whole, hipStream_t st)
 {
-    constexpr int WIDE = MODE == kGated ? 1 : 2;
-    // Two groups of columns a workgroup halve the reads of P; worth it once P has rows to
-    // read, where that leaves two workgroups a compute unit (us, one group against two:
-    // 8-bit 28672x8192 at m = 4 46.5 / 55.9, 16384x4096 at m = 16 19.6 / 16.7, m = 32 28.1 /
-    // 21.4).
-    const bool wide = a.m > 8 && a.n >= 16 * WIDE * 512;
+    // Two groups of columns a workgroup halve the reads of P (the gated product has two as it
+    // is); worth it once P has rows to read, where that leaves two workgroups a compute unit
+    // (us, one group against two: 8-bit 28672x8192 at m = 4 47.2 / 56.1, 16384x4096 at m = 16
+    // 20.9 / 18.8, m = 32 30.1 / 23.9).
+    const bool wide = a.m > 8 && a.n >= 16 * 2 * 512;
     return with_bool(whole, [&](auto al) {
         constexpr bool ALIGNED = decltype(al)::value;
         auto go = [&](auto mi) {
             constexpr int MI = decltype(mi)::value;
-            return wide ? skinny_shape<T, O, MODE, ACT, MI, WIDE, ALIGNED>(a, st)
-                        : skinny_shape<T, O, MODE, ACT, MI, 1, ALIGNED>(a, st);
+            if constexpr (MODE == kInt8)
+                if (wide) return skinny_shape<T, O, MODE, ACT, MI, 2, ALIGNED>(a, st);
+            return skinny_shape<T, O, MODE, ACT, MI, 1, ALIGNED>(a, st);
         };
         if (a.m <= 16) return go(int_c<1>{});
         if (a.m <= 32) return go(int_c<2>{});
