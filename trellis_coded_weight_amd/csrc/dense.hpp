@@ -34,7 +34,7 @@ __device__ __forceinline__ T from_f32(float v)
 }
 
 // v as the sum of two values of T, both of v's sign: hi is the largest one below |v| in
-// magnitude, lo the rest, rounded.  Their sum is within 2^-15 (bf16) or 2^-21 (fp16, and
+// magnitude (in fp16 2^-24 below at least), lo the rest, rounded.  Their sum is within 2^-15 (bf16) or 2^-21 (fp16, and
 // 2^-25 absolute) of v, and a v of up to 131008 stays finite in fp16.  hi stays below |v| also
 // where v itself is a value of T, so that lo is not 0 where hi is not: an infinite factor
 // then gives v's infinity twice and not inf + 0 * inf.  (Not so for |v| under 2^-110 in bf16,
