@@ -486,8 +486,9 @@ size_t qtcq_gated_vjp_workspace_bytes(int M, int F, int K, int whole_rows);
 
 /* Gradients of the gated projections from grad_h = dLoss/dh.  With
  *   d_gate = grad_h up act'(gate),   d_up = grad_h act(gate)
- * in binary32 (act and act' at an infinite gate are their limits there: a gate past the
- * range of dtype was saved as an infinity),
+ * in binary32.  A projection past the range of dtype was saved as an infinity, so infinite
+ * gates and ups count as large finite ones: act and act' are their limits there, and a
+ * grad_h or act' of 0 makes 0 of them.  With these,
  *   grad_x = d_gate w_gate + d_up w_up,  grad_w_gate = d_gate^T x,  grad_w_up = d_up^T x,
  * sums in binary32, each result rounded once to dtype.  For the products d_gate and d_up
  * are held as the sums of two values of dtype each, within 2^-15 (bf16) or 2^-21 (fp16) of

@@ -81,3 +81,40 @@ def test_slopes_at_infinite_gates(api, act, dtype):
     assert gg[0].tolist() == [0.0 if act == "sigmoid" else 1.0] * 8 and gg[1].tolist() == [0.0] * 8
     assert gu[0].tolist() == [top] * 8 and gu[1].tolist() == [0.0] * 8
     assert bool(torch.isfinite(gg[2]).all()) and bool(torch.isnan(gg[3]).all()) and bool(torch.isnan(gu[3]).all())
+
+
+@pytest.mark.parametrize("round_slopes", [False, True])
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+def test_zero_factors_beside_infinite_projections(api, act, dtype, round_slopes):
+    """Masked tokens (grad_h 0) and closed gates (act' 0) whose saved projections are infinite
+    add nothing: the weight gradients are those of the other tokens, bit for bit."""
+    import torch
+    t = getattr(torch, dtype)
+    inf = float("inf")
+    M, F, K = 9, 72, 40
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+
+    def draw(r, c):
+        return torch.randn(r, c, generator=g, device="cuda").to(t)
+
+    x, wg, wu, gate, up, gh = draw(M, K), draw(F, K), draw(F, K), draw(M, F), draw(M, F), draw(M, F)
+    gh[2] = 0                                              # a masked token
+    gate[4] = -1000                                        # a token whose gates are all closed
+    say("zero factors beside infinite projections %s %s" % (act, dtype))
+    kw = dict(activation=act, round_slopes=round_slopes)
+    clean = api.gated_vjp(x, wg, wu, gate, up, gh, **kw)
+    gate[2, ::2], gate[2, 1::2], up[2, ::3], up[2, 1::3] = inf, -inf, inf, -inf
+    up[4, ::2], up[4, 1::2] = -inf, inf
+    got = api.gated_vjp(x, wg, wu, gate, up, gh, **kw)
+    torch.cuda.synchronize()
+    for a, b in zip(got, clean):
+        assert bool(torch.isfinite(b).all()) and torch.equal(a, b)
+    # NaN is not taken away, and neither is an infinite upstream gradient
+    up[4, 5] = float("nan")
+    gh[2, 7] = inf
+    gx, gwg, gwu = api.gated_vjp(x, wg, wu, gate, up, gh, **kw)
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(gx[4]).all()) and bool(torch.isnan(gwg[5]).all())
+    assert not bool(torch.isfinite(gwg[7]).any()) and not bool(torch.isfinite(gx[2]).any())

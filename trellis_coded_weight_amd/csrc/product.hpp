@@ -192,7 +192,9 @@ pad_rows(PadArgs a)
 // that take them next have 16-bit operands, so each is written as two parts (two_parts), or,
 // with one piece, rounded once to the operands' type: its relative 2^-8 (bf16) or 2^-11 (fp16)
 // at most a term adds in squares over a sum, about what the rounding of the gradient itself
-// costs.  d [pieces][2][M][ldd], dgate and dup in the first piece; columns from F to ldd are
+// costs.  An infinite gate or up may be a finite one that T does not hold, saved as such, so
+// an upstream gradient or slope of 0 makes 0 of it and not NaN: a masked token's projections do
+// not reach the gradients of the weights.  d [pieces][2][M][ldd], dgate and dup in the first piece; columns from F to ldd are
 // written as zero.
 //   grid.x = RowGrid{ldd / 8}.blocks(M), block = 256; ldd a multiple of 8.
 template <typename T, int ACT>
@@ -214,7 +216,11 @@ gated_slopes(const T* __restrict__ gate, const T* __restrict__ up, int64_t ldg, 
         float av, dv;
         activate_grad<ACT>((float)g[e], av, dv);
         const float hv = (float)h[e];
-        const float gv = col + e < F ? hv * (float)u[e] * dv : 0.0f, uv = col + e < F ? hv * av : 0.0f;
+        const float up_v = (float)u[e];
+        // beside an infinite projection, which stands for a large finite one, a 0 stays 0
+        const bool gz = col + e >= F || (__builtin_fabsf(up_v) == __builtin_inff() && hv * dv == 0.0f);
+        const bool uz = col + e >= F || (__builtin_fabsf(av) == __builtin_inff() && hv == 0.0f);
+        const float gv = gz ? 0.0f : hv * up_v * dv, uv = uz ? 0.0f : hv * av;
         T hi, lo;
         two_parts(gv, hi, lo);
         dg[e] = pieces == 2 ? hi : from_f32<T>(gv);
