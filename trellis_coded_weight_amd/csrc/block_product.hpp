@@ -143,8 +143,12 @@ __device__ __forceinline__ void block_tile_product(const ProductArgs& a, int b, 
     // for the ones that matter.  It has no output register: the data goes to LDS.
     auto to_lds = [&](u32x4 r, const char* dst, int off) {
         const uint32_t at = (uint32_t)reinterpret_cast<uintptr_t>((lds_char*)dst);
+        // (m0 is a register the compiler does not give to values, which it warns about)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                      ::"s"(at), "v"(off), "s"(r) : "m0", "memory");
+#pragma clang diagnostic pop
     };
     // HR groups of 64 rows (of k) from row0 of `base` [nrows][k] into dst; nothing but zeros
     // if this step is not there
