@@ -513,6 +513,131 @@ qtcq_status qtcq_gated_vjp(const void* x, int64_t ldx, const void* w_gate, const
                            void* grad_w_up, int64_t ldgw, void* workspace, size_t workspace_bytes,
                            void* stream);
 
+/* ---- Model operators on coded weights --------------------------------------------------
+ * What else a model on coded weights runs around the products above: 8-bit floating point
+ * with a scale for each block of 128 (a row of activations with a few large channels keeps
+ * its other channels' digits, which one scale a row does not), the layer norm ahead of the
+ * projections with its gradients, and the loss that trains the weights against the original
+ * model, given by its top logits.
+ *
+ * The rules of the dense operators hold here too (strides, empty sizes, workspaces,
+ * non-finite inputs, determinism, capture).  8-bit floating point is e4m3: a sign, 4 bits of
+ * exponent with bias 7, 3 of mantissa, largest value 448, 0x7F and 0xFF NaN.
+ * A scale matrix has a stride for its rows and one for its columns, in elements.
+ */
+
+/* Rows to e4m3.  block_rows 1: a scale for each 128 columns of a row (the last block may be
+ * shorter), scale [rows][ceil(cols / 128)]; block_rows 128: one for each 128 x 128 elements,
+ * scale [ceil(rows / 128)][ceil(cols / 128)].  A block's scale is fl32(max |x| / 448) and
+ * q is the exact quotient x / scale rounded to the nearest e4m3 value, halves to even.  A
+ * block of zeros (or one so small that its scale underflows to 0) has scale 0 and q 0; a block
+ * that holds an infinity or NaN has scale NaN and q 0.
+ *   x      [rows][cols] of dtype QTCQ_F32, QTCQ_BF16 or QTCQ_F16, row stride ldx
+ *   q      [rows][cols] e4m3 (out), row stride ldq
+ *   scale  float32 (out), block (i, j) at i * scale_row + j * scale_col, no two at one place;
+ *          with scale_row = 1 the scales of adjacent rows lie together, as the product
+ *          reads them fastest
+ * Errors: QTCQ_ERR_INVALID_ARG (negative sizes, strides, NULL or misaligned buffers),
+ * QTCQ_ERR_UNSUPPORTED (dtype, block_rows, sizes), QTCQ_ERR_DEVICE. */
+qtcq_status qtcq_quantize_blocks(const void* x, int dtype, int64_t rows, int cols, int64_t ldx,
+                                 int block_rows, uint8_t* q, int64_t ldq, float* scale,
+                                 int64_t scale_row, int64_t scale_col, void* stream);
+
+/* Product of two e4m3 matrices with such scales, activations a by weights w:
+ *   y[m][n] = sum_b fl32(a_scale[m][b] w_scale[n / 128][b]) sum_{k in block b} a[m][k] w[n][k]
+ * over the blocks b of 128 of k, sums in binary32, rounded once to dtype.
+ *   a  [M][K] e4m3, row stride lda; a_scale [M][ceil(K / 128)], row stride as_row (at most
+ *      2^20) and column stride as_col
+ *   w  [N][K] e4m3, row stride ldw; w_scale [ceil(N / 128)][ceil(K / 128)], strides ws_row,
+ *      ws_col
+ *   y  [M][N] of dtype QTCQ_F32, QTCQ_BF16 or QTCQ_F16 (out), row stride ldy
+ *   K  at most 2^22
+ *   workspace  >= qtcq_matmul_fp8_workspace_bytes(M, N, K, whole_rows)
+ * Errors: QTCQ_ERR_INVALID_ARG (negative sizes or strides, strides below the rows' lengths,
+ * NULL or misaligned buffers), QTCQ_ERR_UNSUPPORTED (dtype, sizes, as_row),
+ * QTCQ_ERR_WORKSPACE (NULL, misaligned or too small for these operands), QTCQ_ERR_DEVICE. */
+size_t qtcq_matmul_fp8_workspace_bytes(int M, int N, int K, int whole_rows);
+qtcq_status qtcq_matmul_fp8(const uint8_t* a, int64_t lda, const float* a_scale, int64_t as_row,
+                            int64_t as_col, const uint8_t* w, int64_t ldw, const float* w_scale,
+                            int64_t ws_row, int64_t ws_col, int M, int N, int K, int dtype, void* y,
+                            int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Layer norm: mean = sum x / cols, rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps),
+ *   y = (x - mean) rstd weight + bias,
+ * in binary32, y rounded once.
+ *   x, y          [rows][cols] of dtype QTCQ_F32, QTCQ_BF16 or QTCQ_F16, row strides ldx, ldy
+ *   weight, bias  [cols] of weight_dtype (dtype or QTCQ_F32), or NULL: ones, zeros
+ *   eps           >= 0
+ *   mean, rstd    [rows] float32 (out) for qtcq_layer_norm_vjp; both or neither NULL
+ * Errors: QTCQ_ERR_INVALID_ARG (negative sizes, strides below cols, eps, NULL or misaligned
+ * buffers, one of mean and rstd NULL), QTCQ_ERR_UNSUPPORTED (types, sizes), QTCQ_ERR_DEVICE. */
+qtcq_status qtcq_layer_norm(const void* x, int dtype, int64_t rows, int cols, int64_t ldx,
+                            const void* weight, const void* bias, int weight_dtype, float eps,
+                            void* y, int64_t ldy, float* mean, float* rstd, void* stream);
+
+/* Its gradients from grad_y = dLoss/dy.  With xh = (x - mean) rstd and gw = grad_y weight,
+ *   grad_x = rstd (gw - sum gw / cols - xh sum(gw xh) / cols),
+ *   grad_weight = sum over rows of grad_y xh,  grad_bias = sum over rows of grad_y,
+ * in binary32, each result rounded once.
+ *   x, dtype, rows, cols, weight, weight_dtype, mean, rstd : as qtcq_layer_norm
+ *   grad_y       [rows][cols] of dtype, row stride ldgy
+ *   grad_x       [rows][cols] of dtype (out), row stride ldgx, or NULL
+ *   grad_weight, grad_bias  [cols] of weight_dtype (out), each may be NULL
+ *   workspace    >= qtcq_layer_norm_vjp_workspace_bytes(rows, cols); not needed where
+ *                grad_weight and grad_bias are both NULL
+ * Errors: as qtcq_layer_norm, and QTCQ_ERR_WORKSPACE. */
+size_t qtcq_layer_norm_vjp_workspace_bytes(int64_t rows, int cols);
+qtcq_status qtcq_layer_norm_vjp(const void* x, int dtype, int64_t rows, int cols, int64_t ldx,
+                                const void* weight, int weight_dtype, const float* mean,
+                                const float* rstd, const void* grad_y, int64_t ldgy, void* grad_x,
+                                int64_t ldgx, void* grad_weight, void* grad_bias, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* Distillation from a teacher's top logits: for each token (row), with logits z, entries
+ * j = 1 .. k of the teacher's logits t_j at vocabulary indices i_j, and temperature T,
+ *   q = softmax(z / T),  p_j = exp(t_j / T) / sum_j exp(t_j / T),
+ *   loss = sum_j p_j (log p_j - log q[i_j]),
+ * and, in the same call where grad_logits is given (the logits are then read once from
+ * memory),
+ *   grad_logits = grad_loss / T (q sum_j p_j - sum_j p_j e[i_j]).
+ * Logits and their softmax in binary32, what concerns the k entries in binary64.  Entries
+ * with an index outside 0 .. vocab - 1 are padding.  An entry with p_j = 0 adds nothing,
+ * whatever q is there; a token whose entries are all padding (or all -infinity) has loss 0
+ * and gradient 0, whatever its logits are.  The same index twice: both entries count.
+ * Logits of -infinity are masked vocabulary: q = 0 there, and an entry with p_j > 0 at one
+ * makes the loss infinite.
+ *   logits   [rows][vocab] of dtype QTCQ_F32, QTCQ_BF16 or QTCQ_F16, row stride ldl
+ *   index    [rows][k] int32 (index_bytes 4) or int64 (8), row stride ldi; k at most 1024
+ *   teacher  [rows][k] of teacher_dtype QTCQ_F32, QTCQ_BF16 or QTCQ_F16, row stride ldt
+ *   temperature    > 0, in 2^-100 .. 2^100
+ *   teacher_log_z  [rows] float32, or NULL.  Given, p_j = exp(t_j / T - teacher_log_z): the
+ *            teacher's probabilities over its whole vocabulary, whose sum over the entries
+ *            may be below 1
+ *   loss     [rows] float32 (out)
+ *   stats    [rows][5] float32 (out) for qtcq_distill_topk_vjp, or NULL
+ *   grad_loss    [rows] float32; read where grad_logits is given
+ *   grad_logits  [rows][vocab] of dtype (out), row stride ldg, or NULL
+ *   workspace    >= qtcq_distill_topk_workspace_bytes(rows, vocab)
+ * Errors: QTCQ_ERR_INVALID_ARG (negative sizes, strides, temperature, NULL or misaligned
+ * buffers), QTCQ_ERR_UNSUPPORTED (types, index_bytes, sizes, temperature),
+ * QTCQ_ERR_WORKSPACE, QTCQ_ERR_DEVICE. */
+size_t qtcq_distill_topk_workspace_bytes(int64_t rows, int vocab);
+qtcq_status qtcq_distill_topk(const void* logits, int dtype, int64_t rows, int vocab, int64_t ldl,
+                              const void* index, int index_bytes, int64_t ldi, const void* teacher,
+                              int teacher_dtype, int64_t ldt, int k, float temperature,
+                              const float* teacher_log_z, float* loss, float* stats,
+                              const float* grad_loss, void* grad_logits, int64_t ldg,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* The gradient alone, for a grad_loss that is known only after the losses: the same bits as
+ * qtcq_distill_topk gives for it.  stats: what that call wrote for the same logits, index,
+ * teacher, teacher_log_z and temperature.  Other arguments and errors as there. */
+qtcq_status qtcq_distill_topk_vjp(const void* logits, int dtype, int64_t rows, int vocab,
+                                  int64_t ldl, const void* index, int index_bytes, int64_t ldi,
+                                  const void* teacher, int teacher_dtype, int64_t ldt, int k,
+                                  float temperature, const float* stats, const float* grad_loss,
+                                  void* grad_logits, int64_t ldg, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -55,6 +55,7 @@ _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
 _sz = ctypes.c_size_t
+_f32 = ctypes.c_float
 _code = ctypes.c_uint64   # qtcq_code descriptor
 
 _SIGS = {
@@ -99,6 +100,21 @@ _SIGS = {
     "qtcq_gated_vjp_workspace_bytes": (_sz, [_int, _int, _int, _int]),
     "qtcq_gated_vjp": (_int, [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _int, _int,
                               _int, _int, _int, _vp, _i64, _vp, _vp, _i64, _vp, _sz, _vp]),
+    "qtcq_quantize_blocks": (_int, [_vp, _int, _i64, _int, _i64, _int, _vp, _i64, _vp, _i64, _i64,
+                                    _vp]),
+    "qtcq_matmul_fp8_workspace_bytes": (_sz, [_int, _int, _int, _int]),
+    "qtcq_matmul_fp8": (_int, [_vp, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _int, _int,
+                               _int, _int, _vp, _i64, _vp, _sz, _vp]),
+    "qtcq_layer_norm": (_int, [_vp, _int, _i64, _int, _i64, _vp, _vp, _int, _f32, _vp, _i64, _vp,
+                               _vp, _vp]),
+    "qtcq_layer_norm_vjp_workspace_bytes": (_sz, [_i64, _int]),
+    "qtcq_layer_norm_vjp": (_int, [_vp, _int, _i64, _int, _i64, _vp, _int, _vp, _vp, _vp, _i64, _vp,
+                                   _i64, _vp, _vp, _vp, _sz, _vp]),
+    "qtcq_distill_topk_workspace_bytes": (_sz, [_i64, _int]),
+    "qtcq_distill_topk": (_int, [_vp, _int, _i64, _int, _i64, _vp, _int, _i64, _vp, _int, _i64, _int,
+                                 _f32, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _sz, _vp]),
+    "qtcq_distill_topk_vjp": (_int, [_vp, _int, _i64, _int, _i64, _vp, _int, _i64, _vp, _int, _i64,
+                                     _int, _f32, _vp, _vp, _vp, _i64, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -311,3 +327,66 @@ def qtcq_gated_vjp(x, ldx: int, w_gate, w_up, ldw: int, gate: int, up: int, ldg:
                                ldg, grad_h, ldgh, dtype, M, F, K, activation, grad_x,
                                ldgx, grad_w_gate, grad_w_up, ldgw, workspace,
                                workspace_bytes, stream), "qtcq_gated_vjp")
+
+
+def qtcq_quantize_blocks(x: int, dtype: int, rows: int, cols: int, ldx: int, block_rows: int,
+                         q: int, ldq: int, scale: int, scale_row: int, scale_col: int,
+                         stream: int = 0) -> None:
+    _check(_lib.qtcq_quantize_blocks(x, dtype, rows, cols, ldx, block_rows, q, ldq, scale,
+                                     scale_row, scale_col, stream), "qtcq_quantize_blocks")
+
+
+def qtcq_matmul_fp8_workspace_bytes(M: int, N: int, K: int, whole_rows: bool) -> int:
+    return _lib.qtcq_matmul_fp8_workspace_bytes(M, N, K, 1 if whole_rows else 0)
+
+
+def qtcq_matmul_fp8(a: int, lda: int, a_scale: int, as_row: int, as_col: int, w: int, ldw: int,
+                    w_scale: int, ws_row: int, ws_col: int, M: int, N: int, K: int, dtype: int,
+                    y: int, ldy: int, workspace, workspace_bytes: int, stream: int = 0) -> None:
+    _check(_lib.qtcq_matmul_fp8(a, lda, a_scale, as_row, as_col, w, ldw, w_scale, ws_row, ws_col,
+                                M, N, K, dtype, y, ldy, workspace, workspace_bytes, stream),
+           "qtcq_matmul_fp8")
+
+
+def qtcq_layer_norm(x: int, dtype: int, rows: int, cols: int, ldx: int, weight, bias,
+                    weight_dtype: int, eps: float, y: int, ldy: int, mean, rstd,
+                    stream: int = 0) -> None:
+    _check(_lib.qtcq_layer_norm(x, dtype, rows, cols, ldx, weight, bias, weight_dtype, eps, y, ldy,
+                                mean, rstd, stream), "qtcq_layer_norm")
+
+
+def qtcq_layer_norm_vjp_workspace_bytes(rows: int, cols: int) -> int:
+    return _lib.qtcq_layer_norm_vjp_workspace_bytes(rows, cols)
+
+
+def qtcq_layer_norm_vjp(x: int, dtype: int, rows: int, cols: int, ldx: int, weight,
+                        weight_dtype: int, mean: int, rstd: int, grad_y: int, ldgy: int, grad_x,
+                        ldgx: int, grad_weight, grad_bias, workspace, workspace_bytes: int,
+                        stream: int = 0) -> None:
+    _check(_lib.qtcq_layer_norm_vjp(x, dtype, rows, cols, ldx, weight, weight_dtype, mean, rstd,
+                                    grad_y, ldgy, grad_x, ldgx, grad_weight, grad_bias, workspace,
+                                    workspace_bytes, stream), "qtcq_layer_norm_vjp")
+
+
+def qtcq_distill_topk_workspace_bytes(rows: int, vocab: int) -> int:
+    return _lib.qtcq_distill_topk_workspace_bytes(rows, vocab)
+
+
+def qtcq_distill_topk(logits: int, dtype: int, rows: int, vocab: int, ldl: int, index: int,
+                      index_bytes: int, ldi: int, teacher: int, teacher_dtype: int, ldt: int,
+                      k: int, temperature: float, teacher_log_z, loss: int, stats, grad_loss,
+                      grad_logits, ldg: int, workspace, workspace_bytes: int,
+                      stream: int = 0) -> None:
+    _check(_lib.qtcq_distill_topk(logits, dtype, rows, vocab, ldl, index, index_bytes, ldi, teacher,
+                                  teacher_dtype, ldt, k, temperature, teacher_log_z, loss, stats,
+                                  grad_loss, grad_logits, ldg, workspace, workspace_bytes, stream),
+           "qtcq_distill_topk")
+
+
+def qtcq_distill_topk_vjp(logits: int, dtype: int, rows: int, vocab: int, ldl: int, index: int,
+                          index_bytes: int, ldi: int, teacher: int, teacher_dtype: int, ldt: int,
+                          k: int, temperature: float, stats: int, grad_loss: int, grad_logits: int,
+                          ldg: int, stream: int = 0) -> None:
+    _check(_lib.qtcq_distill_topk_vjp(logits, dtype, rows, vocab, ldl, index, index_bytes, ldi,
+                                      teacher, teacher_dtype, ldt, k, temperature, stats, grad_loss,
+                                      grad_logits, ldg, stream), "qtcq_distill_topk_vjp")

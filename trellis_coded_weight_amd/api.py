@@ -2,7 +2,7 @@
 CUDA (HIP) tensors and calls the entry points on the current stream.  Only argument
 marshalling happens here; every step of the path runs in the HIP kernels.  Autograd
 records none of these calls: gradients come from the calls that compute them (bcjr_vjp,
-gated_vjp).
+gated_vjp, layer_norm_vjp, distill_topk, distill_topk_vjp).
 """
 from __future__ import annotations
 
@@ -610,3 +610,227 @@ def gated_vjp(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, gate: t
                        None if grad_wu is None else grad_wu.data_ptr(), K, ws, ws_bytes,
                        _stream(dev))
     return grad_x, grad_wg, grad_wu
+
+
+# ---- model operators on coded weights ---------------------------------------------------
+
+FLOATS = (torch.float32, torch.bfloat16, torch.float16)
+
+
+def _not_recorded(name: str, *tensors) -> None:
+    """Autograd does not see the calls, so inputs that require gradients are refused while it
+    records."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError("%s does not record gradients: call it under torch.no_grad() or with "
+                         "detached inputs, and its vjp for the gradients" % name)
+
+
+def _vector(x, name: str, dtypes, n: int, device: int):
+    """An optional contiguous device vector of n values: its pointer, or None."""
+    if x is None:
+        return None
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dim() == 1 and x.dtype in dtypes
+            and x.shape[0] == n and x.is_contiguous()):
+        raise ValueError("%s must be a contiguous device tensor of %d values in %s"
+                         % (name, n, " or ".join(str(d) for d in dtypes)))
+    if x.get_device() != device:
+        _on_current_device(x, name)
+    return x.data_ptr()
+
+
+def _block_scales(s: torch.Tensor, name: str, shape, device: int):
+    """A matrix of block scales with any strides, broadcast ones too.  Returns both strides."""
+    if not (isinstance(s, torch.Tensor) and s.is_cuda and s.dtype == torch.float32
+            and tuple(s.shape) == shape):
+        raise ValueError("%s must be a float32 device tensor of %s" % (name, list(shape)))
+    if s.get_device() != device:
+        _on_current_device(s, name)
+    return s.stride(0) if shape[0] > 1 else 0, s.stride(1) if shape[1] > 1 else 0
+
+
+def quantize_blocks(x: torch.Tensor, block_rows: int = 1):
+    """Rows of x ([R][C] float32, bfloat16 or float16) to 8-bit floating point with a float32
+    scale for each block: block_rows = 1, of 128 columns of a row (activations), block_rows =
+    128, of 128 x 128 elements (weights).  Returns (q [R][C] float8_e4m3fn, scale
+    [R or ceil(R / 128)][ceil(C / 128)]); x is about q times its block's scale.  The scales
+    of rows lie together (scale.t() is contiguous), as matmul_fp8 reads them fastest."""
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    dev = torch.cuda.current_device()
+    ldx = _rows(x, "x", FLOATS, dev)
+    R, C = x.shape
+    q = x.new_empty((R, C), dtype=torch.float8_e4m3fn)
+    down = R if block_rows == 1 else (R + 127) // 128
+    scale = x.new_empty(((C + 127) // 128, down), dtype=torch.float32)
+    nat.qtcq_quantize_blocks(x.data_ptr(), DTYPES[x.dtype], R, C, ldx, block_rows, q.data_ptr(), C,
+                             scale.data_ptr(), 1, down, _stream(dev))
+    return q, scale.t()
+
+
+def matmul_fp8_workspace(M: int, N: int, K: int, whole_rows: bool = False) -> torch.Tensor:
+    """Device scratch for matmul_fp8 (reusable across calls on one stream).  whole_rows:
+    the rows of a and w start on 16 bytes and are a multiple of 16 bytes long."""
+    return torch.empty(nat.qtcq_matmul_fp8_workspace_bytes(M, N, K, whole_rows),
+                       dtype=torch.uint8, device="cuda")
+
+
+def matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+               dtype: torch.dtype = torch.float32,
+               workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y [M][N] = a w^T for a [M][K] and w [N][K] float8_e4m3fn with the scales of
+    quantize_blocks: a_scale [M][ceil(K / 128)] (block_rows = 1) and w_scale [ceil(N / 128)]
+    [ceil(K / 128)] (block_rows = 128), with any strides.  Sums in float32; dtype float32,
+    bfloat16 or float16; `workspace` (matmul_fp8_workspace(M, N, K)) is allocated when not
+    given and needed."""
+    if dtype not in FLOATS:
+        raise ValueError("dtype must be float32, bfloat16 or float16")
+    dev = torch.cuda.current_device()
+    lda = _rows(a, "a", (torch.float8_e4m3fn,), dev)
+    ldw = _rows(w, "w", (torch.float8_e4m3fn,), dev)
+    (M, K), N = a.shape, w.shape[0]
+    if w.shape[1] != K:
+        raise ValueError("w must have the columns of a")
+    kb = (K + 127) // 128
+    as_row, as_col = _block_scales(a_scale, "a_scale", (M, kb), dev)
+    ws_row, ws_col = _block_scales(w_scale, "w_scale", ((N + 127) // 128, kb), dev)
+    ap, wp = a.data_ptr(), w.data_ptr()
+    need = nat.qtcq_matmul_fp8_workspace_bytes(M, N, K, _whole_rows(ap | wp, K, 1, lda, ldw))
+    _keep, ws, ws_bytes = _workspace(workspace, need, a)
+    y = a.new_empty((M, N), dtype=dtype)
+    nat.qtcq_matmul_fp8(ap, lda, a_scale.data_ptr(), as_row, as_col, wp, ldw, w_scale.data_ptr(),
+                        ws_row, ws_col, M, N, K, DTYPES[dtype], y.data_ptr(), N, ws, ws_bytes,
+                        _stream(dev))
+    return y
+
+
+def _norm_weights(x, weight, bias, dev):
+    """(pointers of weight and bias, their dtype): float32 or the dtype of x, both the same."""
+    dtype = x.dtype if weight is None and bias is None else (bias if weight is None else weight).dtype
+    kinds = (dtype,) if dtype in (torch.float32, x.dtype) else (torch.float32, x.dtype)
+    return (_vector(weight, "weight", kinds, x.shape[1], dev),
+            _vector(bias, "bias", kinds, x.shape[1], dev), dtype)
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
+               bias: torch.Tensor | None = None, eps: float = 1e-5, save: bool = False):
+    """y = (x - mean) rstd weight + bias over the columns of x ([R][C] float32, bfloat16 or
+    float16), with the mean of each row and rstd = 1 / sqrt(its variance + eps), in float32.
+    weight and bias [C] are float32 or of the dtype of x (None: ones, zeros).  With save,
+    returns (y, mean [R], rstd [R]) for layer_norm_vjp."""
+    if not eps >= 0:
+        raise ValueError("eps must not be negative")
+    dev = torch.cuda.current_device()
+    ldx = _rows(x, "x", FLOATS, dev)
+    wp, bp, wt = _norm_weights(x, weight, bias, dev)
+    _not_recorded("layer_norm", x, weight, bias)
+    R, C = x.shape
+    y = x.new_empty((R, C))
+    mean, rstd = (x.new_empty(R, dtype=torch.float32), x.new_empty(R, dtype=torch.float32)) if save else (None, None)
+    nat.qtcq_layer_norm(x.data_ptr(), DTYPES[x.dtype], R, C, ldx, wp, bp, DTYPES[wt], eps,
+                        y.data_ptr(), C, mean.data_ptr() if save else None,
+                        rstd.data_ptr() if save else None, _stream(dev))
+    return (y, mean, rstd) if save else y
+
+
+def layer_norm_vjp_workspace(R: int, C: int) -> torch.Tensor:
+    """Device scratch for layer_norm_vjp (reusable across calls on one stream)."""
+    return torch.empty(nat.qtcq_layer_norm_vjp_workspace_bytes(R, C), dtype=torch.uint8,
+                       device="cuda")
+
+
+def layer_norm_vjp(x: torch.Tensor, weight: torch.Tensor | None, mean: torch.Tensor,
+                   rstd: torch.Tensor, grad_y: torch.Tensor, want_x: bool = True,
+                   want_w: bool = True, workspace: torch.Tensor | None = None):
+    """Gradients of sum(grad_y * y) for y of layer_norm(x, weight, bias), with the mean and
+    rstd that it saved.  Returns (grad_x [R][C], grad_weight [C], grad_bias [C]), None where
+    not wanted; the last two in the dtype of weight (of x where weight is None).  `workspace`
+    (layer_norm_vjp_workspace(R, C)) is allocated when not given and needed."""
+    dev = torch.cuda.current_device()
+    ldx = _rows(x, "x", FLOATS, dev)
+    ldgy = _rows(grad_y, "grad_y", (x.dtype,), dev, x.shape)
+    wp, _, wt = _norm_weights(x, weight, None, dev)
+    R, C = x.shape
+    mp = _vector(mean, "mean", (torch.float32,), R, dev)
+    rp = _vector(rstd, "rstd", (torch.float32,), R, dev)
+    if mp is None or rp is None:
+        raise ValueError("mean and rstd are those that layer_norm saved")
+    need = nat.qtcq_layer_norm_vjp_workspace_bytes(R, C) if want_w else 0
+    _keep, ws, ws_bytes = _workspace(workspace, need, x)
+    grad_x = x.new_empty((R, C)) if want_x else None
+    grad_w, grad_b = (x.new_empty(C, dtype=wt), x.new_empty(C, dtype=wt)) if want_w else (None, None)
+    nat.qtcq_layer_norm_vjp(x.data_ptr(), DTYPES[x.dtype], R, C, ldx, wp, DTYPES[wt], mp, rp,
+                            grad_y.data_ptr(), ldgy, grad_x.data_ptr() if want_x else None, C,
+                            grad_w.data_ptr() if want_w else None,
+                            grad_b.data_ptr() if want_w else None, ws, ws_bytes, _stream(dev))
+    return grad_x, grad_w, grad_b
+
+
+def _distill_inputs(logits, index, teacher, temperature, dev):
+    """(row strides of logits, index and teacher)"""
+    if not 2.0 ** -100 <= temperature <= 2.0 ** 100:
+        raise ValueError("temperature must be positive, from 2^-100 to 2^100")
+    ldl = _rows(logits, "logits", FLOATS, dev)
+    ldi = _rows(index, "index", (torch.int64, torch.int32), dev)
+    if index.shape[0] != logits.shape[0]:
+        raise ValueError("index must have the rows of logits")
+    return ldl, ldi, _rows(teacher, "teacher", FLOATS, dev, index.shape)
+
+
+def distill_topk_workspace(R: int, V: int) -> torch.Tensor:
+    """Device scratch for distill_topk (reusable across calls on one stream)."""
+    return torch.empty(nat.qtcq_distill_topk_workspace_bytes(R, V), dtype=torch.uint8, device="cuda")
+
+
+def distill_topk(logits: torch.Tensor, index: torch.Tensor, teacher: torch.Tensor,
+                 temperature: float = 1.0, teacher_log_z: torch.Tensor | None = None,
+                 grad_loss: torch.Tensor | None = None, save: bool = False,
+                 workspace: torch.Tensor | None = None):
+    """loss [R] = sum_j p_j (log p_j - log q[index_j]) of each row of logits ([R][V] float32,
+    bfloat16 or float16), q = softmax(logits / temperature) and p = softmax(teacher /
+    temperature) over the teacher's top logits [R][k] at the vocabulary entries index [R][k]
+    (int64 or int32; one outside 0 .. V - 1 is padding; k at most 1024).  With teacher_log_z
+    [R] (float32), p = exp(teacher / temperature - teacher_log_z): the teacher's probabilities
+    over its whole vocabulary.
+
+    With grad_loss [R] (float32: what each loss weighs in the total, 0 for tokens without
+    one), returns (loss, grad_logits): the gradient of sum(grad_loss * loss) in the same pass.
+    Otherwise, with save, returns (loss, stats) for distill_topk_vjp.  `workspace`
+    (distill_topk_workspace(R, V)) is allocated when not given and needed."""
+    if grad_loss is not None and save:
+        raise ValueError("save is for distill_topk_vjp: not with grad_loss")
+    dev = torch.cuda.current_device()
+    ldl, ldi, ldt = _distill_inputs(logits, index, teacher, temperature, dev)
+    _not_recorded("distill_topk", logits, teacher, teacher_log_z)
+    (R, V), k = logits.shape, index.shape[1]
+    zp = _vector(teacher_log_z, "teacher_log_z", (torch.float32,), R, dev)
+    gp = _vector(grad_loss, "grad_loss", (torch.float32,), R, dev)
+    _keep, ws, ws_bytes = _workspace(workspace, nat.qtcq_distill_topk_workspace_bytes(R, V), logits)
+    loss = logits.new_empty(R, dtype=torch.float32)
+    stats = logits.new_empty((R, 5), dtype=torch.float32) if save else None
+    grad = logits.new_empty((R, V)) if grad_loss is not None else None
+    nat.qtcq_distill_topk(logits.data_ptr(), DTYPES[logits.dtype], R, V, ldl, index.data_ptr(),
+                          index.element_size(), ldi, teacher.data_ptr(), DTYPES[teacher.dtype], ldt,
+                          k, temperature, zp, loss.data_ptr(), stats.data_ptr() if save else None,
+                          gp, grad.data_ptr() if grad is not None else None, V, ws, ws_bytes,
+                          _stream(dev))
+    return (loss, stats) if save else loss if grad is None else (loss, grad)
+
+
+def distill_topk_vjp(logits: torch.Tensor, index: torch.Tensor, teacher: torch.Tensor,
+                     stats: torch.Tensor, grad_loss: torch.Tensor,
+                     temperature: float = 1.0) -> torch.Tensor:
+    """The gradient of sum(grad_loss * loss) with respect to the logits, for the loss of
+    distill_topk and the stats that it saved for the same inputs: for a grad_loss [R]
+    (float32) that is known only after the losses."""
+    dev = torch.cuda.current_device()
+    ldl, ldi, ldt = _distill_inputs(logits, index, teacher, temperature, dev)
+    (R, V), k = logits.shape, index.shape[1]
+    gp = _vector(grad_loss, "grad_loss", (torch.float32,), R, dev)
+    if gp is None or not (isinstance(stats, torch.Tensor) and stats.shape == (R, 5)):
+        raise ValueError("stats are those that distill_topk saved, grad_loss a value a row")
+    sp = _vector(stats.view(-1), "stats", (torch.float32,), R * 5, dev)
+    grad = logits.new_empty((R, V))
+    nat.qtcq_distill_topk_vjp(logits.data_ptr(), DTYPES[logits.dtype], R, V, ldl, index.data_ptr(),
+                              index.element_size(), ldi, teacher.data_ptr(), DTYPES[teacher.dtype],
+                              ldt, k, temperature, sp, gp, grad.data_ptr(), V, _stream(dev))
+    return grad

@@ -1,0 +1,129 @@
+// fp8_skinny.hpp -- the product of e4m3 matrices for few rows of activations, where reading
+// the weights once is the work, gfx950.
+//
+// A workgroup of 8 waves takes 16 MI rows of a and NJ groups of 16 rows of w; its waves share
+// k: wave v takes the blocks v, v + 8, ... of 128 bytes of every row.  Operands go from memory
+// to registers in the matrix instruction's layout with no LDS and no barrier on the way, DEPTH
+// blocks in flight a wave, a block's scales with it.  The waves' sums are added in wave order
+// through LDS.
+//
+// ALIGNED: rows start on 16 bytes and are whole chunks; buffer loads whose range check returns
+// zeros past the matrices.  Otherwise rows past the last are read as the last one (their
+// results are not stored), and the last block of k is loaded with its end guarded.
+#pragma once
+
+#include "fp8_product.hpp"
+
+namespace qtcq {
+
+struct Fp8SkinnyShape {
+    static constexpr int kThreads = 512;
+    static constexpr int kWaves = kThreads / 64;
+};
+
+// grid = (ceil(n / (16 NJ)), ceil(m / (16 MI))), block = 512
+template <typename O, int MI, int NJ, int DEPTH, bool ALIGNED>
+__global__ void __launch_bounds__(Fp8SkinnyShape::kThreads)
+fp8_skinny_product(Fp8Args a)
+{
+    constexpr int NW = Fp8SkinnyShape::kWaves, F = MI * NJ;
+    static_assert(F <= NW, "a wave finishes one fragment");
+    __shared__ f32x4 red[NW][F][64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int i0 = blockIdx.y * 16 * MI, j0 = blockIdx.x * 16 * NJ;
+    const int r = lane & 15, c = lane >> 4;
+    const int nblk = (a.k + 127) / 128;
+
+    __amdgpu_buffer_rsrc_t ra, rw;
+    if constexpr (ALIGNED) {
+        // both end with their matrix
+        auto rsrc = [&](const uint8_t* p, int64_t ld, int row0, int nrows, int rows) {
+            const int n = nrows - row0 < rows ? nrows - row0 : rows;
+            return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p + row0 * ld), (short)0,
+                                                     n > 0 ? (n - 1) * (int)ld + a.k : 0, kRawBufferWord3);
+        };
+        ra = rsrc(a.a, a.lda, i0, a.m, 16 * MI);
+        rw = rsrc(a.w, a.ldw, j0, a.n, 16 * NJ);
+    }
+    struct Set { u32x4 p[2][MI], q[2][NJ]; float s[MI]; float t; };
+    auto load = [&](int blk, Set& o) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int at = blk * 128 + 64 * h + 16 * c;
+            if constexpr (ALIGNED) {
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+                    o.q[h][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                        rw, at < a.k ? (r + 16 * j) * (int)a.ldw + at : 0x7FFFFFFF, 0, 0));
+#pragma unroll
+                for (int i = 0; i < MI; ++i)
+                    o.p[h][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                        ra, at < a.k ? (r + 16 * i) * (int)a.lda + at : 0x7FFFFFFF, 0, 0));
+            } else {
+                auto chunk = [&](const uint8_t* base, int64_t ld, int row, int nrows) {
+                    const uint8_t* p = base + (int64_t)(row < nrows ? row : nrows - 1) * ld;
+                    return (blk + 1) * 128 <= a.k ? load_loose(p + at) : at < a.k ? load_chunk<uint8_t>(p, at, a.k)
+                                                                                  : u32x4{0u, 0u, 0u, 0u};
+                };
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) o.q[h][j] = chunk(a.w, a.ldw, j0 + 16 * j + r, a.n);
+#pragma unroll
+                for (int i = 0; i < MI; ++i) o.p[h][i] = chunk(a.a, a.lda, i0 + 16 * i + r, a.m);
+            }
+        }
+        // a block past the last: scales of 0, so that nothing is added
+        const bool there = blk < nblk;
+        const int b = there ? blk : 0;
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const int row = i0 + 16 * i + r < a.m ? i0 + 16 * i + r : a.m - 1;
+            const float s = a.a_scale[row * a.as_row + b * a.as_col];
+            o.s[i] = there ? s : 0.0f;
+        }
+        const float t = a.w_scale[(j0 >> 7) * a.ws_row + b * a.ws_col];
+        o.t = there ? t : 0.0f;
+    };
+    f32x4 acc[MI][NJ] = {};
+    auto multiply = [&](const Set& o) {
+        typedef BlockOperand<false> Op;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const Op q(o.q[0][j], o.q[1][j]);
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                const float f = o.s[i] * o.t;
+                const f32x4 t = Op::mul(q, Op(o.p[0][i], o.p[1][i]));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(t[e], f, acc[i][j][e]);
+            }
+        }
+    };
+    if (wave < nblk) {
+        Set set[DEPTH];
+#pragma unroll
+        for (int d = 0; d < DEPTH - 1; ++d) load(wave + d * NW, set[d]);
+        for (int b = wave; b < nblk; b += DEPTH * NW) {
+#pragma unroll
+            for (int d = 0; d < DEPTH; ++d) {
+                load(b + (d + DEPTH - 1) * NW, set[(d + DEPTH - 1) % DEPTH]);
+                multiply(set[d]);
+            }
+        }
+    }
+#pragma unroll
+    for (int f = 0; f < F; ++f) red[wave][f][lane] = acc[f / NJ][f % NJ];
+    __syncthreads();
+    if (wave < F) {
+        f32x4 s = red[0][wave][lane];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) s += red[w][wave][lane];
+        const int row = i0 + wave / NJ * 16 + r, col = j0 + wave % NJ * 16 + 4 * c;
+        if (row < a.m && col < a.n) {
+            const float v[4] = {s[0], s[1], s[2], s[3]};
+            store4(static_cast<O*>(a.y) + (int64_t)row * a.ldy + col, v, a.n - col);
+        }
+    }
+}
+
+}  // namespace qtcq

@@ -1,0 +1,86 @@
+// launch_distill.hip -- launches of the distillation loss and its gradient (distill.hpp).
+#include "model_host.hpp"
+#include "distill.hpp"
+
+namespace qtcq {
+namespace host {
+namespace {
+
+constexpr int kThreads = 1024;
+
+// Segments of a row: enough for two workgroups a compute unit, of at least 8192 elements.
+void cut_row(DistillArgs& a)
+{
+    const int64_t want = a.rows > 0 ? (2 * kComputeUnits + a.rows - 1) / a.rows : 1;
+    const int64_t most = (a.vocab + 8191) / 8192;
+    const int64_t n = want < most ? want : most;
+    if (n < 2) {
+        a.segments = 1;
+        a.segment = a.vocab;
+        return;
+    }
+    a.segment = (int)((a.vocab + n - 1) / n + 7) / 8 * 8;
+    a.segments = (a.vocab + a.segment - 1) / a.segment;
+}
+
+unsigned capped(int64_t n) { return (unsigned)(n < (1 << 20) ? n : 1 << 20); }
+
+template <typename T>
+qtcq_status grad_impl(const DistillArgs& a, hipStream_t st)
+{
+    hipLaunchKernelGGL((distill_grad<T, kThreads>), dim3(capped(a.rows * a.segments)), dim3(kThreads), 0, st, a);
+    return launch_status();
+}
+
+template <typename T>
+qtcq_status distill_impl(const DistillArgs& a, hipStream_t st)
+{
+    if (a.segments == 1) {
+        if (a.grad)
+            hipLaunchKernelGGL((distill_rows<T, kThreads, true>), dim3(capped(a.rows)), dim3(kThreads), 0, st, a);
+        else
+            hipLaunchKernelGGL((distill_rows<T, kThreads, false>), dim3(capped(a.rows)), dim3(kThreads), 0, st, a);
+        return launch_status();
+    }
+    hipLaunchKernelGGL((distill_partial<T, kThreads>), dim3((unsigned)(a.rows * a.segments)), dim3(kThreads), 0, st, a);
+    hipLaunchKernelGGL((distill_join<T, 256>), dim3((unsigned)a.rows), dim3(256), 0, st, a);
+    return a.grad ? grad_impl<T>(a, st) : launch_status();
+}
+
+}  // namespace
+
+size_t distill_workspace_bytes(int64_t rows, int vocab)
+{
+    DistillArgs a = {};
+    a.rows = rows;
+    a.vocab = vocab;
+    cut_row(a);
+    return a.segments == 1 ? 0 : round256((size_t)rows * a.segments * 8) + round256((size_t)rows * kDistillStats * 4);
+}
+
+qtcq_status launch_distill(DistillArgs a, int dtype, void* ws, hipStream_t st)
+{
+    cut_row(a);
+    a.part = static_cast<float*>(ws);
+    // the gradient's launch reads the statistics
+    if (a.segments > 1 && !a.stats)
+        a.stats = reinterpret_cast<float*>(static_cast<char*>(ws) + round256((size_t)a.rows * a.segments * 8));
+    switch (dtype) {
+    case QTCQ_BF16: return distill_impl<__bf16>(a, st);
+    case QTCQ_F16: return distill_impl<_Float16>(a, st);
+    default: return distill_impl<float>(a, st);
+    }
+}
+
+qtcq_status launch_distill_grad(DistillArgs a, int dtype, hipStream_t st)
+{
+    cut_row(a);
+    switch (dtype) {
+    case QTCQ_BF16: return grad_impl<__bf16>(a, st);
+    case QTCQ_F16: return grad_impl<_Float16>(a, st);
+    default: return grad_impl<float>(a, st);
+    }
+}
+
+}  // namespace host
+}  // namespace qtcq

@@ -18,6 +18,7 @@
 
 #include "codes.hpp"
 #include "dense.hpp"
+#include "reduce.hpp"
 
 namespace qtcq {
 
@@ -98,28 +99,6 @@ __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, ui
 {
     const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0C0C0400u), hi = __builtin_amdgcn_perm(d, c, 0x04000C0Cu);
     return lo | hi;
-}
-
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu; }
-
-// Largest of m over the wave's 64 lanes.
-__device__ __forceinline__ uint32_t wave_max(uint32_t m)
-{
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-        const uint32_t v = (uint32_t)__shfl_xor((int)m, o, 64);
-        m = v > m ? v : m;
-    }
-    return m;
-}
-
-// The larger of |x| over both halves of 16-bit pairs, as 16-bit patterns (an infinity or NaN
-// is above every finite value).
-__device__ __forceinline__ uint32_t pair_max(uint32_t m, uint32_t pair)
-{
-    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, m),
-                                                                  __builtin_bit_cast(u16x2, pair & 0x7FFF7FFFu)));
 }
 
 struct QuantShape {
