@@ -546,15 +546,14 @@ qtcq_status qtcq_quantize_blocks(const void* x, int dtype, int64_t rows, int col
 /* Product of two e4m3 matrices with such scales, activations a by weights w:
  *   y[m][n] = sum_b fl32(a_scale[m][b] w_scale[n / 128][b]) sum_{k in block b} a[m][k] w[n][k]
  * over the blocks b of 128 of k, sums in binary32, rounded once to dtype.
- *   a  [M][K] e4m3, row stride lda; a_scale [M][ceil(K / 128)], row stride as_row (at most
- *      2^20) and column stride as_col
- *   w  [N][K] e4m3, row stride ldw; w_scale [ceil(N / 128)][ceil(K / 128)], strides ws_row,
- *      ws_col
+ *   a  [M][K] e4m3, row stride lda; a_scale [M][ceil(K / 128)], strides as_row and as_col
+ *   w  [N][K] e4m3, row stride ldw; w_scale [ceil(N / 128)][ceil(K / 128)], strides ws_row
+ *      and ws_col; as_row and ws_row at most 2^20
  *   y  [M][N] of dtype QTCQ_F32, QTCQ_BF16 or QTCQ_F16 (out), row stride ldy
  *   K  at most 2^22
  *   workspace  >= qtcq_matmul_fp8_workspace_bytes(M, N, K, whole_rows)
  * Errors: QTCQ_ERR_INVALID_ARG (negative sizes or strides, strides below the rows' lengths,
- * NULL or misaligned buffers), QTCQ_ERR_UNSUPPORTED (dtype, sizes, as_row),
+ * NULL or misaligned buffers), QTCQ_ERR_UNSUPPORTED (dtype, sizes, as_row, ws_row),
  * QTCQ_ERR_WORKSPACE (NULL, misaligned or too small for these operands), QTCQ_ERR_DEVICE. */
 size_t qtcq_matmul_fp8_workspace_bytes(int M, int N, int K, int whole_rows);
 qtcq_status qtcq_matmul_fp8(const uint8_t* a, int64_t lda, const float* a_scale, int64_t as_row,

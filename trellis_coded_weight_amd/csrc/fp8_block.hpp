@@ -1,0 +1,236 @@
+// fp8_block.hpp -- the product of e4m3 matrices with block scales for any number of rows, in
+// workgroup tiles of 32 FP x 256 (FP = 8, 4, 2), for operands whose rows start on 16 bytes and
+// hold whole 16-byte chunks, gfx950.
+//
+// Eight waves, 2 x 4, each 16 FP rows of a by 64 rows of w.  A step is one block of 128 of k.
+// Its tiles (a's 4 FP KB, w's 32 KB) and its scales go from memory straight to LDS, into a ring
+// of 2 (FP = 8) or 3 places, so the next one or two steps are on their way during a step.
+// LDS rows are 128 bytes, their 16-byte chunk c at place c ^ ((row >> 1) & 7): the 16 lanes
+// that read one chunk of 16 rows at once touch 16 different places of the 256-byte bank row.
+//
+// Within a step a wave holds its four groups of 16 rows of w in registers and takes its rows of
+// a two groups at a time, the next two on their way from LDS meanwhile.  Before the last two
+// all reads of the step are done: wait until the next step has landed, barrier, start the
+// loads of a later step into the places just left; then the last two groups go through w's
+// four one by one, each of which is replaced by the next step's as it is done with.
+//
+// A block's sums must be scaled before they are added to the result's, which are therefore
+// ordinary vector registers: one fused multiply-add an element and block beside the matrix
+// instructions (four after each).
+//
+// Where tiles are fewer than the compute units, k is cut into shares; each writes its sums in
+// 32 bits, and join_shares adds them in order.
+#pragma once
+
+#include <type_traits>
+
+#include "block_product.hpp"
+#include "fp8_product.hpp"
+
+namespace qtcq {
+
+struct Fp8Shape {
+    static constexpr int kThreads = 512;
+    static constexpr int kCols = 256;
+    static constexpr int kScales = 2048;      // bytes of a step's scales: 64 floats a wave
+    static constexpr int rows(int fp) { return 32 * fp; }
+    static constexpr int places(int fp) { return fp == 8 ? 2 : 3; }
+    static constexpr int step_bytes(int fp) { return (rows(fp) + kCols) * 128 + kScales; }
+};
+
+// grid.x = shares * tiles, block = 512
+template <typename O, int FP, bool FAST>
+__global__ void __launch_bounds__(Fp8Shape::kThreads)
+fp8_block_product(Fp8Args a)
+{
+    typedef BlockOperand<FAST> Op;
+    constexpr int ROWS = Fp8Shape::rows(FP), R = Fp8Shape::places(FP), STEP = Fp8Shape::step_bytes(FP);
+    constexpr int TP = ROWS * 128, TQ = Fp8Shape::kCols * 128;
+    constexpr int LP = FP / 2, LQ = 4, LOADS = LP + LQ + 1;      // loads of a step by one wave
+    constexpr int PAIRS = FP / 2;
+    __shared__ __align__(1024) char lds[R * STEP];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 2, wn = wave & 3;
+    int share, ti, tj;
+    block_tile(blockIdx.x, a.shares, (a.m + ROWS - 1) / ROWS, (a.n + Fp8Shape::kCols - 1) / Fp8Shape::kCols, share, ti, tj);
+    const int i0 = ti * ROWS, j0 = tj * Fp8Shape::kCols;
+    const int steps = (a.k + 127) / 128;
+    const int s0 = share * a.share_steps, s1 = s0 + a.share_steps < steps ? s0 + a.share_steps : steps;
+
+    auto rsrc = [](const void* p, int bytes) {
+        const uint64_t at = reinterpret_cast<uint64_t>(p);
+        return u32x4{(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu, (uint32_t)bytes, (uint32_t)kRawBufferWord3};
+    };
+    // 16 (or 4) bytes a lane from r + off to LDS at dst + 16 (4) lane; counted by `landed`
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+    auto to_lds = [&](u32x4 r, const char* dst, int off) {
+        const uint32_t at = (uint32_t)reinterpret_cast<uintptr_t>((lds_char*)dst);
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                     ::"s"(at), "v"(off), "s"(r) : "m0", "memory");
+    };
+    auto to_lds4 = [&](u32x4 r, const char* dst, int off) {
+        const uint32_t at = (uint32_t)reinterpret_cast<uintptr_t>((lds_char*)dst);
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                     ::"s"(at), "v"(off), "s"(r) : "m0", "memory");
+    };
+#pragma clang diagnostic pop
+    // where a lane's chunks come from: row 64 h + 8 wave + lane / 8 of a tile
+    const int from_row = 8 * wave + (lane >> 3);
+    const int from_chunk = ((lane & 7) ^ (((wave & 1) << 2) | (lane >> 4))) * 16;
+    // H groups of 64 rows from row0 of `base`, the 128 bytes from k0; zeros past the rows, past
+    // k and where the step is not there
+    auto stage_rows = [&](bool there, const uint8_t* base, int64_t ld, int row0, int nrows, int k, int k0, char* dst, auto hr) {
+        constexpr int H = decltype(hr)::value;
+        const int left = there ? k - k0 : 0;
+        const u32x4 r = rsrc(base + row0 * ld + k0, (nrows - row0 < 64 * H ? nrows - row0 - 1 : 64 * H - 1) * (int)ld + left);
+        const int off = from_chunk < left ? from_row * (int)ld + from_chunk : 0x7FFFFFFF;
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+            to_lds(r, dst + (64 * h + 8 * wave) * 128, off == 0x7FFFFFFF ? off : off + h * 64 * (int)ld);
+    };
+    // step s into place i: a's tile, w's, then a float a lane of the scales: waves 0 .. FP / 2 - 1
+    // a's rows, wave 4 w's two blocks of columns, the others nothing
+    auto stage = [&](int s, int i) {
+        char* dst = lds + i * STEP;
+        const bool there = s < s1;
+        const int b = there ? s : s0;
+        stage_rows(there, a.a, a.lda, i0, a.m, a.ak, b * 128, dst, std::integral_constant<int, FP / 2>{});
+        stage_rows(there, a.w, a.ldw, j0, a.n, a.wk, b * 128, dst + TP, std::integral_constant<int, 4>{});
+        const bool of_w = wave == 4;
+        const int row = of_w ? lane : wave * 64 + lane;
+        const int rows = of_w ? (a.n - j0 > 128 ? 2 : 1) : (wave < FP / 2 ? (a.m - i0 < ROWS ? a.m - i0 : ROWS) : 0);
+        const int64_t ld = of_w ? a.ws_row : a.as_row;
+        const float* base = of_w ? a.w_scale + (j0 >> 7) * a.ws_row + b * a.ws_col : a.a_scale + i0 * a.as_row + b * a.as_col;
+        const u32x4 r = rsrc(base, there && rows > 0 ? ((rows - 1) * (int)ld + 1) * 4 : 0);
+        to_lds4(r, dst + TP + TQ + wave * 256, row < rows ? row * (int)ld * 4 : 0x7FFFFFFF);
+    };
+
+    // LDS address of a lane's two chunks of a row group
+    const int at0 = (lane & 15) * 128 + (((lane >> 4) ^ ((lane >> 1) & 7)) * 16), at1 = at0 ^ 64;
+    auto read = [&](const char* tile, int row) {
+        return Op(*reinterpret_cast<const u32x4*>(tile + row * 128 + at0), *reinterpret_cast<const u32x4*>(tile + row * 128 + at1));
+    };
+    auto read_a = [&](int i, int g) { return read(lds + i * STEP, (wm * FP + g) * 16); };
+    auto read_w = [&](int i, int g) { return read(lds + i * STEP + TP, wn * 64 + g * 16); };
+    auto scales_of = [&](int i, float (&f)[FP]) {
+        const float* s = reinterpret_cast<const float*>(lds + i * STEP + TP + TQ);
+        const float t = s[256 + (wn >> 1)];
+#pragma unroll
+        for (int g = 0; g < FP; ++g) f[g] = s[(wm * FP + g) * 16 + (lane & 15)] * t;
+    };
+    // reads are issued ahead of the matrix instructions that follow
+    auto fence = [] {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // this wave's reads are done and all but its newest n loads have landed, then the same of
+    // all waves
+    auto landed = [&](auto n) {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(decltype(n)::value) : "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    f32x4 acc[FP][4] = {};
+    auto add = [&](int g, int j, const Op& q, const Op& p, float f) {
+        const f32x4 t = Op::mul(q, p);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[g][j][e] = __builtin_fmaf(t[e], f, acc[g][j][e]);
+    };
+    if (s0 < s1) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) stage(s0 + i, i);
+        landed(std::integral_constant<int, (R - 1) * LOADS>{});
+        Op q[4] = {read_w(0, 0), read_w(0, 1), read_w(0, 2), read_w(0, 3)};
+        Op p[2][2] = {{read_a(0, 0), read_a(0, 1)}, {read_a(0, 0), read_a(0, 1)}};
+        float f[FP];
+        scales_of(0, f);
+        int at = 0;                               // place of step s
+        for (int s = s0; s < s1; ++s) {
+            const int next = at + 1 < R ? at + 1 : 0;
+#pragma unroll
+            for (int u = 0; u < PAIRS - 1; ++u) {
+                p[(u + 1) & 1][0] = read_a(at, 2 * u + 2);
+                p[(u + 1) & 1][1] = read_a(at, 2 * u + 3);
+                fence();
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) add(2 * u + h, j, q[j], p[u & 1][h], f[2 * u + h]);
+            }
+            landed(std::integral_constant<int, (R - 2) * LOADS>{});
+            stage(s + R, at);
+            const Op n0 = read_a(next, 0), n1 = read_a(next, 1);
+            float nf[FP];
+            scales_of(next, nf);
+            fence();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) add(FP - 2 + h, j, q[j], p[(PAIRS - 1) & 1][h], f[FP - 2 + h]);
+                q[j] = read_w(next, j);
+                fence();
+            }
+            p[0][0] = n0;
+            p[0][1] = n1;
+#pragma unroll
+            for (int g = 0; g < FP; ++g) f[g] = nf[g];
+            at = next;
+        }
+        // nothing may still be on its way to LDS when the workgroup ends
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+
+    // a lane's results: rows row0 + 16 g, four columns from col0 + 16 j
+    const int row0 = i0 + wm * FP * 16 + (lane & 15), col0 = j0 + wn * 64 + 4 * (lane >> 4);
+    if (a.part) {
+#pragma unroll
+        for (int g = 0; g < FP; ++g) {
+            const int row = row0 + g * 16;
+            if (row >= a.m) continue;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int col = col0 + j * 16;
+                if (col < a.n)
+                    *reinterpret_cast<f32x4*>(a.part + ((int64_t)share * a.m + row) * a.part_pitch + col) = acc[g][j];
+            }
+        }
+    } else if (sizeof(O) == 2 && i0 + ROWS <= a.m && j0 + Fp8Shape::kCols <= a.n) {
+        // a whole tile of 16-bit results goes out through LDS, in whole rows of the tile
+        constexpr int PITCH = Fp8Shape::kCols * 2 + 16;
+        static_assert(ROWS * PITCH <= R * STEP, "the tile fits LDS");
+        struct __attribute__((aligned(8))) Four { O e[4]; };
+        struct __attribute__((packed, aligned(2))) Loose { u32x4 v; };
+        landed(std::integral_constant<int, 0>{});         // LDS is no longer read or loaded
+#pragma unroll
+        for (int g = 0; g < FP; ++g)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                Four o;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o.e[e] = from_f32<O>(acc[g][j][e]);
+                *reinterpret_cast<Four*>(lds + (row0 - i0 + g * 16) * PITCH + (col0 - j0 + j * 16) * 2) = o;
+            }
+        __syncthreads();
+        const int r = 2 * wave + (lane >> 5), c = lane & 31;
+        O* o = static_cast<O*>(a.y) + (int64_t)(i0 + r) * a.ldy + j0 + c * 8;
+#pragma unroll
+        for (int h = 0; h < ROWS / 16; ++h) {
+            reinterpret_cast<Loose*>(o)->v = *reinterpret_cast<const u32x4*>(lds + (r + h * 16) * PITCH + c * 16);
+            o += 16 * a.ldy;
+        }
+    } else {
+#pragma unroll
+        for (int g = 0; g < FP; ++g)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (row0 + g * 16 < a.m && col0 + j * 16 < a.n) {
+                    const float v[4] = {acc[g][j][0], acc[g][j][1], acc[g][j][2], acc[g][j][3]};
+                    store4(static_cast<O*>(a.y) + (int64_t)(row0 + g * 16) * a.ldy + col0 + j * 16, v, a.n - (col0 + j * 16));
+                }
+    }
+}
+
+}  // namespace qtcq

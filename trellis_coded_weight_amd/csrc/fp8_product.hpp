@@ -26,7 +26,7 @@ struct Fp8Args {
     const float* w_scale;
     int64_t as_row, as_col, ws_row, ws_col;
     int m, n, k;
-    int pk;                  // k of the operands with their zero padding
+    int ak, wk;              // k of a and w with their zero padding
     void* y;
     int64_t ldy;
     float* part;             // the shares' sums [shares][m][part_pitch], or NULL

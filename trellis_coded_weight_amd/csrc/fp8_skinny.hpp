@@ -1,7 +1,7 @@
 // fp8_skinny.hpp -- the product of e4m3 matrices for few rows of activations, where reading
 // the weights once is the work, gfx950.
 //
-// A workgroup of 8 waves takes 16 MI rows of a and NJ groups of 16 rows of w; its waves share
+// A workgroup of 8 waves takes all rows of a, MI groups of 16, and NJ groups of 16 rows of w; its waves share
 // k: wave v takes the blocks v, v + 8, ... of 128 bytes of every row.  Operands go from memory
 // to registers in the matrix instruction's layout with no LDS and no barrier on the way, DEPTH
 // blocks in flight a wave, a block's scales with it.  The waves' sums are added in wave order
@@ -21,7 +21,7 @@ struct Fp8SkinnyShape {
     static constexpr int kWaves = kThreads / 64;
 };
 
-// grid = (ceil(n / (16 NJ)), ceil(m / (16 MI))), block = 512
+// a.m <= 16 MI.  grid.x = ceil(n / (16 NJ)), block = 512
 template <typename O, int MI, int NJ, int DEPTH, bool ALIGNED>
 __global__ void __launch_bounds__(Fp8SkinnyShape::kThreads)
 fp8_skinny_product(Fp8Args a)
@@ -31,7 +31,7 @@ fp8_skinny_product(Fp8Args a)
     __shared__ f32x4 red[NW][F][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int i0 = blockIdx.y * 16 * MI, j0 = blockIdx.x * 16 * NJ;
+    const int j0 = blockIdx.x * 16 * NJ;
     const int r = lane & 15, c = lane >> 4;
     const int nblk = (a.k + 127) / 128;
 
@@ -43,7 +43,7 @@ fp8_skinny_product(Fp8Args a)
             return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p + row0 * ld), (short)0,
                                                      n > 0 ? (n - 1) * (int)ld + a.k : 0, kRawBufferWord3);
         };
-        ra = rsrc(a.a, a.lda, i0, a.m, 16 * MI);
+        ra = rsrc(a.a, a.lda, 0, a.m, 16 * MI);
         rw = rsrc(a.w, a.ldw, j0, a.n, 16 * NJ);
     }
     struct Set { u32x4 p[2][MI], q[2][NJ]; float s[MI]; float t; };
@@ -69,7 +69,7 @@ fp8_skinny_product(Fp8Args a)
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) o.q[h][j] = chunk(a.w, a.ldw, j0 + 16 * j + r, a.n);
 #pragma unroll
-                for (int i = 0; i < MI; ++i) o.p[h][i] = chunk(a.a, a.lda, i0 + 16 * i + r, a.m);
+                for (int i = 0; i < MI; ++i) o.p[h][i] = chunk(a.a, a.lda, 16 * i + r, a.m);
             }
         }
         // a block past the last: scales of 0, so that nothing is added
@@ -77,7 +77,7 @@ fp8_skinny_product(Fp8Args a)
         const int b = there ? blk : 0;
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
-            const int row = i0 + 16 * i + r < a.m ? i0 + 16 * i + r : a.m - 1;
+            const int row = 16 * i + r < a.m ? 16 * i + r : a.m - 1;
             const float s = a.a_scale[row * a.as_row + b * a.as_col];
             o.s[i] = there ? s : 0.0f;
         }
@@ -118,7 +118,7 @@ fp8_skinny_product(Fp8Args a)
         f32x4 s = red[0][wave][lane];
 #pragma unroll
         for (int w = 1; w < NW; ++w) s += red[w][wave][lane];
-        const int row = i0 + wave / NJ * 16 + r, col = j0 + wave % NJ * 16 + 4 * c;
+        const int row = wave / NJ * 16 + r, col = j0 + wave % NJ * 16 + 4 * c;
         if (row < a.m && col < a.n) {
             const float v[4] = {s[0], s[1], s[2], s[3]};
             store4(static_cast<O*>(a.y) + (int64_t)row * a.ldy + col, v, a.n - col);

@@ -91,7 +91,9 @@ qtcq_status qtcq_matmul_fp8(const uint8_t* a, int64_t lda, const float* a_scale,
 {
     if (M < 0 || N < 0 || K < 0 || lda < K || ldw < K || ldy < N || !readable(as_row, as_col) || !readable(ws_row, ws_col))
         return QTCQ_ERR_INVALID_ARG;
-    if (!float_type(dtype) || !fp8_sizes_ok(M, N, K) || as_row > kScaleMaxStride) return QTCQ_ERR_UNSUPPORTED;
+    if (!float_type(dtype) || !fp8_sizes_ok(M, N, K) || as_row > kScaleMaxStride ||
+        ws_row > kScaleMaxStride)
+        return QTCQ_ERR_UNSUPPORTED;
     if (M == 0 || N == 0) return QTCQ_OK;
     if (!there(a, M, K, 1) || !there(w, N, K, 1) || !there(a_scale, M, K, 4) || !there(w_scale, N, K, 4) ||
         !there(y, M, N, type_size(dtype)))
