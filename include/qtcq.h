@@ -599,7 +599,7 @@ qtcq_status qtcq_layer_norm_vjp(const void* x, int dtype, int64_t rows, int cols
  * and, in the same call where grad_logits is given (the logits are then read once from
  * memory),
  *   grad_logits = grad_loss / T (q sum_j p_j - sum_j p_j e[i_j]).
- * Logits and their softmax in binary32, what concerns the k entries in binary64.  Entries
+ * Logits and their softmax in binary32, sums over the k entries in binary64.  Entries
  * with an index outside 0 .. vocab - 1 are padding.  An entry with p_j = 0 adds nothing,
  * whatever q is there; a token whose entries are all padding (or all -infinity) has loss 0
  * and gradient 0, whatever its logits are.  The same index twice: both entries count.

@@ -135,7 +135,10 @@ def distill(z, index, t, tau, log_z=None, grad_loss=None, dtype=None):
     # running sum's factors when the maximum rises, whose logs add up to the range of z
     far = torch.where(torch.isfinite(a), a, 0.0).abs().clamp(max=104.0)
     es = U * (depth(V) + 16 + 8 * far.amax(1)) if V else 0.0
-    bound = 1.01 * (mass[:, 0] * es + 4 * U * loss.abs()) + 2.0 ** -120
+    # log p and log q are sums in binary64 of products and of two logarithms of sums, each within
+    # 2 U; p is an exp2 of what is behind the point (8 U) of a logarithm that is off by so much
+    terms = torch.where(p > 0, p * (lp - picked), 0.0).abs().sum(1)
+    bound = 1.01 * (mass[:, 0] * (es + 8 * U) + 16 * U * terms + 4 * U * loss.abs()) + 2.0 ** -120
     if grad_loss is None:
         return loss, bound
     scale = (grad_loss.double() / tau)[:, None]

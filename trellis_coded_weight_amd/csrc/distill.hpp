@@ -16,41 +16,16 @@
 // vocabulary) nor a large maximum costs digits.  A workgroup takes a row, and with the
 // gradient wanted in the same call reads it again at once, while the caches still hold it;
 // with few rows several workgroups share one (distill_partial, distill_join, distill_grad).
-// The k entries' own arithmetic is in binary64.
+// The k entries' own sums are in binary64.
 //
-// stats [rows][kDistillStats]: m, log s, the same two of the teacher, and sum p.
+// stats [rows][kDistillStats]: m, log2 s, the same two of the teacher, and sum p.
 #pragma once
 
-#include "dense.hpp"
-#include "norm.hpp"
+#include "model_args.hpp"
 #include "reduce.hpp"
+#include "rows.hpp"
 
 namespace qtcq {
-
-constexpr int kDistillMaxK = 1024;
-constexpr int kDistillStats = 5;
-
-struct DistillArgs {
-    const void* logits;
-    int64_t rows, ldl;
-    int vocab;
-    const void* index;       // [rows][k] int32, or int64 where wide
-    int64_t ldi;
-    bool wide;
-    const void* teacher;     // [rows][k]
-    int64_t ldt;
-    int teacher_type;        // qtcq_dtype: float32, bfloat16, float16
-    int k;
-    float tau;
-    const float* teacher_log_z;  // [rows], or NULL: the sum over the entries
-    float* loss;             // [rows]
-    float* stats;            // [rows][kDistillStats], or NULL
-    const float* grad_loss;  // [rows]
-    void* grad;              // [rows][vocab], or NULL
-    int64_t ldg;
-    float* part;             // [rows][segments][2]: m and s of each segment
-    int segments, segment;   // a row's segments and their length
-};
 
 struct RowStats { float m, ls, tm, tls, mass; };
 
@@ -59,13 +34,13 @@ constexpr float kLog2e = 1.4426950408889634f;
 // where a maximum of -infinity is subtracted (a row without anything finite): 0
 __device__ __forceinline__ float finite_ref(float m) { return m == -__builtin_inff() ? 0.0f : m; }
 
-// LDS of a workgroup that finishes rows
+// LDS of a workgroup: reductions, and the row's entries (dynamic, 16 bytes each)
 struct DistillShared {
     float red[2][16];
-    double sum[16];
-    int index[kDistillMaxK];
-    float p[kDistillMaxK];
+    double sum[2][16];
 };
+struct Entry { int index; float t, z, p; };     // p: for the gradient
+extern __shared__ __align__(16) char distill_entries[];
 
 __device__ __forceinline__ double wave_sum(double v)
 {
@@ -86,53 +61,87 @@ template <int NT>
 __device__ __forceinline__ float block_max(float v, float (&red)[16])
 {
     v = wave_max_f32(v);
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
+    if constexpr (NT > 64) {
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = red[threadIdx.x & (NT / 64 - 1)];
 #pragma unroll
-    for (int w = 0; w < NT / 64; ++w) v = __builtin_fmaxf(v, red[w]);
-    __syncthreads();
+        for (int o = NT / 128; o > 0; o >>= 1) v = __builtin_fmaxf(v, __shfl_xor(v, o, 64));
+        __syncthreads();
+    }
     return v;
 }
 template <int NT, typename F>
 __device__ __forceinline__ F block_sum(F v, F* red)
 {
     v = wave_sum(v);
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = 0;
+    if constexpr (NT > 64) {
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = red[threadIdx.x & (NT / 64 - 1)];
 #pragma unroll
-    for (int w = 0; w < NT / 64; ++w) v += red[w];
-    __syncthreads();
+        for (int o = NT / 128; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+        __syncthreads();
+    }
     return v;
+}
+
+// A row's elements lo .. hi - 1 through f(chunk, element), U chunks a thread at a time with the
+// next ones on their way; `fill` past the end.
+template <typename T, int NT, int U, typename F>
+__device__ __forceinline__ void each_chunk(const T* row, int lo, int hi, T fill, F&& f)
+{
+    constexpr int E = 16 / (int)sizeof(T), STEP = U * NT * E;
+    int at = lo + (int)threadIdx.x * E;
+    int left = hi - lo;                                // from the workgroup's first element on
+    u32x4 v[U];
+    auto load = [&](int from, u32x4 (&o)[U]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) o[u] = load_loose(row + from + u * NT * E);
+    };
+    if (left >= STEP) {
+        load(at, v);
+        for (; left >= 2 * STEP; left -= STEP, at += STEP) {
+            u32x4 next[U];
+            load(at + STEP, next);
+            f(v, at, std::integral_constant<int, U>{});
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = next[u];
+        }
+        f(v, at, std::integral_constant<int, U>{});
+        left -= STEP, at += STEP;
+    }
+    for (; at < hi; at += NT * E) {
+        u32x4 w[1] = {load_filled<T>(row, at, hi, fill)};
+        f(w, at, std::integral_constant<int, 1>{});
+    }
 }
 
 // The running maximum m and sum s of elements lo .. hi - 1 of a row, of the whole workgroup.
 template <typename T, int NT>
 __device__ __forceinline__ void softmax_sums(const T* row, int lo, int hi, float k2, DistillShared& sh, float& m, float& s)
 {
-    constexpr int E = 16 / (int)sizeof(T), U = 4;
+    constexpr int E = 16 / (int)sizeof(T);
     m = -__builtin_inff();
     s = 0.0f;
-    for (int at = lo + (int)threadIdx.x * E; at < hi; at += U * NT * E) {
-        Elems<T, E> v[U];
+    each_chunk<T, NT, 2>(row, lo, hi, (T)-__builtin_inff(), [&](auto& v, int, auto count) {
+        constexpr int N = decltype(count)::value;
+        float x[N][E], top = m;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int c = at + u * NT * E;
-            v[u] = load_elems<T, E>(row, c < hi ? c : hi, hi, (T)-__builtin_inff());
+        for (int u = 0; u < N; ++u) {
+            unpack<T>(v[u], x[u]);
+#pragma unroll
+            for (int e = 0; e < E; ++e) top = __builtin_fmaxf(top, x[u][e]);
         }
-        float top = m;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int e = 0; e < E; ++e) top = __builtin_fmaxf(top, to_f32(v[u].e[e]));
         const float ref = finite_ref(top);
-        s *= __builtin_amdgcn_exp2f((m - ref) * k2);
+        float sum[2] = {s * __builtin_amdgcn_exp2f((m - ref) * k2), 0.0f};
         m = top;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < N; ++u)
 #pragma unroll
-            for (int e = 0; e < E; ++e) s += __builtin_amdgcn_exp2f((to_f32(v[u].e[e]) - ref) * k2);
-    }
+            for (int e = 0; e < E; ++e) sum[e & 1] += __builtin_amdgcn_exp2f((x[u][e] - ref) * k2);
+        s = sum[0] + sum[1];
+    });
     const float all = block_max<NT>(m, sh.red[0]);
     s = block_sum<NT>(s * __builtin_amdgcn_exp2f((m - finite_ref(all)) * k2), sh.red[1]);
     m = all;
@@ -154,41 +163,70 @@ __device__ __forceinline__ int index_at(const DistillArgs& a, int64_t row, int j
     return v >= 0 && v < a.vocab ? (int)v : -1;
 }
 
-// From a row's maximum and sum: its loss, and its statistics.
+// A row's entries to LDS, with the logits at them; thread t has the entries t, t + NT, ... from
+// here to their last use but for the search for repeated indices.
 template <typename T, int NT>
+__device__ __forceinline__ void load_entries(const DistillArgs& a, int64_t row)
+{
+    Entry* en = reinterpret_cast<Entry*>(distill_entries);
+    for (int j = threadIdx.x; j < a.k; j += NT) {
+        const int i = index_at(a, row, j);
+        const float t = teacher_at(a, row, j);
+        en[j] = Entry{i, t, i >= 0 ? to_f32(static_cast<const T*>(a.logits)[row * a.ldl + i]) : 0.0f, 0.0f};
+    }
+}
+
+// log2 of a sum that is 1 or more (or 0, infinite or NaN): the exponent, and the logarithm of
+// the mantissa, whose error is then 2^-24 and not that of a number above 16.
+__device__ __forceinline__ double log2_of(float s)
+{
+    if (!(s >= 1.0f && s < __builtin_inff())) return (double)__builtin_amdgcn_logf(s);
+    const uint32_t b = __builtin_bit_cast(uint32_t, s);
+    return (double)((int)(b >> 23) - 127) + (double)__builtin_amdgcn_logf(__builtin_bit_cast(float, (b & 0x7FFFFFu) | 0x3F800000u));
+}
+
+// 2^v: the hardware's exp2 takes the part behind the point
+__device__ __forceinline__ float exp2_of(double v)
+{
+    if (!(v > -160.0)) return v == v ? 0.0f : (float)v;
+    const double n = rint(v);
+    return __builtin_ldexpf(__builtin_amdgcn_exp2f((float)(v - n)), (int)n);
+}
+
+// From a row's maximum and sum: its loss, and its statistics.
+template <int NT>
 __device__ __forceinline__ RowStats finish_row(const DistillArgs& a, int64_t row, float m, float s, DistillShared& sh)
 {
-    const T* z = static_cast<const T*>(a.logits) + row * a.ldl;
-    const double inv = 1.0 / (double)a.tau;
-    const double ls = log((double)s);
+    const Entry* en = reinterpret_cast<const Entry*>(distill_entries);
+    const double k2 = 1.4426950408889634 / (double)a.tau;
+    const double ls = log2_of(s);
     const double ref = (double)finite_ref(m);
     // the teacher's maximum and sum, or those that the given sum stands for
     float tm = 0.0f;
     double tls = 0.0;
     if (a.teacher_log_z) {
-        tls = (double)a.teacher_log_z[row];
+        tls = (double)a.teacher_log_z[row] * 1.4426950408889634;
     } else {
         tm = -__builtin_inff();
         for (int j = threadIdx.x; j < a.k; j += NT)
-            if (index_at(a, row, j) >= 0) tm = __builtin_fmaxf(tm, teacher_at(a, row, j));
+            if (en[j].index >= 0) tm = __builtin_fmaxf(tm, en[j].t);
         tm = finite_ref(block_max<NT>(tm, sh.red[0]));
         double e = 0.0;
         for (int j = threadIdx.x; j < a.k; j += NT)
-            if (index_at(a, row, j) >= 0) e += exp(((double)teacher_at(a, row, j) - (double)tm) * inv);
-        tls = log(block_sum<NT>(e, sh.sum));
+            if (en[j].index >= 0) e += (double)exp2_of(((double)en[j].t - (double)tm) * k2);
+        tls = log2_of((float)block_sum<NT>(e, sh.sum[0]));
     }
     double loss = 0.0, mass = 0.0;
     for (int j = threadIdx.x; j < a.k; j += NT) {
-        const int i = index_at(a, row, j);
-        if (i < 0) continue;
-        const double t = ((double)teacher_at(a, row, j) - (double)tm) * inv;
+        if (en[j].index < 0) continue;
+        const double t = ((double)en[j].t - (double)tm) * k2;
         // log p; nothing has a share where the sum is 0
-        const double lp = t - tls, p = t == -__builtin_inf() ? 0.0 : exp(lp);
+        const double lp = t - tls, p = t == -__builtin_inf() ? 0.0 : (double)exp2_of(lp);
         mass += p;
-        if (p != 0.0) loss += p * (lp - (((double)to_f32(z[i]) - ref) * inv - ls));
+        if (p != 0.0) loss += p * (lp - (((double)en[j].z - ref) * k2 - ls));
     }
-    loss = block_sum<NT>(loss, sh.sum);
-    mass = block_sum<NT>(mass, sh.sum);
+    loss = block_sum<NT>(loss, sh.sum[0]) * 0.6931471805599453;
+    mass = block_sum<NT>(mass, sh.sum[1]);
     if (!a.teacher_log_z && mass > 0.0) mass = 1.0;
     const RowStats r = {m, (float)ls, tm, (float)tls, (float)mass};
     if (threadIdx.x == 0) {
@@ -205,67 +243,65 @@ __device__ __forceinline__ RowStats finish_row(const DistillArgs& a, int64_t row
 // entries' elements again.  An index that comes up more than once is written by its first
 // entry, with all of their p in order.
 template <typename T, int NT>
-__device__ __forceinline__ void gradient(const DistillArgs& a, int64_t row, int lo, int hi, const RowStats& r,
-                                         DistillShared& sh)
+__device__ __forceinline__ void gradient(const DistillArgs& a, int64_t row, int lo, int hi, const RowStats& r)
 {
-    constexpr int E = 16 / (int)sizeof(T), U = 2;
+    constexpr int E = 16 / (int)sizeof(T);
+    Entry* en = reinterpret_cast<Entry*>(distill_entries);
     const T* z = static_cast<const T*>(a.logits) + row * a.ldl;
     T* g = static_cast<T*>(a.grad) + row * a.ldg;
-    const float k2 = kLog2e / a.tau, ref = finite_ref(r.m), ls2 = r.ls * kLog2e;
+    const float k2 = kLog2e / a.tau, ref = finite_ref(r.m);
     const float scale = a.grad_loss[row] / a.tau, coef = scale * r.mass;
     const bool none = r.mass == 0.0f;
-    for (int j = threadIdx.x; j < a.k; j += NT) {
-        const int i = index_at(a, row, j);
-        sh.index[j] = i;
-        sh.p[j] = i >= 0 ? __builtin_amdgcn_exp2f((teacher_at(a, row, j) - r.tm) * k2 - r.tls * kLog2e) : 0.0f;
-    }
-    auto q = [&](float x) { return none ? 0.0f : coef * __builtin_amdgcn_exp2f(__builtin_fmaf(x - ref, k2, -ls2)); };
-    for (int at = lo + (int)threadIdx.x * E; at < hi; at += U * NT * E) {
-        Elems<T, E> v[U];
+    for (int j = threadIdx.x; j < a.k; j += NT)
+        en[j].p = en[j].index >= 0 ? __builtin_amdgcn_exp2f((en[j].t - r.tm) * k2 - r.tls) : 0.0f;
+    auto q = [&](float x) { return coef * __builtin_amdgcn_exp2f(__builtin_fmaf(x - ref, k2, -r.ls)); };
+    each_chunk<T, NT, 2>(z, lo, hi, (T)0.0f, [&](auto& v, int at, auto count) {
+        constexpr int N = decltype(count)::value;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int c = at + u * NT * E;
-            v[u] = load_elems<T, E>(z, c < hi ? c : hi, hi, (T)0.0f);
+        for (int u = 0; u < N; ++u) {
+            float x[E];
+            unpack<T>(v[u], x);
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = q(x[e]);
+            const u32x4 o = none ? u32x4{0u, 0u, 0u, 0u} : pack<T>(x);
+            if constexpr (N > 1)
+                store_loose(g + at + u * NT * E, o);
+            else
+                store_chunk(g, at, hi, o);
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int c = at + u * NT * E;
-            float o[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = q(to_f32(v[u].e[e]));
-            if (c < hi) store_elems<T, E>(g, c, hi, o);
-        }
-    }
+    });
     // the stores above are done before the entries' are issued, in every wave
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (!none)
         for (int j = threadIdx.x; j < a.k; j += NT) {
-            const int i = sh.index[j];
+            const int i = en[j].index;
             if (i < lo || i >= hi) continue;
             float p = 0.0f;
             bool first = true;
             for (int l = 0; l < a.k; ++l)
-                if (sh.index[l] == i) {
+                if (en[l].index == i) {
                     first = first && l >= j;
-                    p += sh.p[l];
+                    p += en[l].p;
                 }
-            if (first) g[i] = from_f32<T>(q(to_f32(z[i])) - scale * p);
+            if (first) g[i] = from_f32<T>(q(en[j].z) - scale * p);
         }
     __syncthreads();                                  // LDS is free for the next row
 }
 
 // A workgroup a row.  grid.x: any number of workgroups up to the rows
+// (eight waves a SIMD: 64 registers, so that two rows' workgroups run on a compute unit)
 template <typename T, int NT, bool GRAD>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, 8)
 distill_rows(DistillArgs a)
 {
     __shared__ DistillShared sh;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         float m, s;
+        load_entries<T, NT>(a, row);
         softmax_sums<T, NT>(static_cast<const T*>(a.logits) + row * a.ldl, 0, a.vocab, kLog2e / a.tau, sh, m, s);
-        const RowStats r = finish_row<T, NT>(a, row, m, s, sh);
-        if constexpr (GRAD) gradient<T, NT>(a, row, 0, a.vocab, r, sh);
+        const RowStats r = finish_row<NT>(a, row, m, s, sh);
+        if constexpr (GRAD) gradient<T, NT>(a, row, 0, a.vocab, r);
     }
 }
 
@@ -296,9 +332,10 @@ distill_join(DistillArgs a)
     const float* p = a.part + row * a.segments * 2;
     const float k2 = kLog2e / a.tau;
     float m = -__builtin_inff(), s = 0.0f;
+    load_entries<T, NT>(a, row);
     for (int i = 0; i < a.segments; ++i) m = __builtin_fmaxf(m, p[2 * i]);
     for (int i = 0; i < a.segments; ++i) s += p[2 * i + 1] * __builtin_amdgcn_exp2f((p[2 * i] - finite_ref(m)) * k2);
-    finish_row<T, NT>(a, row, m, s, sh);
+    finish_row<NT>(a, row, m, s, sh);
 }
 
 // A workgroup a segment of a row: its gradient.  Segment i of rows * segments, in turn
@@ -306,13 +343,13 @@ template <typename T, int NT>
 __global__ void __launch_bounds__(NT)
 distill_grad(DistillArgs a)
 {
-    __shared__ DistillShared sh;
     for (int64_t b = blockIdx.x; b < a.rows * a.segments; b += gridDim.x) {
         const int64_t row = b / a.segments;
         const int lo = (int)(b - row * a.segments) * a.segment;
         const int hi = lo + a.segment < a.vocab ? lo + a.segment : a.vocab;
         const float* s = a.stats + row * kDistillStats;
-        gradient<T, NT>(a, row, lo, hi, RowStats{s[0], s[1], s[2], s[3], s[4]}, sh);
+        load_entries<T, NT>(a, row);
+        gradient<T, NT>(a, row, lo, hi, RowStats{s[0], s[1], s[2], s[3], s[4]});
     }
 }
 

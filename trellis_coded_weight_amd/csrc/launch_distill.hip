@@ -6,8 +6,6 @@ namespace qtcq {
 namespace host {
 namespace {
 
-constexpr int kThreads = 1024;
-
 // Segments of a row: enough for two workgroups a compute unit, of at least 8192 elements.
 void cut_row(DistillArgs& a)
 {
@@ -25,25 +23,47 @@ void cut_row(DistillArgs& a)
 
 unsigned capped(int64_t n) { return (unsigned)(n < (1 << 20) ? n : 1 << 20); }
 
+// f(threads a row) for rows (or segments) of n elements
+template <typename F>
+void with_threads(int n, F&& f)
+{
+    if (n <= 2048)
+        f(int_c<64>{});
+    else if (n <= 16384)
+        f(int_c<256>{});
+    else
+        f(int_c<1024>{});
+}
+
 template <typename T>
 qtcq_status grad_impl(const DistillArgs& a, hipStream_t st)
 {
-    hipLaunchKernelGGL((distill_grad<T, kThreads>), dim3(capped(a.rows * a.segments)), dim3(kThreads), 0, st, a);
+    with_threads(a.segment, [&](auto nt) {
+        constexpr int NT = decltype(nt)::value;
+        hipLaunchKernelGGL((distill_grad<T, NT>), dim3(capped(a.rows * a.segments)), dim3(NT), sizeof(Entry) * a.k, st, a);
+    });
     return launch_status();
 }
 
 template <typename T>
 qtcq_status distill_impl(const DistillArgs& a, hipStream_t st)
 {
+    const size_t entries = sizeof(Entry) * a.k;
     if (a.segments == 1) {
-        if (a.grad)
-            hipLaunchKernelGGL((distill_rows<T, kThreads, true>), dim3(capped(a.rows)), dim3(kThreads), 0, st, a);
-        else
-            hipLaunchKernelGGL((distill_rows<T, kThreads, false>), dim3(capped(a.rows)), dim3(kThreads), 0, st, a);
+        with_threads(a.vocab, [&](auto nt) {
+            constexpr int NT = decltype(nt)::value;
+            if (a.grad)
+                hipLaunchKernelGGL((distill_rows<T, NT, true>), dim3(capped(a.rows)), dim3(NT), entries, st, a);
+            else
+                hipLaunchKernelGGL((distill_rows<T, NT, false>), dim3(capped(a.rows)), dim3(NT), entries, st, a);
+        });
         return launch_status();
     }
-    hipLaunchKernelGGL((distill_partial<T, kThreads>), dim3((unsigned)(a.rows * a.segments)), dim3(kThreads), 0, st, a);
-    hipLaunchKernelGGL((distill_join<T, 256>), dim3((unsigned)a.rows), dim3(256), 0, st, a);
+    with_threads(a.segment, [&](auto nt) {
+        constexpr int NT = decltype(nt)::value;
+        hipLaunchKernelGGL((distill_partial<T, NT>), dim3((unsigned)(a.rows * a.segments)), dim3(NT), 0, st, a);
+    });
+    hipLaunchKernelGGL((distill_join<T, 256>), dim3((unsigned)a.rows), dim3(256), entries, st, a);
     return a.grad ? grad_impl<T>(a, st) : launch_status();
 }
 

@@ -4,13 +4,9 @@
 #pragma once
 
 #include "dense_host.hpp"
+#include "model_args.hpp"
 
 namespace qtcq {
-
-struct Fp8Args;
-struct NormArgs;
-struct NormGradArgs;
-struct DistillArgs;
 
 namespace host {
 

@@ -16,68 +16,11 @@
 // order.  No atomics: the same bits on every run.
 #pragma once
 
-#include "dense.hpp"
+#include "model_args.hpp"
 #include "reduce.hpp"
+#include "rows.hpp"
 
 namespace qtcq {
-
-struct NormArgs {
-    const void* x;
-    int64_t rows, ldx;
-    int cols;
-    const void* weight;      // [cols], or NULL: ones
-    const void* bias;        // [cols], or NULL: zeros
-    float eps;
-    void* y;
-    int64_t ldy;
-    float* mean;             // [rows], or NULL
-    float* rstd;
-};
-
-struct NormGradArgs {
-    const void* x;
-    const void* grad_y;
-    int64_t rows, ldx, ldgy;
-    int cols;
-    const void* weight;
-    const float* mean;
-    const float* rstd;
-    void* grad_x;            // or NULL
-    int64_t ldgx;
-    float* part;             // [row groups][2][part_pitch]: sums of dw, then of db
-    int part_pitch;
-};
-
-template <typename T, int E>
-struct Elems { T e[E]; };
-
-// E elements at `at` of a row of n, `fill` past its end
-template <typename T, int E>
-__device__ __forceinline__ Elems<T, E> load_elems(const T* row, int at, int n, T fill)
-{
-    struct __attribute__((packed, aligned(sizeof(T)))) Loose { Elems<T, E> v; };
-    if (at + E <= n) return reinterpret_cast<const Loose*>(row + at)->v;
-    Elems<T, E> o;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o.e[e] = at + e < n ? row[at + e] : fill;
-    return o;
-}
-
-template <typename T, int E>
-__device__ __forceinline__ void store_elems(T* row, int at, int n, const float (&v)[E])
-{
-    struct __attribute__((packed, aligned(sizeof(T)))) Loose { Elems<T, E> v; };
-    if (at + E <= n) {
-        Loose o;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o.v.e[e] = from_f32<T>(v[e]);
-        *reinterpret_cast<Loose*>(row + at) = o;
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        if (at + e < n) row[at + e] = from_f32<T>(v[e]);
-}
 
 constexpr int norm_threads(int rt) { return rt < 256 ? 256 : rt; }
 
@@ -161,7 +104,7 @@ layer_norm_rows(NormArgs a)
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 v[e] = __builtin_fmaf((to_f32(o.e[e]) - mean) * rstd, to_f32(w.e[e]), to_f32(b.e[e]));
-            store_elems<T, E>(y + row * a.ldy, c * E, n, v);
+            store_chunk<T>(y + row * a.ldy, c * E, n, pack<T>(v));
         };
 #pragma unroll
         for (int i = 0; i < NCH; ++i)
@@ -237,7 +180,7 @@ layer_norm_grad(NormGradArgs a)
                 const float xh = (to_f32(ox.e[e]) - mean) * rstd, gw = to_f32(og.e[e]) * to_f32(w.e[e]);
                 v[e] = rstd * (gw - __builtin_fmaf(xh, m2, m1));
             }
-            store_elems<T, E>(gx + row * a.ldgx, c * E, n, v);
+            store_chunk<T>(gx + row * a.ldgx, c * E, n, pack<T>(v));
         };
 #pragma unroll
         for (int i = 0; i < NCH; ++i)

@@ -2,8 +2,6 @@
 // weights"): argument validation; accepted calls go to launch_blocks.hip, launch_fp8.hip,
 // launch_norm.hip and launch_distill.hip.
 #include "model_host.hpp"
-#include "distill.hpp"
-#include "fp8_product.hpp"
 
 namespace host = qtcq::host;
 using namespace qtcq::host;
