@@ -86,65 +86,83 @@ __device__ __forceinline__ F block_sum(F v, F* red)
     return v;
 }
 
-// A row's elements lo .. hi - 1 through f(chunk, element), U chunks a thread at a time with the
-// next ones on their way; `fill` past the end.
-template <typename T, int NT, int U, typename F>
-__device__ __forceinline__ void each_chunk(const T* row, int lo, int hi, T fill, F&& f)
+// The chunks of 16 bytes of a row's elements lo .. hi - 1, two at a time: f(v, c, whole) for
+// chunks c and c + NT of the thread, of which those below `whole` are there (`fill` elsewhere),
+// with the next two on their way.  The elements behind the last whole chunk are the last
+// thread's, which takes them last: f(v, whole, 0) with them in v[0].
+template <typename T, int NT, typename F>
+__device__ __forceinline__ void each_pair(const T* row, int lo, int hi, T fill, F&& f)
 {
-    constexpr int E = 16 / (int)sizeof(T), STEP = U * NT * E;
-    int at = lo + (int)threadIdx.x * E;
-    int left = hi - lo;                                // from the workgroup's first element on
-    u32x4 v[U];
-    auto load = [&](int from, u32x4 (&o)[U]) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) o[u] = load_loose(row + from + u * NT * E);
-    };
-    if (left >= STEP) {
-        load(at, v);
-        for (; left >= 2 * STEP; left -= STEP, at += STEP) {
-            u32x4 next[U];
-            load(at + STEP, next);
-            f(v, at, std::integral_constant<int, U>{});
-#pragma unroll
-            for (int u = 0; u < U; ++u) v[u] = next[u];
+    constexpr int E = 16 / (int)sizeof(T);
+    const T* z = row + lo;
+    const int whole = (hi - lo) / E, t = threadIdx.x;
+    const u32x4 none = __builtin_bit_cast(u32x4, load_filled<T>(row, 0, 0, fill));
+    u32x4 v[2];
+    int c = t, left = whole;                           // whole chunks from the workgroup's first on
+    if (left >= 2 * NT) {
+        v[0] = load_loose(z + c * E);
+        v[1] = load_loose(z + (c + NT) * E);
+        for (; left >= 4 * NT; left -= 2 * NT, c += 2 * NT) {
+            const u32x4 next[2] = {load_loose(z + (c + 2 * NT) * E), load_loose(z + (c + 3 * NT) * E)};
+            f(v, c, whole);
+            v[0] = next[0];
+            v[1] = next[1];
         }
-        f(v, at, std::integral_constant<int, U>{});
-        left -= STEP, at += STEP;
+        f(v, c, whole);
+        left -= 2 * NT, c += 2 * NT;
     }
-    for (; at < hi; at += NT * E) {
-        u32x4 w[1] = {load_filled<T>(row, at, hi, fill)};
-        f(w, at, std::integral_constant<int, 1>{});
+    if (left > 0) {
+        v[0] = c < whole ? load_loose(z + c * E) : none;
+        v[1] = c + NT < whole ? load_loose(z + (c + NT) * E) : none;
+        f(v, c, whole);
     }
+    if (t == NT - 1 && whole * E < hi - lo) {
+        v[0] = load_filled<T>(z, whole * E, hi - lo, fill);
+        v[1] = none;
+        f(v, whole, 0);
+    }
+}
+
+// Two chunks into the running maximum m and sum s of a thread.  One of -infinities changes
+// no bit of them.
+template <typename T>
+__device__ __forceinline__ void take_pair(const u32x4* v, float k2, float& m, float& s)
+{
+    constexpr int E = 16 / (int)sizeof(T);
+    float x[2][E], top = m;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        unpack<T>(v[u], x[u]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) top = __builtin_fmaxf(top, x[u][e]);
+    }
+    const float ref = finite_ref(top);
+    float sum[2] = {s * __builtin_amdgcn_exp2f((m - ref) * k2), 0.0f};
+    m = top;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum[e & 1] += __builtin_amdgcn_exp2f((x[u][e] - ref) * k2);
+    s = sum[0] + sum[1];
+}
+
+// The threads' maxima and sums joined, the same in all of the workgroup.
+template <int NT>
+__device__ __forceinline__ void join_threads(float k2, DistillShared& sh, float& m, float& s)
+{
+    const float all = block_max<NT>(m, sh.red[0]);
+    s = block_sum<NT>(s * __builtin_amdgcn_exp2f((m - finite_ref(all)) * k2), sh.red[1]);
+    m = all;
 }
 
 // The running maximum m and sum s of elements lo .. hi - 1 of a row, of the whole workgroup.
 template <typename T, int NT>
 __device__ __forceinline__ void softmax_sums(const T* row, int lo, int hi, float k2, DistillShared& sh, float& m, float& s)
 {
-    constexpr int E = 16 / (int)sizeof(T);
     m = -__builtin_inff();
     s = 0.0f;
-    each_chunk<T, NT, 2>(row, lo, hi, (T)-__builtin_inff(), [&](auto& v, int, auto count) {
-        constexpr int N = decltype(count)::value;
-        float x[N][E], top = m;
-#pragma unroll
-        for (int u = 0; u < N; ++u) {
-            unpack<T>(v[u], x[u]);
-#pragma unroll
-            for (int e = 0; e < E; ++e) top = __builtin_fmaxf(top, x[u][e]);
-        }
-        const float ref = finite_ref(top);
-        float sum[2] = {s * __builtin_amdgcn_exp2f((m - ref) * k2), 0.0f};
-        m = top;
-#pragma unroll
-        for (int u = 0; u < N; ++u)
-#pragma unroll
-            for (int e = 0; e < E; ++e) sum[e & 1] += __builtin_amdgcn_exp2f((x[u][e] - ref) * k2);
-        s = sum[0] + sum[1];
-    });
-    const float all = block_max<NT>(m, sh.red[0]);
-    s = block_sum<NT>(s * __builtin_amdgcn_exp2f((m - finite_ref(all)) * k2), sh.red[1]);
-    m = all;
+    each_pair<T, NT>(row, lo, hi, (T)-__builtin_inff(), [&](const u32x4* v, int, int) { take_pair<T>(v, k2, m, s); });
+    join_threads<NT>(k2, sh, m, s);
 }
 
 __device__ __forceinline__ float teacher_at(const DistillArgs& a, int64_t row, int j)
@@ -239,59 +257,67 @@ __device__ __forceinline__ RowStats finish_row(const DistillArgs& a, int64_t row
     return r;
 }
 
-// The gradient of elements lo .. hi - 1 of a row: first as if no entry were there, then the
-// entries' elements again.  An index that comes up more than once is written by its first
-// entry, with all of their p in order.
-template <typename T, int NT>
-__device__ __forceinline__ void gradient(const DistillArgs& a, int64_t row, int lo, int hi, const RowStats& r)
+// The gradient of a row's elements as if no entry were there (q), and the entries' elements.
+template <typename T>
+struct RowGradient {
+    static constexpr int E = 16 / (int)sizeof(T);
+    T* g;
+    float k2, ref, ls, scale, coef;
+    bool none;
+
+    __device__ __forceinline__ RowGradient(const DistillArgs& a, int64_t row, const RowStats& r)
+        : g(static_cast<T*>(a.grad) + row * a.ldg), k2(kLog2e / a.tau), ref(finite_ref(r.m)), ls(r.ls),
+          scale(a.grad_loss[row] / a.tau), coef(scale * r.mass), none(r.mass == 0.0f) {}
+    __device__ __forceinline__ float q(float x) const
+    {
+        return coef * __builtin_amdgcn_exp2f(__builtin_fmaf(x - ref, k2, -ls));
+    }
+    __device__ __forceinline__ u32x4 chunk(u32x4 v) const
+    {
+        float x[E];
+        unpack<T>(v, x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = q(x[e]);
+        return none ? u32x4{0u, 0u, 0u, 0u} : pack<T>(x);
+    }
+    // The elements lo .. hi - 1 that entries are at, once all others are written.  An index that
+    // comes up more than once is written by its first entry, with all of their p in order.
+    template <int NT>
+    __device__ __forceinline__ void entries(int k, int lo, int hi) const
+    {
+        // the chunks' stores are done before the entries' are issued, in every wave
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        const Entry* en = reinterpret_cast<const Entry*>(distill_entries);
+        if (!none)
+            for (int j = threadIdx.x; j < k; j += NT) {
+                const int i = en[j].index;
+                if (i < lo || i >= hi) continue;
+                float p = 0.0f;
+                bool first = true;
+                for (int l = 0; l < k; ++l)
+                    if (en[l].index == i) {
+                        first = first && l >= j;
+                        p += en[l].p;
+                    }
+                if (first) g[i] = from_f32<T>(q(en[j].z) - scale * p);
+            }
+        __syncthreads();                              // LDS is free for the next row
+    }
+};
+
+// p of a row's entries, as their gradients take it
+template <int NT>
+__device__ __forceinline__ void entry_shares(const DistillArgs& a, const RowStats& r)
 {
-    constexpr int E = 16 / (int)sizeof(T);
     Entry* en = reinterpret_cast<Entry*>(distill_entries);
-    const T* z = static_cast<const T*>(a.logits) + row * a.ldl;
-    T* g = static_cast<T*>(a.grad) + row * a.ldg;
-    const float k2 = kLog2e / a.tau, ref = finite_ref(r.m);
-    const float scale = a.grad_loss[row] / a.tau, coef = scale * r.mass;
-    const bool none = r.mass == 0.0f;
     for (int j = threadIdx.x; j < a.k; j += NT)
-        en[j].p = en[j].index >= 0 ? __builtin_amdgcn_exp2f((en[j].t - r.tm) * k2 - r.tls) : 0.0f;
-    auto q = [&](float x) { return coef * __builtin_amdgcn_exp2f(__builtin_fmaf(x - ref, k2, -r.ls)); };
-    each_chunk<T, NT, 2>(z, lo, hi, (T)0.0f, [&](auto& v, int at, auto count) {
-        constexpr int N = decltype(count)::value;
-#pragma unroll
-        for (int u = 0; u < N; ++u) {
-            float x[E];
-            unpack<T>(v[u], x);
-#pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = q(x[e]);
-            const u32x4 o = none ? u32x4{0u, 0u, 0u, 0u} : pack<T>(x);
-            if constexpr (N > 1)
-                store_loose(g + at + u * NT * E, o);
-            else
-                store_chunk(g, at, hi, o);
-        }
-    });
-    // the stores above are done before the entries' are issued, in every wave
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (!none)
-        for (int j = threadIdx.x; j < a.k; j += NT) {
-            const int i = en[j].index;
-            if (i < lo || i >= hi) continue;
-            float p = 0.0f;
-            bool first = true;
-            for (int l = 0; l < a.k; ++l)
-                if (en[l].index == i) {
-                    first = first && l >= j;
-                    p += en[l].p;
-                }
-            if (first) g[i] = from_f32<T>(q(en[j].z) - scale * p);
-        }
-    __syncthreads();                                  // LDS is free for the next row
+        en[j].p = en[j].index >= 0 ? __builtin_amdgcn_exp2f((en[j].t - r.tm) * (kLog2e / a.tau) - r.tls) : 0.0f;
 }
 
-// A workgroup a row.  grid.x: any number of workgroups up to the rows
-// (eight waves a SIMD: 64 registers, so that two rows' workgroups run on a compute unit)
-template <typename T, int NT, bool GRAD>
+// A workgroup a row, for the loss.  grid.x: any number of workgroups up to the rows
+// (eight waves a SIMD: 64 registers, so that two rows of 1024 threads run on a compute unit)
+template <typename T, int NT>
 __global__ void __launch_bounds__(NT, 8)
 distill_rows(DistillArgs a)
 {
@@ -300,8 +326,58 @@ distill_rows(DistillArgs a)
         float m, s;
         load_entries<T, NT>(a, row);
         softmax_sums<T, NT>(static_cast<const T*>(a.logits) + row * a.ldl, 0, a.vocab, kLog2e / a.tau, sh, m, s);
+        finish_row<NT>(a, row, m, s, sh);
+        __syncthreads();                              // LDS is free for the next row
+    }
+}
+
+// A workgroup a row, for the loss and the gradient: HOLD chunks a thread of the row stay in
+// registers from the one to the other; what a longer row has beyond them is read again.  The
+// chunks are taken in the order of each_pair, so that the loss is that of distill_rows.
+//   grid.x: any number of workgroups up to the rows
+template <typename T, int NT, int HOLD>
+__global__ void __launch_bounds__(NT)
+distill_train(DistillArgs a)
+{
+    constexpr int E = 16 / (int)sizeof(T);
+    static_assert(HOLD % 2 == 0, "chunks are taken in pairs");
+    __shared__ DistillShared sh;
+    const float k2 = kLog2e / a.tau;
+    const int whole = a.vocab / E, t = threadIdx.x;   // whole chunks; the last thread has the rest
+    const bool last = t == NT - 1 && whole * E < a.vocab;
+    const T low = (T)-__builtin_inff();
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const T* z = static_cast<const T*>(a.logits) + row * a.ldl;
+        const u32x4 none = __builtin_bit_cast(u32x4, load_filled<T>(z, 0, 0, low));
+        u32x4 held[HOLD];
+#pragma unroll
+        for (int i = 0; i < HOLD; ++i) held[i] = t + i * NT < whole ? load_loose(z + (t + i * NT) * E) : none;
+        load_entries<T, NT>(a, row);
+        float m = -__builtin_inff(), s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < HOLD; i += 2)
+            if (i * NT < whole) take_pair<T>(held + i, k2, m, s);
+        for (int c = t + HOLD * NT; c < whole; c += 2 * NT) {
+            const u32x4 v[2] = {load_loose(z + c * E), c + NT < whole ? load_loose(z + (c + NT) * E) : none};
+            take_pair<T>(v, k2, m, s);
+        }
+        if (last) {
+            const u32x4 v[2] = {load_filled<T>(z, whole * E, a.vocab, low), none};
+            take_pair<T>(v, k2, m, s);
+        }
+        join_threads<NT>(k2, sh, m, s);
         const RowStats r = finish_row<NT>(a, row, m, s, sh);
-        if constexpr (GRAD) gradient<T, NT>(a, row, 0, a.vocab, r);
+        const RowGradient<T> grad(a, row, r);
+        entry_shares<NT>(a, r);
+        // (the places of the chunks are formed again: kept, they would take HOLD registers)
+        int c0 = t;
+        asm volatile("" : "+v"(c0));
+#pragma unroll
+        for (int i = 0; i < HOLD; ++i)
+            if (c0 + i * NT < whole) store_loose(grad.g + (c0 + i * NT) * E, grad.chunk(held[i]));
+        for (int c = c0 + HOLD * NT; c < whole; c += NT) store_loose(grad.g + c * E, grad.chunk(load_loose(z + c * E)));
+        if (last) store_chunk(grad.g, whole * E, a.vocab, grad.chunk(load_filled<T>(z, whole * E, a.vocab, low)));
+        grad.template entries<NT>(a.k, 0, a.vocab);
     }
 }
 
@@ -348,8 +424,21 @@ distill_grad(DistillArgs a)
         const int lo = (int)(b - row * a.segments) * a.segment;
         const int hi = lo + a.segment < a.vocab ? lo + a.segment : a.vocab;
         const float* s = a.stats + row * kDistillStats;
+        const RowStats r = {s[0], s[1], s[2], s[3], s[4]};
         load_entries<T, NT>(a, row);
-        gradient<T, NT>(a, row, lo, hi, RowStats{s[0], s[1], s[2], s[3], s[4]});
+        entry_shares<NT>(a, r);
+        const RowGradient<T> grad(a, row, r);
+        constexpr int E = 16 / (int)sizeof(T);
+        T* g = grad.g + lo;
+        each_pair<T, NT>(static_cast<const T*>(a.logits) + row * a.ldl, lo, hi, (T)0.0f, [&](const u32x4* v, int c, int whole) {
+            if (whole == 0) {
+                store_chunk(g, c * E, hi - lo, grad.chunk(v[0]));
+            } else {
+                if (c < whole) store_loose(g + c * E, grad.chunk(v[0]));
+                if (c + NT < whole) store_loose(g + (c + NT) * E, grad.chunk(v[1]));
+            }
+        });
+        grad.template entries<NT>(a.k, lo, hi);
     }
 }
 

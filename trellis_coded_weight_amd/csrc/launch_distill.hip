@@ -23,22 +23,25 @@ void cut_row(DistillArgs& a)
 
 unsigned capped(int64_t n) { return (unsigned)(n < (1 << 20) ? n : 1 << 20); }
 
-// f(threads a row) for rows (or segments) of n elements
-template <typename F>
-void with_threads(int n, F&& f)
+// f(threads a row, chunks a thread holds) for rows (or segments) of n elements
+template <typename T, typename F>
+void with_shape(int n, F&& f)
 {
-    if (n <= 2048)
-        f(int_c<64>{});
-    else if (n <= 16384)
-        f(int_c<256>{});
+    const int chunks = n / (16 / (int)sizeof(T));
+    if (chunks <= 256)
+        f(int_c<64>{}, int_c<4>{});
+    else if (chunks <= 2048)
+        f(int_c<256>{}, int_c<8>{});
+    else if (chunks <= 8192)
+        f(int_c<512>{}, int_c<16>{});
     else
-        f(int_c<1024>{});
+        f(int_c<1024>{}, int_c<16>{});
 }
 
 template <typename T>
 qtcq_status grad_impl(const DistillArgs& a, hipStream_t st)
 {
-    with_threads(a.segment, [&](auto nt) {
+    with_shape<T>(a.segment, [&](auto nt, auto) {
         constexpr int NT = decltype(nt)::value;
         hipLaunchKernelGGL((distill_grad<T, NT>), dim3(capped(a.rows * a.segments)), dim3(NT), sizeof(Entry) * a.k, st, a);
     });
@@ -50,16 +53,16 @@ qtcq_status distill_impl(const DistillArgs& a, hipStream_t st)
 {
     const size_t entries = sizeof(Entry) * a.k;
     if (a.segments == 1) {
-        with_threads(a.vocab, [&](auto nt) {
-            constexpr int NT = decltype(nt)::value;
+        with_shape<T>(a.vocab, [&](auto nt, auto hold) {
+            constexpr int NT = decltype(nt)::value, HOLD = decltype(hold)::value;
             if (a.grad)
-                hipLaunchKernelGGL((distill_rows<T, NT, true>), dim3(capped(a.rows)), dim3(NT), entries, st, a);
+                hipLaunchKernelGGL((distill_train<T, NT, HOLD>), dim3(capped(a.rows)), dim3(NT), entries, st, a);
             else
-                hipLaunchKernelGGL((distill_rows<T, NT, false>), dim3(capped(a.rows)), dim3(NT), entries, st, a);
+                hipLaunchKernelGGL((distill_rows<T, NT>), dim3(capped(a.rows)), dim3(NT), entries, st, a);
         });
         return launch_status();
     }
-    with_threads(a.segment, [&](auto nt) {
+    with_shape<T>(a.segment, [&](auto nt, auto) {
         constexpr int NT = decltype(nt)::value;
         hipLaunchKernelGGL((distill_partial<T, NT>), dim3((unsigned)(a.rows * a.segments)), dim3(NT), 0, st, a);
     });
