@@ -39,7 +39,12 @@ struct DistillShared {
     float red[2][16];
     double sum[2][16];
 };
-struct Entry { int index; float t, z, p; };     // p: for the gradient
+// z: the logit at the index, and then, for the gradient, the number of the next entry of its
+// list (1 and up; 0 ends it).  t: the teacher's logit, and then what its element's gradient has
+// to give up: the p of all entries at the index for the first of them, 0 for the others.
+struct Entry { int index; union { float z; uint32_t next; }; float t, p; };
+// lists of entries by the chunk that they are in, and how many there are
+constexpr int kLists(int nt) { return nt < 512 ? nt * 8 : 4096; }
 extern __shared__ __align__(16) char distill_entries[];
 
 __device__ __forceinline__ double wave_sum(double v)
@@ -89,7 +94,8 @@ __device__ __forceinline__ F block_sum(F v, F* red)
 // The chunks of 16 bytes of a row's elements lo .. hi - 1, two at a time: f(v, c, whole) for
 // chunks c and c + NT of the thread, of which those below `whole` are there (`fill` elsewhere),
 // with the next two on their way.  The elements behind the last whole chunk are the last
-// thread's, which takes them last: f(v, whole, 0) with them in v[0].
+// thread's, whose wave takes them last: f(v, whole, whole + 1) with them in that thread's v[0],
+// and c past that in the other threads.
 template <typename T, int NT, typename F>
 __device__ __forceinline__ void each_pair(const T* row, int lo, int hi, T fill, F&& f)
 {
@@ -116,10 +122,11 @@ __device__ __forceinline__ void each_pair(const T* row, int lo, int hi, T fill, 
         v[1] = c + NT < whole ? load_loose(z + (c + NT) * E) : none;
         f(v, c, whole);
     }
-    if (t == NT - 1 && whole * E < hi - lo) {
-        v[0] = load_filled<T>(z, whole * E, hi - lo, fill);
+    if (t >= NT - 64 && whole * E < hi - lo) {
+        const bool mine = t == NT - 1;
+        v[0] = mine ? load_filled<T>(z, whole * E, hi - lo, fill) : none;
         v[1] = none;
-        f(v, whole, 0);
+        f(v, mine ? whole : whole + 1, whole + 1);
     }
 }
 
@@ -190,7 +197,9 @@ __device__ __forceinline__ void load_entries(const DistillArgs& a, int64_t row)
     for (int j = threadIdx.x; j < a.k; j += NT) {
         const int i = index_at(a, row, j);
         const float t = teacher_at(a, row, j);
-        en[j] = Entry{i, t, i >= 0 ? to_f32(static_cast<const T*>(a.logits)[row * a.ldl + i]) : 0.0f, 0.0f};
+        en[j].index = i;
+        en[j].z = i >= 0 ? to_f32(static_cast<const T*>(a.logits)[row * a.ldl + i]) : 0.0f;
+        en[j].t = t;
     }
 }
 
@@ -257,62 +266,82 @@ __device__ __forceinline__ RowStats finish_row(const DistillArgs& a, int64_t row
     return r;
 }
 
-// The gradient of a row's elements as if no entry were there (q), and the entries' elements.
-template <typename T>
+// The gradient of a row's elements lo .. hi - 1, a chunk at a time.  A chunk's list holds the
+// entries that are in it (and in others of the same list), each taken off its element before
+// the store.
+template <typename T, int NT>
 struct RowGradient {
     static constexpr int E = 16 / (int)sizeof(T);
-    T* g;
+    T* g;                                             // from lo on
+    int lo, n;
     float k2, ref, ls, scale, coef;
     bool none;
+    const uint32_t* lists;
 
-    __device__ __forceinline__ RowGradient(const DistillArgs& a, int64_t row, const RowStats& r)
-        : g(static_cast<T*>(a.grad) + row * a.ldg), k2(kLog2e / a.tau), ref(finite_ref(r.m)), ls(r.ls),
-          scale(a.grad_loss[row] / a.tau), coef(scale * r.mass), none(r.mass == 0.0f) {}
-    __device__ __forceinline__ float q(float x) const
-    {
-        return coef * __builtin_amdgcn_exp2f(__builtin_fmaf(x - ref, k2, -ls));
-    }
-    __device__ __forceinline__ u32x4 chunk(u32x4 v) const
+    __device__ __forceinline__ RowGradient(const DistillArgs& a, int64_t row, int from, int to, const RowStats& r,
+                                           const uint32_t* heads)
+        : g(static_cast<T*>(a.grad) + row * a.ldg + from), lo(from), n(to - from), k2(kLog2e / a.tau), ref(finite_ref(r.m)),
+          ls(r.ls), scale(a.grad_loss[row] / a.tau), coef(scale * r.mass), none(r.mass == 0.0f), lists(heads) {}
+
+    // chunk c (from lo on) with the logits v, if it is `there`
+    __device__ __forceinline__ void put(bool there, int c, u32x4 v) const
     {
         float x[E];
         unpack<T>(v, x);
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = q(x[e]);
-        return none ? u32x4{0u, 0u, 0u, 0u} : pack<T>(x);
-    }
-    // The elements lo .. hi - 1 that entries are at, once all others are written.  An index that
-    // comes up more than once is written by its first entry, with all of their p in order.
-    template <int NT>
-    __device__ __forceinline__ void entries(int k, int lo, int hi) const
-    {
-        // the chunks' stores are done before the entries' are issued, in every wave
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        const Entry* en = reinterpret_cast<const Entry*>(distill_entries);
-        if (!none)
-            for (int j = threadIdx.x; j < k; j += NT) {
-                const int i = en[j].index;
-                if (i < lo || i >= hi) continue;
-                float p = 0.0f;
-                bool first = true;
-                for (int l = 0; l < k; ++l)
-                    if (en[l].index == i) {
-                        first = first && l >= j;
-                        p += en[l].p;
-                    }
-                if (first) g[i] = from_f32<T>(q(en[j].z) - scale * p);
-            }
-        __syncthreads();                              // LDS is free for the next row
+        for (int e = 0; e < E; ++e) x[e] = coef * __builtin_amdgcn_exp2f(__builtin_fmaf(x[e] - ref, k2, -ls));
+        uint32_t at = there ? lists[c & (kLists(NT) - 1)] : 0u;
+        if (__builtin_expect(at != 0u, 0)) {
+            const Entry* en = reinterpret_cast<const Entry*>(distill_entries);
+            do {
+                const Entry o = en[at - 1];
+                const int e0 = o.index - lo - c * E;
+                if (o.t != 0.0f && e0 >= 0 && e0 < E) {
+                    const float p = scale * o.t;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) x[e] = e == e0 ? x[e] - p : x[e];
+                }
+                at = o.next;
+            } while (at != 0u);
+        }
+        if (there) store_chunk(g, c * E, n, none ? u32x4{0u, 0u, 0u, 0u} : pack<T>(x));
     }
 };
 
-// p of a row's entries, as their gradients take it
-template <int NT>
-__device__ __forceinline__ void entry_shares(const DistillArgs& a, const RowStats& r)
+// The lists of a row's entries in the elements lo .. hi - 1.  Their order within a list is that
+// of arrival, on which no result depends: an index's first entry alone has a share to give
+// up, the sum of p over the entries at that index in their own order.
+template <typename T, int NT>
+__device__ __forceinline__ void list_entries(const DistillArgs& a, int lo, int hi, const RowStats& r, uint32_t* lists)
 {
+    constexpr int E = 16 / (int)sizeof(T);
     Entry* en = reinterpret_cast<Entry*>(distill_entries);
+    for (int i = threadIdx.x; i < kLists(NT); i += NT) lists[i] = 0;
+    __syncthreads();
+    const bool any = r.mass != 0.0f;
+    auto inside = [&](int j) { return any && en[j].index >= lo && en[j].index < hi; };
     for (int j = threadIdx.x; j < a.k; j += NT)
-        en[j].p = en[j].index >= 0 ? __builtin_amdgcn_exp2f((en[j].t - r.tm) * (kLog2e / a.tau) - r.tls) : 0.0f;
+        if (inside(j)) {
+            en[j].p = __builtin_amdgcn_exp2f((en[j].t - r.tm) * (kLog2e / a.tau) - r.tls);
+            en[j].next = atomicExch(&lists[(en[j].index - lo) / E & (kLists(NT) - 1)], (uint32_t)j + 1u);
+        }
+    __syncthreads();
+    for (int j = threadIdx.x; j < a.k; j += NT)
+        if (inside(j)) {
+            const int i = en[j].index;
+            bool first = true, alone = true;
+            for (uint32_t l = lists[(i - lo) / E & (kLists(NT) - 1)]; l != 0u; l = en[l - 1].next)
+                if (en[l - 1].index == i && (int)l - 1 != j) {
+                    alone = false;
+                    first = first && (int)l - 1 > j;
+                }
+            float p = first ? en[j].p : 0.0f;
+            if (first && !alone)
+                for (int l = j + 1; l < a.k; ++l)
+                    if (en[l].index == i) p += en[l].p;
+            en[j].t = p;
+        }
+    __syncthreads();
 }
 
 // A workgroup a row, for the loss.  grid.x: any number of workgroups up to the rows
@@ -332,8 +361,10 @@ distill_rows(DistillArgs a)
 }
 
 // A workgroup a row, for the loss and the gradient: HOLD chunks a thread of the row stay in
-// registers from the one to the other; what a longer row has beyond them is read again.  The
-// chunks are taken in the order of each_pair, so that the loss is that of distill_rows.
+// registers from the one to the other; what a longer row has beyond them is read again.  As
+// a chunk's gradient is stored, the same chunk of the workgroup's next row is loaded in its
+// place.  The chunks are taken in the order of each_pair, so that the loss is that of
+// distill_rows.
 //   grid.x: any number of workgroups up to the rows
 template <typename T, int NT, int HOLD>
 __global__ void __launch_bounds__(NT)
@@ -342,16 +373,17 @@ distill_train(DistillArgs a)
     constexpr int E = 16 / (int)sizeof(T);
     static_assert(HOLD % 2 == 0, "chunks are taken in pairs");
     __shared__ DistillShared sh;
+    __shared__ uint32_t lists[kLists(NT)];
     const float k2 = kLog2e / a.tau;
     const int whole = a.vocab / E, t = threadIdx.x;   // whole chunks; the last thread has the rest
-    const bool last = t == NT - 1 && whole * E < a.vocab;
+    const bool rest = t >= NT - 64 && whole * E < a.vocab, last = t == NT - 1;
     const T low = (T)-__builtin_inff();
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const T* z = static_cast<const T*>(a.logits) + row * a.ldl;
-        const u32x4 none = __builtin_bit_cast(u32x4, load_filled<T>(z, 0, 0, low));
-        u32x4 held[HOLD];
+    const T* z = static_cast<const T*>(a.logits) + blockIdx.x * a.ldl;
+    const u32x4 none = __builtin_bit_cast(u32x4, load_filled<T>(z, 0, 0, low));
+    u32x4 held[HOLD];
 #pragma unroll
-        for (int i = 0; i < HOLD; ++i) held[i] = t + i * NT < whole ? load_loose(z + (t + i * NT) * E) : none;
+    for (int i = 0; i < HOLD; ++i) held[i] = t + i * NT < whole ? load_loose(z + (t + i * NT) * E) : none;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         load_entries<T, NT>(a, row);
         float m = -__builtin_inff(), s = 0.0f;
 #pragma unroll
@@ -361,23 +393,35 @@ distill_train(DistillArgs a)
             const u32x4 v[2] = {load_loose(z + c * E), c + NT < whole ? load_loose(z + (c + NT) * E) : none};
             take_pair<T>(v, k2, m, s);
         }
-        if (last) {
-            const u32x4 v[2] = {load_filled<T>(z, whole * E, a.vocab, low), none};
+        if (rest) {
+            const u32x4 v[2] = {last ? load_filled<T>(z, whole * E, a.vocab, low) : none, none};
             take_pair<T>(v, k2, m, s);
         }
         join_threads<NT>(k2, sh, m, s);
         const RowStats r = finish_row<NT>(a, row, m, s, sh);
-        const RowGradient<T> grad(a, row, r);
-        entry_shares<NT>(a, r);
-        // (the places of the chunks are formed again: kept, they would take HOLD registers)
+        list_entries<T, NT>(a, 0, a.vocab, r, lists);
+        const RowGradient<T, NT> grad(a, row, 0, a.vocab, r, lists);
+        // (the places of the chunks and their binary32 elements are formed again: kept from the
+        // loss on, they would take more registers than the chunks)
         int c0 = t;
         asm volatile("" : "+v"(c0));
 #pragma unroll
+        for (int i = 0; i < HOLD; ++i) asm volatile("" : "+v"(held[i]));
+        for (int c = HOLD * NT; c < whole; c += NT) {
+            const bool there = c + c0 < whole;
+            grad.put(there, c + c0, there ? load_loose(z + (c + c0) * E) : none);
+        }
+        if (rest) grad.put(last, whole, last ? load_filled<T>(z, whole * E, a.vocab, low) : none);
+        const bool more = row + gridDim.x < a.rows;
+        z += gridDim.x * a.ldl;
+#pragma unroll
         for (int i = 0; i < HOLD; ++i)
-            if (c0 + i * NT < whole) store_loose(grad.g + (c0 + i * NT) * E, grad.chunk(held[i]));
-        for (int c = c0 + HOLD * NT; c < whole; c += NT) store_loose(grad.g + c * E, grad.chunk(load_loose(z + c * E)));
-        if (last) store_chunk(grad.g, whole * E, a.vocab, grad.chunk(load_filled<T>(z, whole * E, a.vocab, low)));
-        grad.template entries<NT>(a.k, 0, a.vocab);
+            if (i * NT < whole) {
+                const bool there = c0 + i * NT < whole;
+                grad.put(there, c0 + i * NT, held[i]);
+                held[i] = there && more ? load_loose(z + (c0 + i * NT) * E) : none;
+            }
+        __syncthreads();                              // LDS is free for the next row
     }
 }
 
@@ -398,7 +442,7 @@ distill_partial(DistillArgs a)
     }
 }
 
-// The segments of a row joined in order, and its loss.  grid.x = rows
+// The segments of a row joined, and its loss.  grid.x = rows
 template <typename T, int NT>
 __global__ void __launch_bounds__(NT)
 distill_join(DistillArgs a)
@@ -409,8 +453,12 @@ distill_join(DistillArgs a)
     const float k2 = kLog2e / a.tau;
     float m = -__builtin_inff(), s = 0.0f;
     load_entries<T, NT>(a, row);
-    for (int i = 0; i < a.segments; ++i) m = __builtin_fmaxf(m, p[2 * i]);
-    for (int i = 0; i < a.segments; ++i) s += p[2 * i + 1] * __builtin_amdgcn_exp2f((p[2 * i] - finite_ref(m)) * k2);
+    for (int i = threadIdx.x; i < a.segments; i += NT) {
+        const float top = __builtin_fmaxf(m, p[2 * i]), ref = finite_ref(top);
+        s = s * __builtin_amdgcn_exp2f((m - ref) * k2) + p[2 * i + 1] * __builtin_amdgcn_exp2f((p[2 * i] - ref) * k2);
+        m = top;
+    }
+    join_threads<NT>(k2, sh, m, s);
     finish_row<NT>(a, row, m, s, sh);
 }
 
@@ -419,6 +467,7 @@ template <typename T, int NT>
 __global__ void __launch_bounds__(NT)
 distill_grad(DistillArgs a)
 {
+    __shared__ uint32_t lists[kLists(NT)];
     for (int64_t b = blockIdx.x; b < a.rows * a.segments; b += gridDim.x) {
         const int64_t row = b / a.segments;
         const int lo = (int)(b - row * a.segments) * a.segment;
@@ -426,19 +475,13 @@ distill_grad(DistillArgs a)
         const float* s = a.stats + row * kDistillStats;
         const RowStats r = {s[0], s[1], s[2], s[3], s[4]};
         load_entries<T, NT>(a, row);
-        entry_shares<NT>(a, r);
-        const RowGradient<T> grad(a, row, r);
-        constexpr int E = 16 / (int)sizeof(T);
-        T* g = grad.g + lo;
+        list_entries<T, NT>(a, lo, hi, r, lists);
+        const RowGradient<T, NT> grad(a, row, lo, hi, r, lists);
         each_pair<T, NT>(static_cast<const T*>(a.logits) + row * a.ldl, lo, hi, (T)0.0f, [&](const u32x4* v, int c, int whole) {
-            if (whole == 0) {
-                store_chunk(g, c * E, hi - lo, grad.chunk(v[0]));
-            } else {
-                if (c < whole) store_loose(g + c * E, grad.chunk(v[0]));
-                if (c + NT < whole) store_loose(g + (c + NT) * E, grad.chunk(v[1]));
-            }
+            grad.put(c < whole, c, v[0]);
+            grad.put(c + NT < whole, c + NT, v[1]);
         });
-        grad.template entries<NT>(a.k, lo, hi);
+        __syncthreads();                              // LDS is free for the next row
     }
 }
 

@@ -55,8 +55,12 @@ qtcq_status distill_impl(const DistillArgs& a, hipStream_t st)
     if (a.segments == 1) {
         with_shape<T>(a.vocab, [&](auto nt, auto hold) {
             constexpr int NT = decltype(nt)::value, HOLD = decltype(hold)::value;
+            // as many workgroups as run at once (by their registers), each of which goes through its
+            // rows; a training row's loads then overlap the stores of the one before
+            constexpr int64_t at_once = (int64_t)kComputeUnits * (NT == 64 ? 32 : NT == 256 ? 5 : 1024 / NT);
             if (a.grad)
-                hipLaunchKernelGGL((distill_train<T, NT, HOLD>), dim3(capped(a.rows)), dim3(NT), entries, st, a);
+                hipLaunchKernelGGL((distill_train<T, NT, HOLD>), dim3((unsigned)(a.rows < at_once ? a.rows : at_once)),
+                                   dim3(NT), entries, st, a);
             else
                 hipLaunchKernelGGL((distill_rows<T, NT>), dim3(capped(a.rows)), dim3(NT), entries, st, a);
         });
