@@ -6,35 +6,28 @@ namespace qtcq {
 namespace host {
 namespace {
 
-// f(RT, NCH) for rows of `chunks` 16-byte chunks: the fewest threads a row that hold it in
-// up to `hold` registers' chunks each
-template <typename F>
-void with_row_shape(int chunks, F&& f)
-{
-    if (chunks <= 64)
-        f(int_c<64>{}, int_c<1>{});
-    else if (chunks <= 256)
-        f(int_c<256>{}, int_c<1>{});
-    else if (chunks <= 1024)
-        f(int_c<1024>{}, int_c<1>{});
-    else
-        f(int_c<1024>{}, int_c<2>{});
-}
-
-// row groups of the weight gradients' sums
-constexpr int kMostWorkgroups = 512;
+// most workgroups of the gradient, each of which writes a part of the weights' gradients
+constexpr int kMostWorkgroups = 256;
 
 template <typename T, typename W>
 qtcq_status norm_impl(const NormArgs& a, hipStream_t st)
 {
     constexpr int E = 16 / (int)sizeof(T);
-    with_row_shape((a.cols + E - 1) / E, [&](auto rt, auto nch) {
-        constexpr int RT = decltype(rt)::value, NCH = decltype(nch)::value, PER = norm_threads(RT) / RT;
-        const int64_t most = 256 * (2048 / norm_threads(RT)), groups = (a.rows + PER - 1) / PER;
-        hipLaunchKernelGGL((layer_norm_rows<T, W, RT, NCH>), dim3((unsigned)(groups < most ? groups : most)),
-                           dim3(norm_threads(RT)), 0, st, a);
-    });
-    return launch_status();
+    auto go = [&](auto rt, auto nch, auto is_long) {
+        constexpr int RT = decltype(rt)::value, NCH = decltype(nch)::value, NT = norm_threads(RT), PER = NT / RT;
+        const int64_t most = kComputeUnits * (2048 / NT), groups = (a.rows + PER - 1) / PER;
+        hipLaunchKernelGGL((layer_norm_rows<T, W, RT, NCH, decltype(is_long)::value>), dim3((unsigned)(groups < most ? groups : most)), dim3(NT), 0, st,
+                           a);
+        return launch_status();
+    };
+    const int chunks = (a.cols + E - 1) / E;
+    if (chunks <= 64) return go(int_c<64>{}, int_c<1>{}, bool_c<false>{});
+    if (chunks <= 128) return go(int_c<64>{}, int_c<2>{}, bool_c<false>{});
+    if (chunks <= 256) return go(int_c<64>{}, int_c<4>{}, bool_c<false>{});
+    if (chunks <= 512) return go(int_c<256>{}, int_c<2>{}, bool_c<false>{});
+    if (chunks <= 1024) return go(int_c<256>{}, int_c<4>{}, bool_c<false>{});
+    if (chunks <= 2048) return go(int_c<1024>{}, int_c<2>{}, bool_c<false>{});
+    return go(int_c<1024>{}, int_c<2>{}, bool_c<true>{});
 }
 
 int part_pitch(int cols) { return (cols + 7) / 8 * 8; }
@@ -48,15 +41,30 @@ qtcq_status grad_impl(NormGradArgs a, W* grad_weight, W* grad_bias, float* part,
     int groups = 0;
     a.part_pitch = part_pitch(a.cols);
     a.part = want_w && held ? part : nullptr;
-    if (a.grad_x || (want_w && held))
-        with_row_shape(chunks, [&](auto rt, auto nch) {
-            constexpr int RT = decltype(rt)::value, NCH = decltype(nch)::value, PER = norm_threads(RT) / RT;
-            const int64_t most = kMostWorkgroups, all = (a.rows + PER - 1) / PER;
-            const unsigned grid = (unsigned)(all < most ? all : most);
-            groups = grid * PER;
-            if (grid == 0) return;
-            hipLaunchKernelGGL((layer_norm_grad<T, W, RT, NCH>), dim3(grid), dim3(norm_threads(RT)), 0, st, a);
-        });
+    auto go = [&](auto rt, auto nch, auto rows, auto is_long) {
+        constexpr int RT = decltype(rt)::value, NCH = decltype(nch)::value, R = decltype(rows)::value;
+        constexpr int PER = kNormGradThreads / RT * R;
+        const int64_t all = (a.rows + PER - 1) / PER;
+        groups = (int)(all < kMostWorkgroups ? all : kMostWorkgroups);
+        if (groups > 0)
+            hipLaunchKernelGGL((layer_norm_grad<T, W, RT, NCH, R, decltype(is_long)::value>), dim3(groups), dim3(kNormGradThreads), 0, st, a);
+    };
+    if (a.grad_x || (want_w && held)) {
+        if (chunks <= 64)
+            go(int_c<64>{}, int_c<1>{}, int_c<2>{}, bool_c<false>{});
+        else if (chunks <= 128)
+            go(int_c<128>{}, int_c<1>{}, int_c<2>{}, bool_c<false>{});
+        else if (chunks <= 256)
+            go(int_c<256>{}, int_c<1>{}, int_c<2>{}, bool_c<false>{});
+        else if (chunks <= 512)
+            go(int_c<512>{}, int_c<1>{}, int_c<2>{}, bool_c<false>{});
+        else if (chunks <= 1024)
+            go(int_c<1024>{}, int_c<1>{}, int_c<2>{}, bool_c<false>{});
+        else if (held)
+            go(int_c<1024>{}, int_c<2>{}, int_c<1>{}, bool_c<false>{});
+        else
+            go(int_c<1024>{}, int_c<1>{}, int_c<1>{}, bool_c<true>{});
+    }
     if (want_w) {
         if (!held) {
             const int64_t share = a.rows / 64 + 1;
@@ -83,8 +91,7 @@ qtcq_status with_types(int dtype, int weight_dtype, F&& f)
 
 size_t norm_grad_workspace_bytes(int64_t rows, int cols)
 {
-    const int64_t most = 4 * kMostWorkgroups;
-    return (size_t)(rows < most ? (rows + 3) / 4 * 4 : most) * 2 * part_pitch(cols) * 4;
+    return (size_t)(rows < kMostWorkgroups ? rows : kMostWorkgroups) * 2 * part_pitch(cols) * 4;
 }
 
 qtcq_status launch_layer_norm(const NormArgs& a, int dtype, int weight_dtype, hipStream_t st)

@@ -8,12 +8,12 @@
 // All in binary32, each result rounded once.  The variance is the mean of the squared
 // differences, never a difference of squares: a row is held in registers between its passes.
 //
-// Both directions are bound by memory (x, g read once, y or dx written once).  RT threads a
-// row (64: a wave, no barrier; 256 and 1024: a workgroup), NCH 16-byte chunks a thread; a
-// workgroup goes through rows blockIdx, + gridDim, ... and keeps the weights of its columns,
-// which all rows share, in registers.  So do the sums of dw and db: each row group (the RT
-// threads) adds its rows in order and writes its sums to part, which join_norm_sums adds in
-// order.  No atomics: the same bits on every run.
+// Both directions are bound by memory (x, g read once, y or dx written once), so a row's loads
+// are issued before the work on the rows ahead of it.  RT threads a row, NCH 16-byte chunks
+// a thread; a workgroup goes through its rows and keeps the weights of its columns, which all
+// rows share, in registers.  So do the sums of dw and db: each group of RT threads adds
+// its rows in order, a workgroup its groups, and join_norm_sums the workgroups.  No atomics:
+// the same bits on every run.
 #pragma once
 
 #include "model_args.hpp"
@@ -22,38 +22,41 @@
 
 namespace qtcq {
 
-constexpr int norm_threads(int rt) { return rt < 256 ? 256 : rt; }
-
-// Sums over the RT threads of a row of N values at once; red: [2][N][16] in LDS, the two
-// halves in turn, so that one barrier a call is enough.
-template <int RT, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[N][16], int& turn)
+// Sums over the RT threads of a row of N values at once (a row group's threads lie together);
+// red: [2][N][waves of the workgroup] in LDS, the two halves in turn, so that one barrier a
+// call is enough.
+template <int NT, int RT, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[N][NT / 64], int& turn)
 {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
     if constexpr (RT > 64) {
-        const int wave = threadIdx.x >> 6;
+        const int wave = threadIdx.x >> 6, first = wave & ~(RT / 64 - 1);
         if ((threadIdx.x & 63) == 0)
 #pragma unroll
             for (int i = 0; i < N; ++i) red[turn][i][wave] = v[i];
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            v[i] = 0.0f;
+            v[i] = red[turn][i][first + (threadIdx.x & (RT / 64 - 1))];
 #pragma unroll
-            for (int w = 0; w < RT / 64; ++w) v[i] += red[turn][i][w];
+            for (int o = RT / 128; o > 0; o >>= 1) v[i] += __shfl_xor(v[i], o, 64);
         }
         turn ^= 1;
     }
 }
 
-// grid.x: any number of workgroups up to ceil(rows / row groups a workgroup)
-template <typename T, typename W, int RT, int NCH>
+constexpr int norm_threads(int rt) { return rt < 256 ? 256 : rt; }
+
+// One row a row group at a time, the next one on its way.  LONG: chunks beyond NCH RT are read
+// anew by each pass.
+//   grid.x: any number of workgroups up to ceil(rows / row groups a workgroup)
+template <typename T, typename W, int RT, int NCH, bool LONG>
 __global__ void __launch_bounds__(norm_threads(RT))
 layer_norm_rows(NormArgs a)
 {
-    constexpr int E = 16 / (int)sizeof(T), PER = norm_threads(RT) / RT;
-    __shared__ float red[2][1][16];
+    constexpr int E = 16 / (int)sizeof(T), NT = norm_threads(RT), PER = NT / RT;
+    __shared__ float red[2][1][NT / 64];
     const int t = threadIdx.x % RT, n = a.cols, nch = (n + E - 1) / E;
     const T* x = static_cast<const T*>(a.x);
     T* y = static_cast<T*>(a.y);
@@ -65,140 +68,246 @@ layer_norm_rows(NormArgs a)
 #pragma unroll
     for (int i = 0; i < NCH; ++i)
         if (t + i * RT < nch) hw[i] = weights(t + i * RT), hb[i] = biases(t + i * RT);
-    int turn = 0;
-    for (int64_t row = (int64_t)blockIdx.x * PER + threadIdx.x / RT; row < a.rows; row += (int64_t)gridDim.x * PER) {
-        const T* xr = x + row * a.ldx;
-        Elems<T, E> held[NCH];
-        auto load = [&](int c) { return load_elems<T, E>(xr, c * E, n, (T)0.0f); };
-        float s[1] = {0.0f};
-        auto add = [&](const Elems<T, E>& o) {
+    Place place[NCH];
 #pragma unroll
-            for (int e = 0; e < E; ++e) s[0] += to_f32(o.e[e]);
+    for (int i = 0; i < NCH; ++i) place[i] = place_of<T>(t + i * RT, n);
+    const bool uneven = n % E != 0;
+    const int64_t step = (int64_t)gridDim.x * PER;
+    int64_t row = (int64_t)blockIdx.x * PER + threadIdx.x / RT;
+    u32x4 next[NCH];
+    auto load = [&](int64_t r, int c) { return load_zero<T>(x + r * a.ldx, c, n); };
+    auto fetch = [&](int64_t r) {
+        const T* xr = x + (r < a.rows ? r : a.rows - 1) * a.ldx;
+        if (n < E) {
+            next[0] = load_short(xr, n);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) next[i] = load_loose(xr + place[i].at);
+        }
+    };
+    fetch(row);
+    int turn = 0;
+    // row groups of a workgroup stay together, for the barriers
+    for (; row - threadIdx.x / RT < a.rows; row += step) {
+        const bool there = row < a.rows;
+        u32x4 held[NCH];
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) held[i] = uneven && n > E ? behind(next[i], place[i].bits) : next[i];
+        if (row + step - threadIdx.x / RT < a.rows) fetch(row + step);
+        float s[1] = {0.0f};
+        auto add = [&](u32x4 o) {
+            float v[E];
+            unpack<T>(o, v);
+#pragma unroll
+            for (int e = 0; e < E; ++e) s[0] += v[e];
         };
 #pragma unroll
         for (int i = 0; i < NCH; ++i)
-            if (t + i * RT < nch) held[i] = load(t + i * RT);
-#pragma unroll
-        for (int i = 0; i < NCH; ++i)
             if (t + i * RT < nch) add(held[i]);
-        for (int c = t + NCH * RT; c < nch; c += RT) add(load(c));
-        row_sums<RT>(s, red, turn);
+        if (LONG && there)
+            for (int c = t + NCH * RT; c < nch; c += RT) add(load(row, c));
+        row_sums<NT, RT>(s, red, turn);
         const float mean = s[0] / (float)n;
         s[0] = 0.0f;
-        auto square = [&](int c, const Elems<T, E>& o) {
+        auto square = [&](int c, u32x4 o) {
+            float v[E];
+            unpack<T>(o, v);
+            if ((c + 1) * E <= n) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float d = c * E + e < n ? to_f32(o.e[e]) - mean : 0.0f;
-                s[0] = __builtin_fmaf(d, d, s[0]);
+                for (int e = 0; e < E; ++e) s[0] = __builtin_fmaf(v[e] - mean, v[e] - mean, s[0]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (c * E + e < n) s[0] = __builtin_fmaf(v[e] - mean, v[e] - mean, s[0]);
             }
         };
 #pragma unroll
         for (int i = 0; i < NCH; ++i)
             if (t + i * RT < nch) square(t + i * RT, held[i]);
-        for (int c = t + NCH * RT; c < nch; c += RT) square(c, load(c));
-        row_sums<RT>(s, red, turn);
+        if (LONG && there)
+            for (int c = t + NCH * RT; c < nch; c += RT) square(c, load(row, c));
+        row_sums<NT, RT>(s, red, turn);
+        if (!there) continue;
         const float rstd = 1.0f / __builtin_sqrtf(s[0] / (float)n + a.eps);
         if (a.mean && t == 0) a.mean[row] = mean, a.rstd[row] = rstd;
-        auto put = [&](int c, const Elems<T, E>& o, const Elems<W, E>& w, const Elems<W, E>& b) {
+        auto put = [&](int c, u32x4 o, const Elems<W, E>& w, const Elems<W, E>& b) {
             float v[E];
+            unpack<T>(o, v);
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                v[e] = __builtin_fmaf((to_f32(o.e[e]) - mean) * rstd, to_f32(w.e[e]), to_f32(b.e[e]));
+            for (int e = 0; e < E; ++e) v[e] = __builtin_fmaf((v[e] - mean) * rstd, to_f32(w.e[e]), to_f32(b.e[e]));
             store_chunk<T>(y + row * a.ldy, c * E, n, pack<T>(v));
         };
 #pragma unroll
         for (int i = 0; i < NCH; ++i)
             if (t + i * RT < nch) put(t + i * RT, held[i], hw[i], hb[i]);
-        for (int c = t + NCH * RT; c < nch; c += RT) put(c, load(c), weights(c), biases(c));
+        for (int c = t + NCH * RT; LONG && c < nch; c += RT) put(c, load(row, c), weights(c), biases(c));
     }
 }
 
+constexpr int kNormGradThreads = 1024;
+
 // grad_x, and the sums of dw and db where a.part is there (then every chunk of a row is held:
-// nch <= NCH RT).
-//   grid.x: any number of workgroups up to ceil(rows / row groups a workgroup); row group
-//   blockIdx.x * (row groups a workgroup) + threadIdx.x / RT writes its part, of zeros where
-//   it had no row
-template <typename T, typename W, int RT, int NCH>
-__global__ void __launch_bounds__(norm_threads(RT))
+// nch <= NCH RT): R rows a row group at a time, the next ones on their way.  LONG: chunks
+// beyond NCH RT are read anew by each pass.
+//   grid.x: any number of workgroups; each writes its part, of zeros where it had no row
+template <typename T, typename W, int RT, int NCH, int R, bool LONG>
+__global__ void __launch_bounds__(kNormGradThreads)
 layer_norm_grad(NormGradArgs a)
 {
-    constexpr int E = 16 / (int)sizeof(T), PER = norm_threads(RT) / RT;
-    __shared__ float red[2][2][16];
-    const int t = threadIdx.x % RT, n = a.cols, nch = (n + E - 1) / E;
+    constexpr int E = 16 / (int)sizeof(T), NT = kNormGradThreads, PER = NT / RT;
+    static_assert(PER == 1 || NCH == 1, "row groups are joined with one chunk a thread");
+    __shared__ float red[2][2 * R][NT / 64];
+    const int t = threadIdx.x % RT, group = threadIdx.x / RT, n = a.cols, nch = (n + E - 1) / E;
     const T* x = static_cast<const T*>(a.x);
     const T* gy = static_cast<const T*>(a.grad_y);
     T* gx = static_cast<T*>(a.grad_x);
     const W* weight = static_cast<const W*>(a.weight);
     const bool want_w = a.part != nullptr;
-    Elems<W, E> hw[NCH];
     auto weights = [&](int c) { return load_elems<W, E>(weight, c * E, weight ? n : 0, (W)1.0f); };
+    Elems<W, E> hw[NCH];
     float dw[NCH][E] = {}, db[NCH][E] = {};
 #pragma unroll
     for (int i = 0; i < NCH; ++i)
         if (t + i * RT < nch) hw[i] = weights(t + i * RT);
-    int turn = 0;
-    for (int64_t row = (int64_t)blockIdx.x * PER + threadIdx.x / RT; row < a.rows; row += (int64_t)gridDim.x * PER) {
-        const T* xr = x + row * a.ldx;
-        const T* gr = gy + row * a.ldgy;
-        const float mean = a.mean[row], rstd = a.rstd[row];
-        Elems<T, E> hx[NCH], hg[NCH];
-        auto load_x = [&](int c) { return load_elems<T, E>(xr, c * E, n, (T)0.0f); };
-        auto load_g = [&](int c) { return load_elems<T, E>(gr, c * E, n, (T)0.0f); };
+    auto load_x = [&](int64_t r, int c) { return load_zero<T>(x + r * a.ldx, c, n); };
+    auto load_g = [&](int64_t r, int c) { return load_zero<T>(gy + r * a.ldgy, c, n); };
+    struct Rows { u32x4 x[R][NCH], g[R][NCH]; float mean[R], rstd[R]; };
+    Place place[NCH];
 #pragma unroll
-        for (int i = 0; i < NCH; ++i)
-            if (t + i * RT < nch) hx[i] = load_x(t + i * RT), hg[i] = load_g(t + i * RT);
-        float s[2] = {0.0f, 0.0f};
+    for (int i = 0; i < NCH; ++i) place[i] = place_of<T>(t + i * RT, n);
+    const bool uneven = n % E != 0;
+    // rows past the last are read as the last one
+    auto fetch = [&](int64_t row, Rows& o) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t at = row + r < a.rows ? row + r : a.rows - 1;
+            o.mean[r] = a.mean[at];
+            o.rstd[r] = a.rstd[at];
+            if (n < E) {
+                o.x[r][0] = load_short(x + at * a.ldx, n);
+                o.g[r][0] = load_short(gy + at * a.ldgy, n);
+                continue;
+            }
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) {
+                o.x[r][i] = load_loose(x + at * a.ldx + place[i].at);
+                o.g[r][i] = load_loose(gy + at * a.ldgy + place[i].at);
+            }
+        }
+    };
+    const int64_t step = (int64_t)gridDim.x * PER * R;
+    int64_t row = ((int64_t)blockIdx.x * PER + group) * R;
+    Rows cur, next;
+    fetch(row, next);
+    int turn = 0;
+    for (int64_t first = (int64_t)blockIdx.x * PER * R; first < a.rows; first += step, row += step) {
+        cur = next;
+        if (first + step < a.rows) fetch(row + step, next);
+        // into place, and rows past the last to zeros
+        if ((uneven && n > E) || first + PER * R > a.rows) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const bool there = row + r < a.rows;
+                if (!there) cur.mean[r] = cur.rstd[r] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < NCH; ++i) {
+                    const int bits = !there ? 128 : (n > E ? place[i].bits : 0);
+                    cur.x[r][i] = behind(cur.x[r][i], bits);
+                    cur.g[r][i] = behind(cur.g[r][i], bits);
+                }
+            }
+        }
+        float s[2 * R] = {};
         // an element past the row's end has g = 0, and x = 0 as any finite x
-        auto add = [&](const Elems<T, E>& ox, const Elems<T, E>& og, const Elems<W, E>& w) {
+        auto add = [&](int r, u32x4 ox, u32x4 og, const Elems<W, E>& w) {
+            float xv[E], gv[E];
+            unpack<T>(ox, xv);
+            unpack<T>(og, gv);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const float xh = (to_f32(ox.e[e]) - mean) * rstd, gw = to_f32(og.e[e]) * to_f32(w.e[e]);
-                s[0] += gw;
-                s[1] = __builtin_fmaf(gw, xh, s[1]);
+                const float gw = gv[e] * to_f32(w.e[e]);
+                s[2 * r] += gw;
+                s[2 * r + 1] = __builtin_fmaf(gw, (xv[e] - cur.mean[r]) * cur.rstd[r], s[2 * r + 1]);
             }
         };
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) {
+                if (t + i * RT >= nch) continue;
+                add(r, cur.x[r][i], cur.g[r][i], hw[i]);
+                if (want_w) {
+                    float xv[E], gv[E];
+                    unpack<T>(cur.x[r][i], xv);
+                    unpack<T>(cur.g[r][i], gv);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        dw[i][e] = __builtin_fmaf(gv[e], (xv[e] - cur.mean[r]) * cur.rstd[r], dw[i][e]);
+                        db[i][e] += gv[e];
+                    }
+                }
+            }
+        if (!gx) continue;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (LONG && row + r < a.rows)
+                for (int c = t + NCH * RT; c < nch; c += RT) add(r, load_x(row + r, c), load_g(row + r, c), weights(c));
+        row_sums<NT, RT>(s, red, turn);
+        // (the elements are taken from their chunks again: kept in binary32 over the sums, they
+        // would not fit the registers)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) asm volatile("" : "+v"(cur.x[r][i]), "+v"(cur.g[r][i]));
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (row + r >= a.rows) continue;
+            const float m1 = s[2 * r] / (float)n, m2 = s[2 * r + 1] / (float)n;
+            auto put = [&](int c, u32x4 ox, u32x4 og, const Elems<W, E>& w) {
+                float xv[E], gv[E];
+                unpack<T>(ox, xv);
+                unpack<T>(og, gv);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    xv[e] = cur.rstd[r] * (gv[e] * to_f32(w.e[e]) - __builtin_fmaf((xv[e] - cur.mean[r]) * cur.rstd[r], m2, m1));
+                store_chunk<T>(gx + (row + r) * a.ldgx, c * E, n, pack<T>(xv));
+            };
+#pragma unroll
+            for (int i = 0; i < NCH; ++i)
+                if (t + i * RT < nch) put(t + i * RT, cur.x[r][i], cur.g[r][i], hw[i]);
+            for (int c = t + NCH * RT; LONG && c < nch; c += RT) put(c, load_x(row + r, c), load_g(row + r, c), weights(c));
+        }
+    }
+    if (!want_w) return;
+    float* p = a.part + (int64_t)blockIdx.x * 2 * a.part_pitch;
+    if constexpr (PER == 1) {
 #pragma unroll
         for (int i = 0; i < NCH; ++i)
             if (t + i * RT < nch) {
-                add(hx[i], hg[i], hw[i]);
-                if (want_w)
+                const int at = (t + i * RT) * E;          // part rows hold whole chunks
 #pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const float g = to_f32(hg[i].e[e]);
-                        dw[i][e] = __builtin_fmaf(g, (to_f32(hx[i].e[e]) - mean) * rstd, dw[i][e]);
-                        db[i][e] += g;
-                    }
+                for (int e = 0; e < E; e += 4) {
+                    *reinterpret_cast<f32x4*>(p + at + e) = f32x4{dw[i][e], dw[i][e + 1], dw[i][e + 2], dw[i][e + 3]};
+                    *reinterpret_cast<f32x4*>(p + a.part_pitch + at + e) =
+                        f32x4{db[i][e], db[i][e + 1], db[i][e + 2], db[i][e + 3]};
+                }
             }
-        if (!gx) continue;
-        for (int c = t + NCH * RT; c < nch; c += RT) add(load_x(c), load_g(c), weights(c));
-        row_sums<RT>(s, red, turn);
-        const float m1 = s[0] / (float)n, m2 = s[1] / (float)n;
-        auto put = [&](int c, const Elems<T, E>& ox, const Elems<T, E>& og, const Elems<W, E>& w) {
-            float v[E];
+    } else {
+        // the row groups' sums in order: group g adds up sums g, g + PER, ... of its chunk
+        __shared__ float sums[2 * E][NT];
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float xh = (to_f32(ox.e[e]) - mean) * rstd, gw = to_f32(og.e[e]) * to_f32(w.e[e]);
-                v[e] = rstd * (gw - __builtin_fmaf(xh, m2, m1));
-            }
-            store_chunk<T>(gx + row * a.ldgx, c * E, n, pack<T>(v));
-        };
-#pragma unroll
-        for (int i = 0; i < NCH; ++i)
-            if (t + i * RT < nch) put(t + i * RT, hx[i], hg[i], hw[i]);
-        for (int c = t + NCH * RT; c < nch; c += RT) put(c, load_x(c), load_g(c), weights(c));
-    }
-    if (!want_w) return;
-    float* p = a.part + ((int64_t)blockIdx.x * PER + threadIdx.x / RT) * 2 * a.part_pitch;
-#pragma unroll
-    for (int i = 0; i < NCH; ++i)
-        if (t + i * RT < nch) {
-            const int at = (t + i * RT) * E;              // part rows hold whole chunks
-#pragma unroll
-            for (int e = 0; e < E; e += 4) {
-                *reinterpret_cast<f32x4*>(p + at + e) = f32x4{dw[i][e], dw[i][e + 1], dw[i][e + 2], dw[i][e + 3]};
-                *reinterpret_cast<f32x4*>(p + a.part_pitch + at + e) = f32x4{db[i][e], db[i][e + 1], db[i][e + 2], db[i][e + 3]};
-            }
+        for (int e = 0; e < E; ++e) {
+            sums[e][threadIdx.x] = dw[0][e];
+            sums[E + e][threadIdx.x] = db[0][e];
         }
+        __syncthreads();
+        for (int e = group; e < 2 * E; e += PER) {
+            float v = 0.0f;
+#pragma unroll
+            for (int k = 0; k < PER; ++k) v += sums[e][k * RT + t];
+            if (t < nch) p[(e < E ? 0 : a.part_pitch) + t * E + e % E] = v;
+        }
+    }
 }
 
 // Sums of dw and db over the rows of one share, for rows too long to be held: a workgroup
@@ -217,14 +326,14 @@ norm_column_sums(NormGradArgs a, int64_t share_rows)
     float s[2 * E] = {};
     if (c * E < n)
         for (int64_t row = first + r; row < last; row += 8) {
-            const Elems<T, E> ox = load_elems<T, E>(static_cast<const T*>(a.x) + row * a.ldx, c * E, n, (T)0.0f);
-            const Elems<T, E> og = load_elems<T, E>(static_cast<const T*>(a.grad_y) + row * a.ldgy, c * E, n, (T)0.0f);
+            float xv[E], gv[E];
+            unpack<T>(load_zero<T>(static_cast<const T*>(a.x) + row * a.ldx, c, n), xv);
+            unpack<T>(load_zero<T>(static_cast<const T*>(a.grad_y) + row * a.ldgy, c, n), gv);
             const float mean = a.mean[row], rstd = a.rstd[row];
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const float g = to_f32(og.e[e]);
-                s[e] = __builtin_fmaf(g, (to_f32(ox.e[e]) - mean) * rstd, s[e]);
-                s[E + e] += g;
+                s[e] = __builtin_fmaf(gv[e], (xv[e] - mean) * rstd, s[e]);
+                s[E + e] += gv[e];
             }
         }
 #pragma unroll

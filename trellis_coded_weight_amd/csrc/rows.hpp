@@ -87,6 +87,59 @@ __device__ __forceinline__ void store_chunk(T* row, int at, int n, u32x4 v)
         if (at + e < n) row[at + e] = o.e[e];
 }
 
+// Where a thread's chunk c of a row of n elements is read: whole chunks where they are, and a
+// last one that is not whole as the row's last 16 bytes, which `behind` then shifts into place.
+// So every load of a row is one instruction with no branch around it (n >= E).
+struct Place { int at, bits; };
+template <typename T>
+__device__ __forceinline__ Place place_of(int c, int n)
+{
+    constexpr int E = 16 / (int)sizeof(T);
+    const int at = c * E, over = at + E - n;
+    return over <= 0 ? Place{at, 0} : Place{n - E, over < E ? over * 8 * (int)sizeof(T) : 128};
+}
+
+// v without its first `bits` bits (0 to 128), zeros behind
+__device__ __forceinline__ u32x4 behind(u32x4 v, int bits)
+{
+    typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+    u64x2 o = __builtin_bit_cast(u64x2, v);
+    const int b = bits & 63;
+    const uint64_t lo = o.x >> b | (o.y << 1) << (63 - b), hi = o.y >> b;
+    o.x = bits < 64 ? lo : (bits < 128 ? hi : 0u);
+    o.y = bits < 64 ? hi : 0u;
+    return __builtin_bit_cast(u32x4, o);
+}
+
+// a row of fewer than E elements, zeros behind it
+template <typename T>
+__device__ __forceinline__ u32x4 load_short(const T* row, int n)
+{
+    constexpr int BITS = 8 * (int)sizeof(T);
+    typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+    u64x2 v = {0u, 0u};
+#pragma unroll 1
+    for (int e = n - 1; e >= 0; --e) {
+        uint64_t o;
+        if constexpr (sizeof(T) == 2)
+            o = __builtin_bit_cast(uint16_t, row[e]);
+        else
+            o = __builtin_bit_cast(uint32_t, row[e]);
+        v.y = v.y << BITS | v.x >> (64 - BITS);
+        v.x = v.x << BITS | o;
+    }
+    return __builtin_bit_cast(u32x4, v);
+}
+
+// chunk c of a row of n elements, zeros behind it
+template <typename T>
+__device__ __forceinline__ u32x4 load_zero(const T* row, int c, int n)
+{
+    if (n < 16 / (int)sizeof(T)) return load_short(row, n);
+    const Place p = place_of<T>(c, n);
+    return behind(load_loose(row + p.at), p.bits);
+}
+
 // 16 bytes at `at` of a row of n, `fill` past its end
 template <typename T>
 __device__ __forceinline__ u32x4 load_filled(const T* row, int at, int n, T fill)
