@@ -133,11 +133,17 @@ fp8_block_product(Fp8Args a)
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(decltype(n)::value) : "memory");
         __builtin_amdgcn_sched_barrier(0);
     };
-    f32x4 acc[FP][4] = {};
-    auto add = [&](int g, int j, const Op& q, const Op& p, float f) {
-        const f32x4 t = Op::mul(q, p);
+    // Product n of a step's 4 FP: the groups in the order above.  Its scaled addition follows LAG
+    // products later, when its result has long come out, with no wait and between the others'
+    // issue.
+    constexpr int LAG = 3, TOTAL = 4 * FP, TAIL = TOTAL - 8;
+    f32x4 acc[FP][4] = {}, sums[LAG + 1];
+    float f[FP];
+    auto issue = [&](int n, const Op& q, const Op& p) { sums[n % (LAG + 1)] = Op::mul(q, p); };
+    auto retire = [&](int n) {
+        const int g = n < TAIL ? n / 4 : FP - 2 + (n - TAIL) % 2, j = n < TAIL ? n % 4 : (n - TAIL) / 2;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[g][j][e] = __builtin_fmaf(t[e], f, acc[g][j][e]);
+        for (int e = 0; e < 4; ++e) acc[g][j][e] = __builtin_fmaf(sums[n % (LAG + 1)][e], f[g], acc[g][j][e]);
     };
     if (s0 < s1) {
 #pragma unroll
@@ -145,7 +151,6 @@ fp8_block_product(Fp8Args a)
         landed(std::integral_constant<int, (R - 1) * LOADS>{});
         Op q[4] = {read_w(0, 0), read_w(0, 1), read_w(0, 2), read_w(0, 3)};
         Op p[2][2] = {{read_a(0, 0), read_a(0, 1)}, {read_a(0, 0), read_a(0, 1)}};
-        float f[FP];
         scales_of(0, f);
         int at = 0;                               // place of step s
         for (int s = s0; s < s1; ++s) {
@@ -156,9 +161,12 @@ fp8_block_product(Fp8Args a)
                 p[(u + 1) & 1][1] = read_a(at, 2 * u + 3);
                 fence();
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) add(2 * u + h, j, q[j], p[u & 1][h], f[2 * u + h]);
+                for (int i = 0; i < 8; ++i) {
+                    const int n = 8 * u + i;
+                    issue(n, q[i % 4], p[u & 1][i / 4]);
+                    if (n >= LAG) retire(n - LAG);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
             landed(std::integral_constant<int, (R - 2) * LOADS>{});
             stage(s + R, at);
@@ -169,10 +177,17 @@ fp8_block_product(Fp8Args a)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) add(FP - 2 + h, j, q[j], p[(PAIRS - 1) & 1][h], f[FP - 2 + h]);
+                for (int h = 0; h < 2; ++h) {
+                    const int n = TAIL + 2 * j + h;
+                    issue(n, q[j], p[(PAIRS - 1) & 1][h]);
+                    if (n >= LAG) retire(n - LAG);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
                 q[j] = read_w(next, j);
                 fence();
             }
+#pragma unroll
+            for (int n = TOTAL - LAG; n < TOTAL; ++n) retire(n);
             p[0][0] = n0;
             p[0][1] = n1;
 #pragma unroll
