@@ -59,13 +59,32 @@ fp8_block_product(Fp8Args a)
     const int steps = (a.k + 127) / 128;
     const int s0 = share * a.share_steps, s1 = s0 + a.share_steps < steps ? s0 + a.share_steps : steps;
 
-    auto rsrc = [](const void* p, int bytes) {
-        const uint64_t at = reinterpret_cast<uint64_t>(p);
+    // What the loads of the next step to be started read: a raw buffer descriptor of each
+    // operand from its tile's row i0 (j0) and the step's k on, and of the scales, moved on by
+    // one step at a time.  Their sizes end with the last row's last byte, or are 0 past the
+    // last step.
+    struct Source { uint64_t at; int bytes; };
+    const int a_rows = (a.m - i0 < ROWS ? a.m - i0 : ROWS), w_rows = (a.n - j0 < Fp8Shape::kCols ? a.n - j0 : Fp8Shape::kCols);
+    const bool of_w = wave == 4;               // its floats are w's two scales, waves 0 .. FP / 2 - 1 have a's
+    const int s_rows = of_w ? (w_rows > 128 ? 2 : 1) : (wave < FP / 2 ? a_rows : 0);
+    const int s_ld = (int)(of_w ? a.ws_row : a.as_row) * 4;
+    const int64_t s_step = (of_w ? a.ws_col : a.as_col) * 4;
+    Source src_a = {reinterpret_cast<uint64_t>(a.a + i0 * a.lda + (int64_t)s0 * 128), (a_rows - 1) * (int)a.lda + a.ak - s0 * 128};
+    Source src_w = {reinterpret_cast<uint64_t>(a.w + j0 * a.ldw + (int64_t)s0 * 128), (w_rows - 1) * (int)a.ldw + a.wk - s0 * 128};
+    uint64_t src_s = reinterpret_cast<uint64_t>(of_w ? a.w_scale + (j0 >> 7) * a.ws_row : a.a_scale + i0 * a.as_row) + s0 * s_step;
+    // where a lane's chunks come from: row 64 h + 8 wave + lane / 8 of a tile
+    const int from_row = 8 * wave + (lane >> 3);
+    const int from_chunk = ((lane & 7) ^ (((wave & 1) << 2) | (lane >> 4))) * 16;
+    const int off_a = from_row * (int)a.lda + from_chunk, off_w = from_row * (int)a.ldw + from_chunk;
+    // a's scales lie as the lanes take them: FP groups' of one row of 16 together
+    const int s_at = wave * 64 + lane, s_row = of_w ? lane : s_at / (16 * FP) * (16 * FP) + s_at % FP * 16 + s_at / FP % 16;
+    const int off_s = s_row < s_rows ? s_row * s_ld : 0x7FFFFFFF;
+    auto rsrc = [](uint64_t at, int bytes) {
         return u32x4{(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu, (uint32_t)bytes, (uint32_t)kRawBufferWord3};
     };
-    // 16 (or 4) bytes a lane from r + off to LDS at dst + 16 (4) lane; counted by `landed`
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
+    // 16 (or 4) bytes a lane from r + off to LDS at dst + 16 (4) lane; counted by `landed`
     auto to_lds = [&](u32x4 r, const char* dst, int off) {
         const uint32_t at = (uint32_t)reinterpret_cast<uintptr_t>((lds_char*)dst);
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
@@ -77,35 +96,27 @@ fp8_block_product(Fp8Args a)
                      ::"s"(at), "v"(off), "s"(r) : "m0", "memory");
     };
 #pragma clang diagnostic pop
-    // where a lane's chunks come from: row 64 h + 8 wave + lane / 8 of a tile
-    const int from_row = 8 * wave + (lane >> 3);
-    const int from_chunk = ((lane & 7) ^ (((wave & 1) << 2) | (lane >> 4))) * 16;
-    // H groups of 64 rows from row0 of `base`, the 128 bytes from k0; zeros past the rows, past
-    // k and where the step is not there
-    auto stage_rows = [&](bool there, const uint8_t* base, int64_t ld, int row0, int nrows, int k, int k0, char* dst, auto hr) {
-        constexpr int H = decltype(hr)::value;
-        const int left = there ? k - k0 : 0;
-        const u32x4 r = rsrc(base + row0 * ld + k0, (nrows - row0 < 64 * H ? nrows - row0 - 1 : 64 * H - 1) * (int)ld + left);
-        const int off = from_chunk < left ? from_row * (int)ld + from_chunk : 0x7FFFFFFF;
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-            to_lds(r, dst + (64 * h + 8 * wave) * 128, off == 0x7FFFFFFF ? off : off + h * 64 * (int)ld);
-    };
-    // step s into place i: a's tile, w's, then a float a lane of the scales: waves 0 .. FP / 2 - 1
-    // a's rows, wave 4 w's two blocks of columns, the others nothing
-    auto stage = [&](int s, int i) {
+    // load l of step s into place i: a's tile, w's, then the scales
+    auto stage = [&](int s, int i, int l) {
         char* dst = lds + i * STEP;
         const bool there = s < s1;
-        const int b = there ? s : s0;
-        stage_rows(there, a.a, a.lda, i0, a.m, a.ak, b * 128, dst, std::integral_constant<int, FP / 2>{});
-        stage_rows(there, a.w, a.ldw, j0, a.n, a.wk, b * 128, dst + TP, std::integral_constant<int, 4>{});
-        const bool of_w = wave == 4;
-        const int row = of_w ? lane : wave * 64 + lane;
-        const int rows = of_w ? (a.n - j0 > 128 ? 2 : 1) : (wave < FP / 2 ? (a.m - i0 < ROWS ? a.m - i0 : ROWS) : 0);
-        const int64_t ld = of_w ? a.ws_row : a.as_row;
-        const float* base = of_w ? a.w_scale + (j0 >> 7) * a.ws_row + b * a.ws_col : a.a_scale + i0 * a.as_row + b * a.as_col;
-        const u32x4 r = rsrc(base, there && rows > 0 ? ((rows - 1) * (int)ld + 1) * 4 : 0);
-        to_lds4(r, dst + TP + TQ + wave * 256, row < rows ? row * (int)ld * 4 : 0x7FFFFFFF);
+        if (l < LP + LQ) {
+            const bool is_a = l < LP;
+            const int h = is_a ? l : l - LP, k = is_a ? a.ak : a.wk;
+            const Source& o = is_a ? src_a : src_w;
+            const int off = (is_a ? off_a : off_w) + h * 64 * (int)(is_a ? a.lda : a.ldw);
+            // a chunk past the row's end goes out of range
+            to_lds(rsrc(o.at, there ? o.bytes : 0), dst + (is_a ? 0 : TP) + (64 * h + 8 * wave) * 128,
+                   from_chunk < k - s * 128 ? off : 0x7FFFFFFF);
+        } else {
+            to_lds4(rsrc(src_s, there && s_rows > 0 ? (s_rows - 1) * s_ld + 4 : 0), dst + TP + TQ + wave * 256, off_s);
+        }
+    };
+    // on to the step after
+    auto advance = [&] {
+        src_a.at += 128, src_a.bytes -= 128;
+        src_w.at += 128, src_w.bytes -= 128;
+        src_s += s_step;
     };
 
     // LDS address of a lane's two chunks of a row group
@@ -118,8 +129,10 @@ fp8_block_product(Fp8Args a)
     auto scales_of = [&](int i, float (&f)[FP]) {
         const float* s = reinterpret_cast<const float*>(lds + i * STEP + TP + TQ);
         const float t = s[256 + (wn >> 1)];
+        struct __attribute__((aligned(FP < 4 ? 8 : 16))) Lane { float f[FP]; };
+        const Lane l = reinterpret_cast<const Lane*>(s)[wm * 16 + (lane & 15)];
 #pragma unroll
-        for (int g = 0; g < FP; ++g) f[g] = s[(wm * FP + g) * 16 + (lane & 15)] * t;
+        for (int g = 0; g < FP; ++g) f[g] = l.f[g] * t;
     };
     // reads are issued ahead of the matrix instructions that follow
     auto fence = [] {
@@ -147,7 +160,11 @@ fp8_block_product(Fp8Args a)
     };
     if (s0 < s1) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) stage(s0 + i, i);
+        for (int i = 0; i < R; ++i) {
+#pragma unroll
+            for (int l = 0; l < LOADS; ++l) stage(s0 + i, i, l);
+            advance();
+        }
         landed(std::integral_constant<int, (R - 1) * LOADS>{});
         Op q[4] = {read_w(0, 0), read_w(0, 1), read_w(0, 2), read_w(0, 3)};
         Op p[2][2] = {{read_a(0, 0), read_a(0, 1)}, {read_a(0, 0), read_a(0, 1)}};
@@ -169,23 +186,26 @@ fp8_block_product(Fp8Args a)
                 }
             }
             landed(std::integral_constant<int, (R - 2) * LOADS>{});
-            stage(s + R, at);
             const Op n0 = read_a(next, 0), n1 = read_a(next, 1);
             float nf[FP];
             scales_of(next, nf);
             fence();
+            // the loads' issue goes between that of the products
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int n = TAIL + 2 * j + h;
                     issue(n, q[j], p[(PAIRS - 1) & 1][h]);
+#pragma unroll
+                    for (int l = (2 * j + h) * LOADS / 8; l < (2 * j + h + 1) * LOADS / 8; ++l) stage(s + R, at, l);
                     if (n >= LAG) retire(n - LAG);
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 q[j] = read_w(next, j);
                 fence();
             }
+            advance();
 #pragma unroll
             for (int n = TOTAL - LAG; n < TOTAL; ++n) retire(n);
             p[0][0] = n0;
