@@ -126,13 +126,12 @@ fp8_block_product(Fp8Args a)
     };
     auto read_a = [&](int i, int g) { return read(lds + i * STEP, (wm * FP + g) * 16); };
     auto read_w = [&](int i, int g) { return read(lds + i * STEP + TP, wn * 64 + g * 16); };
-    auto scales_of = [&](int i, float (&f)[FP]) {
-        const float* s = reinterpret_cast<const float*>(lds + i * STEP + TP + TQ);
-        const float t = s[256 + (wn >> 1)];
-        struct __attribute__((aligned(FP < 4 ? 8 : 16))) Lane { float f[FP]; };
-        const Lane l = reinterpret_cast<const Lane*>(s)[wm * 16 + (lane & 15)];
-#pragma unroll
-        for (int g = 0; g < FP; ++g) f[g] = l.f[g] * t;
+    // a step's scales as they lie in LDS: of a lane's FP rows of a, and of the wave's block of w
+    struct __attribute__((aligned(FP < 4 ? 8 : 16))) RowScales { float f[FP]; };
+    struct Scales { RowScales a; float w; };
+    auto read_scales = [&](int i) {
+        const char* s = lds + i * STEP + TP + TQ;
+        return Scales{reinterpret_cast<const RowScales*>(s)[wm * 16 + (lane & 15)], reinterpret_cast<const float*>(s)[256 + (wn >> 1)]};
     };
     // reads are issued ahead of the matrix instructions that follow
     auto fence = [] {
@@ -146,17 +145,26 @@ fp8_block_product(Fp8Args a)
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(decltype(n)::value) : "memory");
         __builtin_amdgcn_sched_barrier(0);
     };
-    // Product n of a step's 4 FP: the groups in the order above.  Its scaled addition follows LAG
-    // products later, when its result has long come out, with no wait and between the others'
-    // issue.
+    // Product n of a step's 4 FP: rows' group 2 (n / 8) + n % 2 by w's group n % 8 / 2, so that
+    // a group of w is needed as late as can be after it was read.  Its scaled addition follows
+    // LAG products later (into the next step for the last ones), when its result has come out:
+    // no wait for it, and between the issue of others.
     constexpr int LAG = 3, TOTAL = 4 * FP, TAIL = TOTAL - 8;
-    f32x4 acc[FP][4] = {}, sums[LAG + 1];
-    float f[FP];
+    f32x4 acc[FP][4] = {}, sums[LAG + 1] = {};
+    float f[FP], late[2] = {0.0f, 0.0f};          // scales, and the last two of the step before
     auto issue = [&](int n, const Op& q, const Op& p) { sums[n % (LAG + 1)] = Op::mul(q, p); };
-    auto retire = [&](int n) {
-        const int g = n < TAIL ? n / 4 : FP - 2 + (n - TAIL) % 2, j = n < TAIL ? n % 4 : (n - TAIL) / 2;
+    auto add = [&](int n, float scale) {
+        const int g = 2 * (n / 8) + n % 2, j = n % 8 / 2;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[g][j][e] = __builtin_fmaf(sums[n % (LAG + 1)][e], f[g], acc[g][j][e]);
+        for (int e = 0; e < 4; ++e) acc[g][j][e] = __builtin_fmaf(sums[n % (LAG + 1)][e], scale, acc[g][j][e]);
+    };
+    // what follows product n
+    auto retire = [&](int n) {
+        if (n >= LAG)
+            add(n - LAG, f[2 * ((n - LAG) / 8) + (n - LAG) % 2]);
+        else
+            add(TOTAL + n - LAG, late[(TOTAL + n - LAG) % 2]);
+        __builtin_amdgcn_sched_barrier(0);
     };
     if (s0 < s1) {
 #pragma unroll
@@ -168,7 +176,11 @@ fp8_block_product(Fp8Args a)
         landed(std::integral_constant<int, (R - 1) * LOADS>{});
         Op q[4] = {read_w(0, 0), read_w(0, 1), read_w(0, 2), read_w(0, 3)};
         Op p[2][2] = {{read_a(0, 0), read_a(0, 1)}, {read_a(0, 0), read_a(0, 1)}};
-        scales_of(0, f);
+        {
+            const Scales c = read_scales(0);
+#pragma unroll
+            for (int g = 0; g < FP; ++g) f[g] = c.a.f[g] * c.w;
+        }
         int at = 0;                               // place of step s
         for (int s = s0; s < s1; ++s) {
             const int next = at + 1 < R ? at + 1 : 0;
@@ -179,41 +191,40 @@ fp8_block_product(Fp8Args a)
                 fence();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int n = 8 * u + i;
-                    issue(n, q[i % 4], p[u & 1][i / 4]);
-                    if (n >= LAG) retire(n - LAG);
-                    __builtin_amdgcn_sched_barrier(0);
+                    issue(8 * u + i, q[i / 2], p[u & 1][i % 2]);
+                    retire(8 * u + i);
                 }
             }
             landed(std::integral_constant<int, (R - 2) * LOADS>{});
-            const Op n0 = read_a(next, 0), n1 = read_a(next, 1);
-            float nf[FP];
-            scales_of(next, nf);
-            fence();
-            // the loads' issue goes between that of the products
+            // the last pair: products at once, and between them the reads of the next step (a group
+            // of w as the one of this step is done with) and the loads' issue
+            Op n0 = p[0][0], n1 = p[0][1];
+            Scales c = {};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int n = TAIL + 2 * j + h;
-                    issue(n, q[j], p[(PAIRS - 1) & 1][h]);
-#pragma unroll
-                    for (int l = (2 * j + h) * LOADS / 8; l < (2 * j + h + 1) * LOADS / 8; ++l) stage(s + R, at, l);
-                    if (n >= LAG) retire(n - LAG);
-                    __builtin_amdgcn_sched_barrier(0);
+            for (int i = 0; i < 8; ++i) {
+                issue(TAIL + i, q[i / 2], p[(PAIRS - 1) & 1][i % 2]);
+                if (i == 1) {
+                    n0 = read_a(next, 0);
+                    n1 = read_a(next, 1);
+                    c = read_scales(next);
                 }
-                q[j] = read_w(next, j);
-                fence();
+                if (i % 2 == 1) q[i / 2] = read_w(next, i / 2);
+#pragma unroll
+                for (int l = i * LOADS / 8; l < (i + 1) * LOADS / 8; ++l) stage(s + R, at, l);
+                asm volatile("" ::: "memory");
+                retire(TAIL + i);
             }
             advance();
+            late[0] = f[FP - 2];
+            late[1] = f[FP - 1];
 #pragma unroll
-            for (int n = TOTAL - LAG; n < TOTAL; ++n) retire(n);
+            for (int g = 0; g < FP; ++g) f[g] = c.a.f[g] * c.w;
             p[0][0] = n0;
             p[0][1] = n1;
-#pragma unroll
-            for (int g = 0; g < FP; ++g) f[g] = nf[g];
             at = next;
         }
+#pragma unroll
+        for (int n = 0; n < LAG; ++n) add(TOTAL + n - LAG, late[(TOTAL + n - LAG) % 2]);
         // nothing may still be on its way to LDS when the workgroup ends
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
