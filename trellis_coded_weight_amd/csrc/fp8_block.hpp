@@ -9,10 +9,10 @@
 // that read one chunk of 16 rows at once touch 16 different places of the 256-byte bank row.
 //
 // Within a step a wave holds its four groups of 16 rows of w in registers and takes its rows of
-// a two groups at a time, the next two on their way from LDS meanwhile.  Before the last two
-// all reads of the step are done: wait until the next step has landed, barrier, start the
-// loads of a later step into the places just left; then the last two groups go through w's
-// four one by one, each of which is replaced by the next step's as it is done with.
+// a two groups at a time, the next two on their way from LDS meanwhile.  When the last two
+// are read, all reads of the step are done: wait until the next step has landed, barrier, and
+// between the products that are left start the loads of a later step into the places just
+// left and read the next step's first groups, each of w's as this step's is done with.
 //
 // A block's sums must be scaled before they are added to the result's, which are therefore
 // ordinary vector registers: one fused multiply-add an element and block beside the matrix
@@ -59,65 +59,75 @@ fp8_block_product(Fp8Args a)
     const int steps = (a.k + 127) / 128;
     const int s0 = share * a.share_steps, s1 = s0 + a.share_steps < steps ? s0 + a.share_steps : steps;
 
-    // What the loads of the next step to be started read: a raw buffer descriptor of each
+    // What the loads of the step to be started next read: raw buffer descriptors of each
     // operand from its tile's row i0 (j0) and the step's k on, and of the scales, moved on by
     // one step at a time.  Their sizes end with the last row's last byte, or are 0 past the
     // last step.
-    struct Source { uint64_t at; int bytes; };
-    const int a_rows = (a.m - i0 < ROWS ? a.m - i0 : ROWS), w_rows = (a.n - j0 < Fp8Shape::kCols ? a.n - j0 : Fp8Shape::kCols);
+    const int a_rows = a.m - i0 < ROWS ? a.m - i0 : ROWS, w_rows = a.n - j0 < Fp8Shape::kCols ? a.n - j0 : Fp8Shape::kCols;
     const bool of_w = wave == 4;               // its floats are w's two scales, waves 0 .. FP / 2 - 1 have a's
     const int s_rows = of_w ? (w_rows > 128 ? 2 : 1) : (wave < FP / 2 ? a_rows : 0);
     const int s_ld = (int)(of_w ? a.ws_row : a.as_row) * 4;
     const int64_t s_step = (of_w ? a.ws_col : a.as_col) * 4;
-    Source src_a = {reinterpret_cast<uint64_t>(a.a + i0 * a.lda + (int64_t)s0 * 128), (a_rows - 1) * (int)a.lda + a.ak - s0 * 128};
-    Source src_w = {reinterpret_cast<uint64_t>(a.w + j0 * a.ldw + (int64_t)s0 * 128), (w_rows - 1) * (int)a.ldw + a.wk - s0 * 128};
-    uint64_t src_s = reinterpret_cast<uint64_t>(of_w ? a.w_scale + (j0 >> 7) * a.ws_row : a.a_scale + i0 * a.as_row) + s0 * s_step;
+    auto rsrc = [](const void* p, int bytes) {
+        const uint64_t at = reinterpret_cast<uint64_t>(p);
+        return u32x4{(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu, (uint32_t)bytes, (uint32_t)kRawBufferWord3};
+    };
+    u32x4 src_a = rsrc(a.a + i0 * a.lda + (int64_t)s0 * 128, (a_rows - 1) * (int)a.lda + a.ak - s0 * 128);
+    u32x4 src_w = rsrc(a.w + j0 * a.ldw + (int64_t)s0 * 128, (w_rows - 1) * (int)a.ldw + a.wk - s0 * 128);
+    u32x4 src_s = rsrc(reinterpret_cast<const char*>(of_w ? a.w_scale + (j0 >> 7) * a.ws_row : a.a_scale + i0 * a.as_row) + s0 * s_step,
+                       s_rows > 0 ? (s_rows - 1) * s_ld + 4 : 0);
     // where a lane's chunks come from: row 64 h + 8 wave + lane / 8 of a tile
     const int from_row = 8 * wave + (lane >> 3);
     const int from_chunk = ((lane & 7) ^ (((wave & 1) << 2) | (lane >> 4))) * 16;
-    const int off_a = from_row * (int)a.lda + from_chunk, off_w = from_row * (int)a.ldw + from_chunk;
+    int off_a[LP], off_w[LQ];
+#pragma unroll
+    for (int h = 0; h < LP; ++h) off_a[h] = (from_row + 64 * h) * (int)a.lda + from_chunk;
+#pragma unroll
+    for (int h = 0; h < LQ; ++h) off_w[h] = (from_row + 64 * h) * (int)a.ldw + from_chunk;
     // a's scales lie as the lanes take them: FP groups' of one row of 16 together
     const int s_at = wave * 64 + lane, s_row = of_w ? lane : s_at / (16 * FP) * (16 * FP) + s_at % FP * 16 + s_at / FP % 16;
     const int off_s = s_row < s_rows ? s_row * s_ld : 0x7FFFFFFF;
-    auto rsrc = [](uint64_t at, int bytes) {
-        return u32x4{(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu, (uint32_t)bytes, (uint32_t)kRawBufferWord3};
+    // where k ends inside step s, chunks past the rows' ends go out of range
+    auto mask_end = [&](int s) {
+        const bool in_a = from_chunk < a.ak - s * 128, in_w = from_chunk < a.wk - s * 128;
+#pragma unroll
+        for (int h = 0; h < LP; ++h) off_a[h] = in_a ? off_a[h] : 0x7FFFFFFF;
+#pragma unroll
+        for (int h = 0; h < LQ; ++h) off_w[h] = in_w ? off_w[h] : 0x7FFFFFFF;
     };
+    // the descriptors on to step s, which may be past the last
+    auto advance = [&](int s) {
+        auto add = [](u32x4& r, int64_t n) {
+            const uint64_t at = (r.x | (uint64_t)r.y << 32) + n;
+            r.x = (uint32_t)at;
+            r.y = (uint32_t)(at >> 32) & 0xFFFFu;
+        };
+        add(src_a, 128);
+        add(src_w, 128);
+        add(src_s, s_step);
+        const bool there = s < s1;
+        src_a.z = there ? src_a.z - 128 : 0;
+        src_w.z = there ? src_w.z - 128 : 0;
+        src_s.z = there ? src_s.z : 0;
+        mask_end(s);
+    };
+    // Load l of a step: 16 bytes a lane of a's tile, then of w's, then a float of the scales,
+    // from the descriptors to the places of LDS that start at `place` + 1 KB a wave.  Counted
+    // by `landed`.
+    const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((lds_char*)lds);
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-    // 16 (or 4) bytes a lane from r + off to LDS at dst + 16 (4) lane; counted by `landed`
-    auto to_lds = [&](u32x4 r, const char* dst, int off) {
-        const uint32_t at = (uint32_t)reinterpret_cast<uintptr_t>((lds_char*)dst);
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                     ::"s"(at), "v"(off), "s"(r) : "m0", "memory");
-    };
-    auto to_lds4 = [&](u32x4 r, const char* dst, int off) {
-        const uint32_t at = (uint32_t)reinterpret_cast<uintptr_t>((lds_char*)dst);
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-                     ::"s"(at), "v"(off), "s"(r) : "m0", "memory");
+    auto stage = [&](int i, int l) {
+        const uint32_t at = lds0 + i * STEP + (l < LP + LQ ? wave * 1024 : wave * 256);
+        if (l < LP + LQ)
+            asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                         ::"s"(at), "v"(l < LP ? off_a[l] : off_w[l - LP]), "s"(l < LP ? src_a : src_w),
+                         "i"(l < LP ? l * 8192 : TP + (l - LP) * 8192) : "m0", "scc", "memory");
+        else
+            asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                         ::"s"(at), "v"(off_s), "s"(src_s), "i"(TP + TQ) : "m0", "scc", "memory");
     };
 #pragma clang diagnostic pop
-    // load l of step s into place i: a's tile, w's, then the scales
-    auto stage = [&](int s, int i, int l) {
-        char* dst = lds + i * STEP;
-        const bool there = s < s1;
-        if (l < LP + LQ) {
-            const bool is_a = l < LP;
-            const int h = is_a ? l : l - LP, k = is_a ? a.ak : a.wk;
-            const Source& o = is_a ? src_a : src_w;
-            const int off = (is_a ? off_a : off_w) + h * 64 * (int)(is_a ? a.lda : a.ldw);
-            // a chunk past the row's end goes out of range
-            to_lds(rsrc(o.at, there ? o.bytes : 0), dst + (is_a ? 0 : TP) + (64 * h + 8 * wave) * 128,
-                   from_chunk < k - s * 128 ? off : 0x7FFFFFFF);
-        } else {
-            to_lds4(rsrc(src_s, there && s_rows > 0 ? (s_rows - 1) * s_ld + 4 : 0), dst + TP + TQ + wave * 256, off_s);
-        }
-    };
-    // on to the step after
-    auto advance = [&] {
-        src_a.at += 128, src_a.bytes -= 128;
-        src_w.at += 128, src_w.bytes -= 128;
-        src_s += s_step;
-    };
 
     // LDS address of a lane's two chunks of a row group
     const int at0 = (lane & 15) * 128 + (((lane >> 4) ^ ((lane >> 1) & 7)) * 16), at1 = at0 ^ 64;
@@ -167,11 +177,12 @@ fp8_block_product(Fp8Args a)
         __builtin_amdgcn_sched_barrier(0);
     };
     if (s0 < s1) {
+        mask_end(s0);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
 #pragma unroll
-            for (int l = 0; l < LOADS; ++l) stage(s0 + i, i, l);
-            advance();
+            for (int l = 0; l < LOADS; ++l) stage(i, l);
+            advance(s0 + i + 1);
         }
         landed(std::integral_constant<int, (R - 1) * LOADS>{});
         Op q[4] = {read_w(0, 0), read_w(0, 1), read_w(0, 2), read_w(0, 3)};
@@ -181,40 +192,38 @@ fp8_block_product(Fp8Args a)
 #pragma unroll
             for (int g = 0; g < FP; ++g) f[g] = c.a.f[g] * c.w;
         }
+        // product AT is the first behind the barrier: four after the reads of the last pair
+        constexpr int AT = TOTAL > 12 ? TOTAL - 12 : 0;
         int at = 0;                               // place of step s
         for (int s = s0; s < s1; ++s) {
             const int next = at + 1 < R ? at + 1 : 0;
-#pragma unroll
-            for (int u = 0; u < PAIRS - 1; ++u) {
-                p[(u + 1) & 1][0] = read_a(at, 2 * u + 2);
-                p[(u + 1) & 1][1] = read_a(at, 2 * u + 3);
-                fence();
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    issue(8 * u + i, q[i / 2], p[u & 1][i % 2]);
-                    retire(8 * u + i);
-                }
-            }
-            landed(std::integral_constant<int, (R - 2) * LOADS>{});
-            // the last pair: products at once, and between them the reads of the next step (a group
-            // of w as the one of this step is done with) and the loads' issue
             Op n0 = p[0][0], n1 = p[0][1];
             Scales c = {};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                issue(TAIL + i, q[i / 2], p[(PAIRS - 1) & 1][i % 2]);
-                if (i == 1) {
+            for (int n = 0; n < TOTAL; ++n) {
+                const int u = n / 8, i = n % 8;
+                if (i == 0 && u < PAIRS - 1) {
+                    p[(u + 1) & 1][0] = read_a(at, 2 * u + 2);
+                    p[(u + 1) & 1][1] = read_a(at, 2 * u + 3);
+                    fence();
+                }
+                if (n == AT) landed(std::integral_constant<int, (R - 2) * LOADS>{});
+                issue(n, q[i / 2], p[u & 1][i % 2]);
+                // beside the products: the loads of a later step into the places just left, and the
+                // reads of the next step, a group of w as the one of this step is done with
+#pragma unroll
+                for (int l = 0; l < LOADS; ++l)
+                    if (n == AT + l * (TOTAL - AT) / LOADS) stage(at, l);
+                if (n == TAIL + 1) {
                     n0 = read_a(next, 0);
                     n1 = read_a(next, 1);
                     c = read_scales(next);
                 }
-                if (i % 2 == 1) q[i / 2] = read_w(next, i / 2);
-#pragma unroll
-                for (int l = i * LOADS / 8; l < (i + 1) * LOADS / 8; ++l) stage(s + R, at, l);
+                if (n >= TAIL && i % 2 == 1) q[i / 2] = read_w(next, i / 2);
                 asm volatile("" ::: "memory");
-                retire(TAIL + i);
+                retire(n);
             }
-            advance();
+            advance(s + R + 1);
             late[0] = f[FP - 2];
             late[1] = f[FP - 1];
 #pragma unroll
