@@ -1,14 +1,14 @@
 // fp8_block.hpp -- the product of e4m3 matrices with block scales for any number of rows, in
-// workgroup tiles of 32 FP x 256 (FP = 8, 4, 2), for operands whose rows start on 16 bytes and
+// workgroup tiles of 32 FP x 64 QG (256 or 128 columns), for operands whose rows start on 16 bytes and
 // hold whole 16-byte chunks, gfx950.
 //
-// Eight waves, 2 x 4, each 16 FP rows of a by 64 rows of w.  A step is one block of 128 of k.
-// Its tiles (a's 4 FP KB, w's 32 KB) and its scales go from memory straight to LDS, into a ring
-// of 2 (FP = 8) or 3 places, so the next one or two steps are on their way during a step.
+// Eight waves, 2 x 4, each 16 FP rows of a by 16 QG rows of w.  A step is one block of 128 of
+// k.  Its tiles (a's 4 FP KB, w's 8 QG KB) and its scales go from memory straight to LDS, into a ring
+// of 2 to 4 places, so the next one to three steps are on their way during a step.
 // LDS rows are 128 bytes, their 16-byte chunk c at place c ^ ((row >> 1) & 7): the 16 lanes
 // that read one chunk of 16 rows at once touch 16 different places of the 256-byte bank row.
 //
-// Within a step a wave holds its four groups of 16 rows of w in registers and takes its rows of
+// Within a step a wave holds its QG groups of 16 rows of w in registers and takes its rows of
 // a two groups at a time, the next two on their way from LDS meanwhile.  When the last two
 // are read, all reads of the step are done: wait until the next step has landed, barrier, and
 // between the products that are left start the loads of a later step into the places just
@@ -29,24 +29,26 @@
 
 namespace qtcq {
 
+// FP: 32 FP rows a tile; QG: 64 QG columns (a wave's groups of 16 rows of w).
 struct Fp8Shape {
     static constexpr int kThreads = 512;
-    static constexpr int kCols = 256;
     static constexpr int kScales = 2048;      // bytes of a step's scales: 64 floats a wave
     static constexpr int rows(int fp) { return 32 * fp; }
-    static constexpr int places(int fp) { return fp == 8 ? 2 : 3; }
-    static constexpr int step_bytes(int fp) { return (rows(fp) + kCols) * 128 + kScales; }
+    static constexpr int cols(int qg) { return 64 * qg; }
+    static constexpr int places(int fp, int qg) { return fp == 8 ? 2 : (qg == 4 ? 3 : 4); }
+    static constexpr int step_bytes(int fp, int qg) { return (rows(fp) + cols(qg)) * 128 + kScales; }
 };
 
 // grid.x = shares * tiles, block = 512
-template <typename O, int FP, bool FAST>
+template <typename O, int FP, int QG, bool FAST>
 __global__ void __launch_bounds__(Fp8Shape::kThreads)
 fp8_block_product(Fp8Args a)
 {
     typedef BlockOperand<FAST> Op;
-    constexpr int ROWS = Fp8Shape::rows(FP), R = Fp8Shape::places(FP), STEP = Fp8Shape::step_bytes(FP);
-    constexpr int TP = ROWS * 128, TQ = Fp8Shape::kCols * 128;
-    constexpr int LP = FP / 2, LQ = 4, LOADS = LP + LQ + 1;      // loads of a step by one wave
+    constexpr int ROWS = Fp8Shape::rows(FP), COLS = Fp8Shape::cols(QG);
+    constexpr int R = Fp8Shape::places(FP, QG), STEP = Fp8Shape::step_bytes(FP, QG);
+    constexpr int TP = ROWS * 128, TQ = COLS * 128;
+    constexpr int LP = FP / 2, LQ = QG, LOADS = LP + LQ + 1;     // loads of a step by one wave
     constexpr int PAIRS = FP / 2;
     __shared__ __align__(1024) char lds[R * STEP];
 
@@ -54,8 +56,8 @@ fp8_block_product(Fp8Args a)
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
     int share, ti, tj;
-    block_tile(blockIdx.x, a.shares, (a.m + ROWS - 1) / ROWS, (a.n + Fp8Shape::kCols - 1) / Fp8Shape::kCols, share, ti, tj);
-    const int i0 = ti * ROWS, j0 = tj * Fp8Shape::kCols;
+    block_tile(blockIdx.x, a.shares, (a.m + ROWS - 1) / ROWS, (a.n + COLS - 1) / COLS, share, ti, tj);
+    const int i0 = ti * ROWS, j0 = tj * COLS;
     const int steps = (a.k + 127) / 128;
     const int s0 = share * a.share_steps, s1 = s0 + a.share_steps < steps ? s0 + a.share_steps : steps;
 
@@ -63,7 +65,7 @@ fp8_block_product(Fp8Args a)
     // operand from its tile's row i0 (j0) and the step's k on, and of the scales, moved on by
     // one step at a time.  Their sizes end with the last row's last byte, or are 0 past the
     // last step.
-    const int a_rows = a.m - i0 < ROWS ? a.m - i0 : ROWS, w_rows = a.n - j0 < Fp8Shape::kCols ? a.n - j0 : Fp8Shape::kCols;
+    const int a_rows = a.m - i0 < ROWS ? a.m - i0 : ROWS, w_rows = a.n - j0 < COLS ? a.n - j0 : COLS;
     const bool of_w = wave == 4;               // its floats are w's two scales, waves 0 .. FP / 2 - 1 have a's
     const int s_rows = of_w ? (w_rows > 128 ? 2 : 1) : (wave < FP / 2 ? a_rows : 0);
     const int s_ld = (int)(of_w ? a.ws_row : a.as_row) * 4;
@@ -135,13 +137,13 @@ fp8_block_product(Fp8Args a)
         return Op(*reinterpret_cast<const u32x4*>(tile + row * 128 + at0), *reinterpret_cast<const u32x4*>(tile + row * 128 + at1));
     };
     auto read_a = [&](int i, int g) { return read(lds + i * STEP, (wm * FP + g) * 16); };
-    auto read_w = [&](int i, int g) { return read(lds + i * STEP + TP, wn * 64 + g * 16); };
+    auto read_w = [&](int i, int g) { return read(lds + i * STEP + TP, wn * 16 * QG + g * 16); };
     // a step's scales as they lie in LDS: of a lane's FP rows of a, and of the wave's block of w
     struct __attribute__((aligned(FP < 4 ? 8 : 16))) RowScales { float f[FP]; };
     struct Scales { RowScales a; float w; };
     auto read_scales = [&](int i) {
         const char* s = lds + i * STEP + TP + TQ;
-        return Scales{reinterpret_cast<const RowScales*>(s)[wm * 16 + (lane & 15)], reinterpret_cast<const float*>(s)[256 + (wn >> 1)]};
+        return Scales{reinterpret_cast<const RowScales*>(s)[wm * 16 + (lane & 15)], reinterpret_cast<const float*>(s)[256 + (wn * 16 * QG >> 7)]};
     };
     // reads are issued ahead of the matrix instructions that follow
     auto fence = [] {
@@ -155,23 +157,23 @@ fp8_block_product(Fp8Args a)
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(decltype(n)::value) : "memory");
         __builtin_amdgcn_sched_barrier(0);
     };
-    // Product n of a step's 4 FP: rows' group 2 (n / 8) + n % 2 by w's group n % 8 / 2, so that
-    // a group of w is needed as late as can be after it was read.  Its scaled addition follows
+    // Product n of a step's QG FP: rows' group 2 (n / PAIR) + n % 2 by w's group n % PAIR / 2, so
+    // that a group of w is needed as late as can be after it was read.  Its scaled addition follows
     // LAG products later (into the next step for the last ones), when its result has come out:
     // no wait for it, and between the issue of others.
-    constexpr int LAG = 3, TOTAL = 4 * FP, TAIL = TOTAL - 8;
-    f32x4 acc[FP][4] = {}, sums[LAG + 1] = {};
+    constexpr int LAG = 3, PAIR = 2 * QG, TOTAL = QG * FP, TAIL = TOTAL - PAIR;
+    f32x4 acc[FP][QG] = {}, sums[LAG + 1] = {};
     float f[FP], late[2] = {0.0f, 0.0f};          // scales, and the last two of the step before
     auto issue = [&](int n, const Op& q, const Op& p) { sums[n % (LAG + 1)] = Op::mul(q, p); };
     auto add = [&](int n, float scale) {
-        const int g = 2 * (n / 8) + n % 2, j = n % 8 / 2;
+        const int g = 2 * (n / PAIR) + n % 2, j = n % PAIR / 2;
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[g][j][e] = __builtin_fmaf(sums[n % (LAG + 1)][e], scale, acc[g][j][e]);
     };
     // what follows product n
     auto retire = [&](int n) {
         if (n >= LAG)
-            add(n - LAG, f[2 * ((n - LAG) / 8) + (n - LAG) % 2]);
+            add(n - LAG, f[2 * ((n - LAG) / PAIR) + (n - LAG) % 2]);
         else
             add(TOTAL + n - LAG, late[(TOTAL + n - LAG) % 2]);
         __builtin_amdgcn_sched_barrier(0);
@@ -185,15 +187,17 @@ fp8_block_product(Fp8Args a)
             advance(s0 + i + 1);
         }
         landed(std::integral_constant<int, (R - 1) * LOADS>{});
-        Op q[4] = {read_w(0, 0), read_w(0, 1), read_w(0, 2), read_w(0, 3)};
+        Op q[QG];
+#pragma unroll
+        for (int j = 0; j < QG; ++j) q[j] = read_w(0, j);
         Op p[2][2] = {{read_a(0, 0), read_a(0, 1)}, {read_a(0, 0), read_a(0, 1)}};
         {
             const Scales c = read_scales(0);
 #pragma unroll
             for (int g = 0; g < FP; ++g) f[g] = c.a.f[g] * c.w;
         }
-        // product AT is the first behind the barrier: four after the reads of the last pair
-        constexpr int AT = TOTAL > 12 ? TOTAL - 12 : 0;
+        // product AT is the first behind the barrier: six after the reads of the last pair
+        constexpr int AT = TOTAL > 10 ? TOTAL - 10 : 0;
         int at = 0;                               // place of step s
         for (int s = s0; s < s1; ++s) {
             const int next = at + 1 < R ? at + 1 : 0;
@@ -201,7 +205,7 @@ fp8_block_product(Fp8Args a)
             Scales c = {};
 #pragma unroll
             for (int n = 0; n < TOTAL; ++n) {
-                const int u = n / 8, i = n % 8;
+                const int u = n / PAIR, i = n % PAIR;
                 if (i == 0 && u < PAIRS - 1) {
                     p[(u + 1) & 1][0] = read_a(at, 2 * u + 2);
                     p[(u + 1) & 1][1] = read_a(at, 2 * u + 3);
@@ -239,22 +243,22 @@ fp8_block_product(Fp8Args a)
     }
 
     // a lane's results: rows row0 + 16 g, four columns from col0 + 16 j
-    const int row0 = i0 + wm * FP * 16 + (lane & 15), col0 = j0 + wn * 64 + 4 * (lane >> 4);
+    const int row0 = i0 + wm * FP * 16 + (lane & 15), col0 = j0 + wn * 16 * QG + 4 * (lane >> 4);
     if (a.part) {
 #pragma unroll
         for (int g = 0; g < FP; ++g) {
             const int row = row0 + g * 16;
             if (row >= a.m) continue;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < QG; ++j) {
                 const int col = col0 + j * 16;
                 if (col < a.n)
                     *reinterpret_cast<f32x4*>(a.part + ((int64_t)share * a.m + row) * a.part_pitch + col) = acc[g][j];
             }
         }
-    } else if (sizeof(O) == 2 && i0 + ROWS <= a.m && j0 + Fp8Shape::kCols <= a.n) {
+    } else if (sizeof(O) == 2 && i0 + ROWS <= a.m && j0 + COLS <= a.n) {
         // a whole tile of 16-bit results goes out through LDS, in whole rows of the tile
-        constexpr int PITCH = Fp8Shape::kCols * 2 + 16;
+        constexpr int PITCH = COLS * 2 + 16;
         static_assert(ROWS * PITCH <= R * STEP, "the tile fits LDS");
         struct __attribute__((aligned(8))) Four { O e[4]; };
         struct __attribute__((packed, aligned(2))) Loose { u32x4 v; };
@@ -262,25 +266,26 @@ fp8_block_product(Fp8Args a)
 #pragma unroll
         for (int g = 0; g < FP; ++g)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < QG; ++j) {
                 Four o;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o.e[e] = from_f32<O>(acc[g][j][e]);
                 *reinterpret_cast<Four*>(lds + (row0 - i0 + g * 16) * PITCH + (col0 - j0 + j * 16) * 2) = o;
             }
         __syncthreads();
-        const int r = 2 * wave + (lane >> 5), c = lane & 31;
+        constexpr int LR = COLS / 8, RW = 64 / LR;        // lanes a row, rows a wave
+        const int r = RW * wave + lane / LR, c = lane % LR;
         O* o = static_cast<O*>(a.y) + (int64_t)(i0 + r) * a.ldy + j0 + c * 8;
 #pragma unroll
-        for (int h = 0; h < ROWS / 16; ++h) {
-            reinterpret_cast<Loose*>(o)->v = *reinterpret_cast<const u32x4*>(lds + (r + h * 16) * PITCH + c * 16);
-            o += 16 * a.ldy;
+        for (int h = 0; h < ROWS / (8 * RW); ++h) {
+            reinterpret_cast<Loose*>(o)->v = *reinterpret_cast<const u32x4*>(lds + (r + h * 8 * RW) * PITCH + c * 16);
+            o += 8 * RW * a.ldy;
         }
     } else {
 #pragma unroll
         for (int g = 0; g < FP; ++g)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < QG; ++j)
                 if (row0 + g * 16 < a.m && col0 + j * 16 < a.n) {
                     const float v[4] = {acc[g][j][0], acc[g][j][1], acc[g][j][2], acc[g][j][3]};
                     store4(static_cast<O*>(a.y) + (int64_t)(row0 + g * 16) * a.ldy + col0 + j * 16, v, a.n - (col0 + j * 16));

@@ -40,6 +40,7 @@ __device__ __forceinline__ f16x8 e4m3_to_f16(uint32_t lo, uint32_t hi)
 template <bool FAST> struct BlockOperand;
 template <> struct BlockOperand<true> {
     i32x8 v;
+    __device__ __forceinline__ BlockOperand() {}
     __device__ __forceinline__ BlockOperand(u32x4 a, u32x4 b)
         : v(__builtin_bit_cast(i32x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7))) {}
     __device__ __forceinline__ static f32x4 mul(const BlockOperand& a, const BlockOperand& b)
@@ -50,6 +51,7 @@ template <> struct BlockOperand<true> {
 };
 template <> struct BlockOperand<false> {
     f16x8 v[4];
+    __device__ __forceinline__ BlockOperand() {}
     __device__ __forceinline__ BlockOperand(u32x4 a, u32x4 b)
         : v{e4m3_to_f16(a.x, a.y), e4m3_to_f16(a.z, a.w), e4m3_to_f16(b.x, b.y), e4m3_to_f16(b.z, b.w)} {}
     __device__ __forceinline__ static f32x4 mul(const BlockOperand& a, const BlockOperand& b)

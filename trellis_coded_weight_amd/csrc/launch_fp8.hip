@@ -20,11 +20,11 @@ void skinny_shape(const Fp8Args& a, bool whole, hipStream_t st)
         hipLaunchKernelGGL((fp8_skinny_product<O, MI, 1, DEPTH, false>), grid, block, 0, st, a);
 }
 
-template <typename O, int FP>
+template <typename O, int FP, int QG>
 void block_shape(const Fp8Args& a, hipStream_t st)
 {
-    const int64_t tiles = (int64_t)blocks_for(a.m, Fp8Shape::rows(FP)) * blocks_for(a.n, Fp8Shape::kCols);
-    hipLaunchKernelGGL((fp8_block_product<O, FP, sizeof(O) == 2>), dim3((unsigned)(tiles * a.shares)),
+    const int64_t tiles = (int64_t)blocks_for(a.m, Fp8Shape::rows(FP)) * blocks_for(a.n, Fp8Shape::cols(QG));
+    hipLaunchKernelGGL((fp8_block_product<O, FP, QG, sizeof(O) == 2>), dim3((unsigned)(tiles * a.shares)),
                        dim3(Fp8Shape::kThreads), 0, st, a);
 }
 
@@ -62,11 +62,11 @@ qtcq_status product(Fp8Args a, void* ws, size_t wsb, hipStream_t st)
     a.shares = plan.shares;
     a.share_steps = plan.share_steps;
     if (plan.fp == 2)
-        block_shape<O, 2>(a, st);
+        plan.qg == 2 ? block_shape<O, 2, 2>(a, st) : block_shape<O, 2, 4>(a, st);
     else if (PRECISE || plan.fp == 4)
-        block_shape<O, 4>(a, st);
+        plan.qg == 2 ? block_shape<O, 4, 2>(a, st) : block_shape<O, 4, 4>(a, st);
     else if constexpr (!PRECISE)
-        block_shape<O, 8>(a, st);
+        block_shape<O, 8, 4>(a, st);
     // the shares' sums as those of any product
     ProductArgs j = {};
     j.out[0] = a.y;

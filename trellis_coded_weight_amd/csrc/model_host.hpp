@@ -21,7 +21,7 @@ inline int scale_blocks(int n) { return n / 128 + (n % 128 != 0); }
 // Which kernel a product takes, and its scratch (launch_fp8.hip).
 struct Fp8Plan {
     bool skinny;             // the kernel for few rows, which takes no scratch
-    int fp;                  // block kernel: 32 fp rows a tile
+    int fp, qg;              // block kernel: 32 fp rows by 64 qg columns a tile
     int shares, share_steps; // shares of k, and the blocks of each
     int part_pitch;          // row pitch of the shares' sums
     size_t part_bytes;       // the shares' sums
@@ -40,8 +40,9 @@ inline Fp8Plan plan_fp8(int m, int n, int k, bool whole, bool precise)
     p.part_pitch = (n + 3) / 4 * 4;
     const int steps = scale_blocks(k);
     double best = 0;
-    for (int fp = 2; fp <= (precise ? 4 : 8); fp *= 2) {
-        const int64_t tiles = ((int64_t)m + 32 * fp - 1) / (32 * fp) * (((int64_t)n + 255) / 256);
+    for (int c = 0; c < (precise ? 4 : 5); ++c) {
+        const int fp = c < 2 ? 2 : (c < 4 ? 4 : 8), qg = c < 4 && c % 2 == 0 ? 2 : 4;
+        const int64_t tiles = ((int64_t)m + 32 * fp - 1) / (32 * fp) * (((int64_t)n + 64 * qg - 1) / (64 * qg));
         const double step = precise ? (fp == 2 ? 1.1 : 1.8) : (fp == 2 ? 0.7 : (fp == 4 ? 1.0 : 1.7));
         int64_t most = kComputeUnits / tiles;
         if (most > steps / 4) most = steps / 4;
@@ -49,7 +50,7 @@ inline Fp8Plan plan_fp8(int m, int n, int k, bool whole, bool precise)
             const int share = steps > 0 ? (steps + s - 1) / s : 1, shares = steps > 0 ? (steps + share - 1) / share : 1;
             double t = (double)((tiles * shares + kComputeUnits - 1) / kComputeUnits) * (share + 2) * step;
             if (shares > 1) t += 6.0 + 8.0 * shares * m * p.part_pitch / 4e6;
-            if (p.fp == 0 || t < best) best = t, p.fp = fp, p.shares = shares, p.share_steps = share;
+            if (p.fp == 0 || t < best) best = t, p.fp = fp, p.qg = qg, p.shares = shares, p.share_steps = share;
         }
     }
     if (p.shares > 1) p.part_bytes = round256((size_t)p.shares * m * p.part_pitch * 4);
