@@ -28,29 +28,54 @@ struct Fp8Plan {
     size_t a_bytes, w_bytes; // padded copies of the operands
 };
 
+// Whether the kernel for few rows takes a product.  It reads w once at the memory's rate and a
+// once for every 16 columns, in a wave's registers, so its time grows with the groups of 16
+// rows and their length; the tiles pay for shares of k and a second launch (us, few rows
+// against tiles: 28672x8192 at m = 1 44.9 / 49, m = 8 (2^30.8) 55.0 / 49; 8192x8192 at m = 8
+// (2^29) 17.7 / 18.5, 16 (2^30) 20.4 / 18.5, 24 26.6 / 19; 4096x4096 at m = 64 (2^30) 12.3 / 14.4;
+// 1024x8192 at m = 16 10.9 / 13.7, 64 (m k = 2^19) 20.8 / 14.7).  Rows that are not whole chunks
+// cost the tiles a copy and this kernel slower loads: 8192x8193 at m = 4 (2^28) 44.9 / 46.3, 8
+// 50.1 / 46.6; 4096x4097 at m = 16 (2^28) 19.0 / 23.1, 24 (2^28.6) 23.9 / 23.2.
+inline bool fp8_few_rows(int m, int n, int k, bool whole)
+{
+    const double work = (double)m * n * k;
+    if (!whole) return m <= 2 || (m <= 64 && work <= 0x1.4p28);
+    return m <= 2 || (m <= 16 && work <= 0x1.8p29) || (m <= 64 && work <= 0x1p30 && (double)m * k <= 0x1p18);
+}
+
 // `whole`: the operands are whole 16-byte chunks as they are; `precise`: the result is binary32
 inline Fp8Plan plan_fp8(int m, int n, int k, bool whole, bool precise)
 {
     Fp8Plan p = {};
-    const double work = (double)m * n * k;
-    if (whole ? m <= 4 || (m <= 64 && work <= 0x1p31) : m <= 2 || (m <= 64 && work <= 0x1.1p30)) {
+    if (fp8_few_rows(m, n, k, whole)) {
         p.skinny = true;
         return p;
     }
     p.part_pitch = (n + 3) / 4 * 4;
     const int steps = scale_blocks(k);
+    // The tile and the shares of k by the shortest estimate, in us: rounds of workgroups (one a
+    // compute unit) times a share's steps, each as long as on large products, but no less than
+    // the operands take from memory (w somewhat longer for each further row of tiles that reads
+    // it, all of it with fewer workgroups than compute units); shares cost a second launch, and their sums' way out and back.  (28672x8192, 64x128 / 64x256 / 128x128 / 128x256 / 256x256: 64 rows 49 / 57 / 51 / 58
+    // / 67 us, 128 72 / 64 / 58 / 65 / 73, 256 125 / 103 / 90 / 75 / 88, 1024 412 / 330 / 299 / 252
+    // / 219; 93x14336x4096 19 / 28 / 22 / 24 / 27.)
+    struct Shape { int fp, qg; double step, precise; };
+    constexpr Shape shapes[] = {{2, 2, 0.46, 0.78}, {2, 4, 0.70, 1.20}, {4, 2, 0.64, 1.15}, {4, 4, 0.95, 1.75}, {8, 4, 1.65, 0}};
     double best = 0;
-    for (int c = 0; c < (precise ? 4 : 5); ++c) {
-        const int fp = c < 2 ? 2 : (c < 4 ? 4 : 8), qg = c < 4 && c % 2 == 0 ? 2 : 4;
-        const int64_t tiles = ((int64_t)m + 32 * fp - 1) / (32 * fp) * (((int64_t)n + 64 * qg - 1) / (64 * qg));
-        const double step = precise ? (fp == 2 ? 1.1 : 1.8) : (fp == 2 ? 0.7 : (fp == 4 ? 1.0 : 1.7));
+    for (const Shape& c : shapes) {
+        if (precise && c.precise == 0) continue;
+        const int64_t down = ((int64_t)m + 32 * c.fp - 1) / (32 * c.fp), tiles = down * (((int64_t)n + 64 * c.qg - 1) / (64 * c.qg));
+        const double memory = (m + n * (0.85 + 0.15 * down)) * k / 5e6;
         int64_t most = kComputeUnits / tiles;
         if (most > steps / 4) most = steps / 4;
         for (int s = 1; s == 1 || s <= most; ++s) {
             const int share = steps > 0 ? (steps + s - 1) / s : 1, shares = steps > 0 ? (steps + share - 1) / share : 1;
-            double t = (double)((tiles * shares + kComputeUnits - 1) / kComputeUnits) * (share + 2) * step;
-            if (shares > 1) t += 6.0 + 8.0 * shares * m * p.part_pitch / 4e6;
-            if (p.fp == 0 || t < best) best = t, p.fp = fp, p.qg = qg, p.shares = shares, p.share_steps = share;
+            const int64_t groups = tiles * shares;
+            double t = (double)((groups + kComputeUnits - 1) / kComputeUnits) * (share + 2) * (precise ? c.precise : c.step);
+            const double least = groups < kComputeUnits ? memory * kComputeUnits / groups : memory;
+            if (t < least) t = least + 0.1 * t;
+            if (shares > 1) t += 3.0 + 8.0 * shares * m * p.part_pitch / 8e6;
+            if (p.fp == 0 || t < best) best = t, p.fp = c.fp, p.qg = c.qg, p.shares = shares, p.share_steps = share;
         }
     }
     if (p.shares > 1) p.part_bytes = round256((size_t)p.shares * m * p.part_pitch * 4);
