@@ -10,15 +10,21 @@ namespace {
 void cut_row(DistillArgs& a)
 {
     const int64_t want = a.rows > 0 ? (2 * kComputeUnits + a.rows - 1) / a.rows : 1;
-    const int64_t most = (a.vocab + 8191) / 8192;
+    const int64_t most = ((int64_t)a.vocab + 8191) / 8192;
     const int64_t n = want < most ? want : most;
-    if (n < 2) {
-        a.segments = 1;
-        a.segment = a.vocab;
-        return;
-    }
-    a.segment = (int)((a.vocab + n - 1) / n + 7) / 8 * 8;
-    a.segments = (a.vocab + a.segment - 1) / a.segment;
+    a.segment = a.vocab;
+    if (n >= 2) a.segment = (int)((a.vocab + n - 1) / n + 7) / 8 * 8;
+    a.segments = n < 2 ? 1 : (a.vocab + a.segment - 1) / a.segment;
+}
+
+// The same for the loss, which pays a launch more for them: rows of up to 65536 elements, and
+// 128 or more rows, stay whole (us with the gradient, whole rows against segments: 300x32000
+// 18.6 / 22, 64x50000 16.4 / 20, 256x128000 33 / 46, 64x128000 26.8 / 20.1, 16x128000 24.9 / 18.3,
+// 1x131072 24.3 / 18.2).
+void cut_row_for_loss(DistillArgs& a)
+{
+    cut_row(a);
+    if (a.vocab <= 65536 || a.rows >= 128) a.segments = 1, a.segment = a.vocab;
 }
 
 unsigned capped(int64_t n) { return (unsigned)(n < (1 << 20) ? n : 1 << 20); }
@@ -71,7 +77,10 @@ qtcq_status distill_impl(const DistillArgs& a, hipStream_t st)
         hipLaunchKernelGGL((distill_partial<T, NT>), dim3((unsigned)(a.rows * a.segments)), dim3(NT), 0, st, a);
     });
     hipLaunchKernelGGL((distill_join<T, 256>), dim3((unsigned)a.rows), dim3(256), entries, st, a);
-    return a.grad ? grad_impl<T>(a, st) : launch_status();
+    if (!a.grad) return launch_status();
+    DistillArgs g = a;
+    cut_row(g);
+    return grad_impl<T>(g, st);
 }
 
 }  // namespace
@@ -81,13 +90,13 @@ size_t distill_workspace_bytes(int64_t rows, int vocab)
     DistillArgs a = {};
     a.rows = rows;
     a.vocab = vocab;
-    cut_row(a);
+    cut_row_for_loss(a);
     return a.segments == 1 ? 0 : round256((size_t)rows * a.segments * 8) + round256((size_t)rows * kDistillStats * 4);
 }
 
 qtcq_status launch_distill(DistillArgs a, int dtype, void* ws, hipStream_t st)
 {
-    cut_row(a);
+    cut_row_for_loss(a);
     a.part = static_cast<float*>(ws);
     // the gradient's launch reads the statistics
     if (a.segments > 1 && !a.stats)
