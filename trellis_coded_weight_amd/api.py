@@ -629,8 +629,8 @@ def _vector(x, name: str, dtypes, n: int, device: int):
     """An optional contiguous device vector of n values: its pointer, or None."""
     if x is None:
         return None
-    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dim() == 1 and x.dtype in dtypes
-            and x.shape[0] == n and x.is_contiguous()):
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype in dtypes
+            and x.shape == (n,) and x.is_contiguous()):
         raise ValueError("%s must be a contiguous device tensor of %d values in %s"
                          % (name, n, " or ".join(str(d) for d in dtypes)))
     if x.get_device() != device:
@@ -661,10 +661,10 @@ def quantize_blocks(x: torch.Tensor, block_rows: int = 1):
     R, C = x.shape
     q = x.new_empty((R, C), dtype=torch.float8_e4m3fn)
     down = R if block_rows == 1 else (R + 127) // 128
-    scale = x.new_empty(((C + 127) // 128, down), dtype=torch.float32)
+    scale = x.new_empty_strided((down, (C + 127) // 128), (1, down), dtype=torch.float32)
     nat.qtcq_quantize_blocks(x.data_ptr(), DTYPES[x.dtype], R, C, ldx, block_rows, q.data_ptr(), C,
                              scale.data_ptr(), 1, down, _stream(dev))
-    return q, scale.t()
+    return q, scale
 
 
 def matmul_fp8_workspace(M: int, N: int, K: int, whole_rows: bool = False) -> torch.Tensor:
