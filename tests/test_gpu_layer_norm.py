@@ -11,7 +11,7 @@ TYPES = ["float32", "bfloat16", "float16"]
 EPS = 1e-5
 SIZES = [(1, 1), (3, 2), (1, 8), (5, 63), (4, 64), (7, 65), (2, 511), (9, 513), (33, 1000), (6, 1024), (3, 2049),
          (5, 2731), (2, 4099), (3, 8192), (4, 8200), (2, 16384), (2, 16400), (1, 40001), (2, 70000), (1031, 40), (2500, 300),
-         (700, 2048), (600, 5000)]
+         (700, 2048), (600, 5000), (768, 2730), (769, 1000), (800, 2048), (801, 4100), (770, 8192)]
 
 
 @pytest.fixture(scope="module")

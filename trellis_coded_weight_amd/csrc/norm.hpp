@@ -146,17 +146,23 @@ layer_norm_rows(NormArgs a)
 
 constexpr int kNormGradThreads = 1024;
 
+// LDS of the gradient: of the sums over a row, and of those over row groups or rows
+template <int R>
+struct NormGradShared {
+    float red[2][2 * R][kNormGradThreads / 64];
+    float sums[16 * kNormGradThreads];
+};
+
 // grad_x, and the sums of dw and db where a.part is there (then every chunk of a row is held:
 // nch <= NCH RT): R rows a row group at a time, the next ones on their way.  LONG: chunks
 // beyond NCH RT are read anew by each pass.
-//   grid.x: any number of workgroups; each writes its part, of zeros where it had no row
+//   workgroup `block` of `blocks`, of 1024 threads; each writes its part, of zeros where it had
+//   no row
 template <typename T, typename W, int RT, int NCH, int R, bool LONG>
-__global__ void __launch_bounds__(kNormGradThreads)
-layer_norm_grad(NormGradArgs a)
+__device__ __forceinline__ void norm_grad_rows(const NormGradArgs& a, unsigned block, unsigned blocks, NormGradShared<R>& sh)
 {
     constexpr int E = 16 / (int)sizeof(T), NT = kNormGradThreads, PER = NT / RT;
     static_assert(PER == 1 || NCH == 1, "row groups are joined with one chunk a thread");
-    __shared__ float red[2][2 * R][NT / 64];
     const int t = threadIdx.x % RT, group = threadIdx.x / RT, n = a.cols, nch = (n + E - 1) / E;
     const T* x = static_cast<const T*>(a.x);
     const T* gy = static_cast<const T*>(a.grad_y);
@@ -195,12 +201,12 @@ layer_norm_grad(NormGradArgs a)
             }
         }
     };
-    const int64_t step = (int64_t)gridDim.x * PER * R;
-    int64_t row = ((int64_t)blockIdx.x * PER + group) * R;
+    const int64_t step = (int64_t)blocks * PER * R;
+    int64_t row = ((int64_t)block * PER + group) * R;
     Rows cur, next;
     fetch(row, next);
     int turn = 0;
-    for (int64_t first = (int64_t)blockIdx.x * PER * R; first < a.rows; first += step, row += step) {
+    for (int64_t first = (int64_t)block * PER * R; first < a.rows; first += step, row += step) {
         cur = next;
         if (first + step < a.rows) fetch(row + step, next);
         // into place, and rows past the last to zeros
@@ -252,7 +258,7 @@ layer_norm_grad(NormGradArgs a)
         for (int r = 0; r < R; ++r)
             if (LONG && row + r < a.rows)
                 for (int c = t + NCH * RT; c < nch; c += RT) add(r, load_x(row + r, c), load_g(row + r, c), weights(c));
-        row_sums<NT, RT>(s, red, turn);
+        row_sums<NT, RT>(s, sh.red, turn);
         // (the elements are taken from their chunks again: kept in binary32 over the sums, they
         // would not fit the registers)
 #pragma unroll
@@ -279,7 +285,7 @@ layer_norm_grad(NormGradArgs a)
         }
     }
     if (!want_w) return;
-    float* p = a.part + (int64_t)blockIdx.x * 2 * a.part_pitch;
+    float* p = a.part + (int64_t)block * 2 * a.part_pitch;
     if constexpr (PER == 1) {
 #pragma unroll
         for (int i = 0; i < NCH; ++i)
@@ -294,20 +300,85 @@ layer_norm_grad(NormGradArgs a)
             }
     } else {
         // the row groups' sums in order: group g adds up sums g, g + PER, ... of its chunk
-        __shared__ float sums[2 * E][NT];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            sums[e][threadIdx.x] = dw[0][e];
-            sums[E + e][threadIdx.x] = db[0][e];
+            sh.sums[e * NT + threadIdx.x] = dw[0][e];
+            sh.sums[(E + e) * NT + threadIdx.x] = db[0][e];
         }
         __syncthreads();
         for (int e = group; e < 2 * E; e += PER) {
             float v = 0.0f;
 #pragma unroll
-            for (int k = 0; k < PER; ++k) v += sums[e][k * RT + t];
+            for (int k = 0; k < PER; ++k) v += sh.sums[e * NT + k * RT + t];
             if (t < nch) p[(e < E ? 0 : a.part_pitch) + t * E + e % E] = v;
         }
     }
+}
+
+// grid.x: any number of workgroups
+template <typename T, typename W, int RT, int NCH, int R, bool LONG>
+__global__ void __launch_bounds__(kNormGradThreads)
+layer_norm_grad(NormGradArgs a)
+{
+    __shared__ NormGradShared<R> sh;
+    norm_grad_rows<T, W, RT, NCH, R, LONG>(a, blockIdx.x, gridDim.x, sh);
+}
+
+// Few rows, in one launch: workgroups 0 .. nx - 1 write grad_x, and each of the others takes 16
+// chunks of columns over all rows, which it reads again, 64 rows at a time, and writes their
+// weights' gradients.
+//   grid.x = nx + ceil(chunks / 16) (nx alone where no weight's gradient is wanted)
+template <typename T, typename W, int RT, int NCH, int R>
+__global__ void __launch_bounds__(kNormGradThreads)
+layer_norm_grad_few(NormGradArgs a, W* __restrict__ dw, W* __restrict__ db, int nx)
+{
+    __shared__ NormGradShared<R> sh;
+    if ((int)blockIdx.x < nx) {
+        norm_grad_rows<T, W, RT, NCH, R, false>(a, blockIdx.x, nx, sh);
+        return;
+    }
+    constexpr int E = 16 / (int)sizeof(T), U = 4;
+    const int r = threadIdx.x >> 4, t = threadIdx.x & 15, n = a.cols;
+    const int c = ((int)blockIdx.x - nx) * 16 + t;
+    const T* x = static_cast<const T*>(a.x);
+    const T* gy = static_cast<const T*>(a.grad_y);
+    float s[2 * E] = {};
+    if (c * E < n)
+        for (int64_t row = r; row < a.rows; row += U * 64) {
+            u32x4 xv[U], gv[U];
+            float mean[U], rstd[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                // (rows past the last are read as it, and left out below)
+                const int64_t at = row + u * 64 < a.rows ? row + u * 64 : a.rows - 1;
+                xv[u] = load_zero<T>(x + at * a.ldx, c, n);
+                gv[u] = load_zero<T>(gy + at * a.ldgy, c, n);
+                mean[u] = a.mean[at];
+                rstd[u] = a.rstd[at];
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (row + u * 64 >= a.rows) continue;
+                float xf[E], gf[E];
+                unpack<T>(xv[u], xf);
+                unpack<T>(gv[u], gf);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    s[e] = __builtin_fmaf(gf[e], (xf[e] - mean[u]) * rstd[u], s[e]);
+                    s[E + e] += gf[e];
+                }
+            }
+        }
+#pragma unroll
+    for (int e = 0; e < 2 * E; ++e) sh.sums[e * kNormGradThreads + threadIdx.x] = s[e];
+    __syncthreads();
+    // sum e of chunk t, over the 64 rows' threads in order
+    const int e = r;
+    if (e >= 2 * E || c * E + e % E >= n) return;
+    float v = 0.0f;
+    for (int k = 0; k < 64; ++k) v += sh.sums[e * kNormGradThreads + k * 16 + t];
+    W* out = e < E ? dw : db;
+    if (out) out[c * E + e % E] = from_f32<W>(v);
 }
 
 // Sums of dw and db over the rows of one share, for rows too long to be held: a workgroup
