@@ -520,8 +520,8 @@ qtcq_status qtcq_gated_vjp(const void* x, int64_t ldx, const void* w_gate, const
  * projections with its gradients, and the loss that trains the weights against the original
  * model, given by its top logits.
  *
- * The rules of the dense operators hold here too (strides, empty sizes, workspaces,
- * non-finite inputs, determinism, capture).  8-bit floating point is e4m3: a sign, 4 bits of
+ * The rules of the dense operators hold here too (strides, empty sizes, outputs apart from
+ * inputs, workspaces, non-finite inputs, determinism, capture).  8-bit floating point is e4m3: a sign, 4 bits of
  * exponent with bias 7, 3 of mantissa, largest value 448, 0x7F and 0xFF NaN.
  * A scale matrix has a stride for its rows and one for its columns, in elements.
  */
@@ -538,14 +538,17 @@ qtcq_status qtcq_gated_vjp(const void* x, int64_t ldx, const void* w_gate, const
  *          with scale_row = 1 the scales of adjacent rows lie together, as the product
  *          reads them fastest
  * Errors: QTCQ_ERR_INVALID_ARG (negative sizes, strides, NULL or misaligned buffers),
- * QTCQ_ERR_UNSUPPORTED (dtype, block_rows, sizes), QTCQ_ERR_DEVICE. */
+ * QTCQ_ERR_UNSUPPORTED (dtype, block_rows, sizes, more than 2^40 elements), QTCQ_ERR_DEVICE. */
 qtcq_status qtcq_quantize_blocks(const void* x, int dtype, int64_t rows, int cols, int64_t ldx,
                                  int block_rows, uint8_t* q, int64_t ldq, float* scale,
                                  int64_t scale_row, int64_t scale_col, void* stream);
 
 /* Product of two e4m3 matrices with such scales, activations a by weights w:
  *   y[m][n] = sum_b fl32(a_scale[m][b] w_scale[n / 128][b]) sum_{k in block b} a[m][k] w[n][k]
- * over the blocks b of 128 of k, sums in binary32, rounded once to dtype.
+ * over the blocks b of 128 of k, sums in binary32, rounded once to dtype.  A 16-bit result may
+ * come from the 8-bit matrix instruction, which sums 8 neighbours of k at a time, each product
+ * cut off at 2^-13 of the group's largest, and keeps 12 bits of their sum (1.4e-5 of the
+ * results' norm on random values, below their rounding).  Binary32 results have exact products.
  *   a  [M][K] e4m3, row stride lda; a_scale [M][ceil(K / 128)], strides as_row and as_col
  *   w  [N][K] e4m3, row stride ldw; w_scale [ceil(N / 128)][ceil(K / 128)], strides ws_row
  *      and ws_col; as_row and ws_row at most 2^20

@@ -261,7 +261,7 @@ def test_matmul_fp8_non_finite_scales(api, M, N, K):
 def test_matmul_fp8_empty(api):
     import torch
     f8 = torch.float8_e4m3fn
-    for M, N, K in ((0, 5, 128), (5, 0, 128), (4, 300, 0), (0, 0, 0)):
+    for M, N, K in ((0, 5, 128), (5, 0, 128), (500, 0, 300), (4, 300, 0), (300, 300, 0), (0, 0, 0)):
         y = api.matmul_fp8(torch.empty(M, K, device="cuda").to(f8), torch.empty(M, -(-K // 128), device="cuda"),
                            torch.empty(N, K, device="cuda").to(f8), torch.empty(-(-N // 128), -(-K // 128), device="cuda"))
         torch.cuda.synchronize()

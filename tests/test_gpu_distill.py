@@ -92,7 +92,7 @@ def test_distill_strided(api, dtype, wide, R):
     check(api, z, big[:, 7:27], tb[:, 4:24], gl, 1.0)
 
 
-@pytest.mark.parametrize("V", [3000, 40000])
+@pytest.mark.parametrize("V", [3000, 40000, 70000])
 def test_distill_given_sum(api, V):
     """The teacher's probabilities over its whole vocabulary: their sum here is below 1."""
     import torch
@@ -104,7 +104,7 @@ def test_distill_given_sum(api, V):
     assert float(grad.double().sum(1).abs().max()) < 1e-5
 
 
-@pytest.mark.parametrize("V", [500, 30000])
+@pytest.mark.parametrize("V", [500, 30000, 70000])
 def test_distill_repeated_indices(api, V):
     import torch
     z, index, t, gl = inputs(5, V, 40, "float32")
@@ -115,7 +115,7 @@ def test_distill_repeated_indices(api, V):
     check(api, z, index, t, gl, 1.0)
 
 
-@pytest.mark.parametrize("V", [700, 30000])
+@pytest.mark.parametrize("V", [700, 30000, 70000])
 def test_distill_indices_out_of_range(api, V):
     """Any index outside the vocabulary is padding, whatever its teacher's value."""
     import torch
@@ -132,7 +132,7 @@ def test_distill_indices_out_of_range(api, V):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("V", [600, 40000])
+@pytest.mark.parametrize("V", [600, 40000, 70000])
 def test_distill_masked_vocabulary(api, V, dtype):
     """Logits of -infinity or of the type's lowest value at most of the vocabulary; rows of
     them alone; teachers of -infinity."""
@@ -166,7 +166,7 @@ def test_distill_masked_vocabulary(api, V, dtype):
     assert float(loss2[6]) == float("inf") and bool(torch.isfinite(loss2[7]))
 
 
-@pytest.mark.parametrize("V", [600, 40000])
+@pytest.mark.parametrize("V", [600, 40000, 70000])
 def test_distill_non_finite_rows(api, V):
     """NaN or +infinity in a row's logits or teacher's values reach that token alone, and a
     token without entries is 0 even then."""

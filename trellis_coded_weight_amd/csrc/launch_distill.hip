@@ -29,19 +29,27 @@ void cut_row_for_loss(DistillArgs& a)
 
 unsigned capped(int64_t n) { return (unsigned)(n < (1 << 20) ? n : 1 << 20); }
 
-// f(threads a row, chunks a thread holds) for rows (or segments) of n elements
+// f(threads a row, chunks a thread holds) for rows or segments of n elements, long ones (as the
+// segments of a loss always are)
 template <typename T, typename F>
-void with_shape(int n, F&& f)
+void with_long_shape(int n, F&& f)
 {
     const int chunks = n / (16 / (int)sizeof(T));
-    if (chunks <= 256)
-        f(int_c<64>{}, int_c<4>{});
-    else if (chunks <= 2048)
+    if (chunks <= 2048)
         f(int_c<256>{}, int_c<8>{});
     else if (chunks <= 8192)
         f(int_c<512>{}, int_c<16>{});
     else
         f(int_c<1024>{}, int_c<16>{});
+}
+
+template <typename T, typename F>
+void with_shape(int n, F&& f)
+{
+    if (n / (16 / (int)sizeof(T)) <= 256)
+        f(int_c<64>{}, int_c<4>{});
+    else
+        with_long_shape<T>(n, f);
 }
 
 template <typename T>
@@ -72,7 +80,7 @@ qtcq_status distill_impl(const DistillArgs& a, hipStream_t st)
         });
         return launch_status();
     }
-    with_shape<T>(a.segment, [&](auto nt, auto) {
+    with_long_shape<T>(a.segment, [&](auto nt, auto) {
         constexpr int NT = decltype(nt)::value;
         hipLaunchKernelGGL((distill_partial<T, NT>), dim3((unsigned)(a.rows * a.segments)), dim3(NT), 0, st, a);
     });

@@ -16,6 +16,9 @@ constexpr int64_t kScaleMaxStride = (int64_t)1 << 20;
 // K of the e4m3 product: rows of 4 MB, so that a tile's offsets stay below 2^31
 constexpr int kFp8MaxK = 1 << 22;
 
+// elements of a matrix to be quantized: its pieces are counted in 32 bits
+constexpr int64_t kBlocksMaxElements = (int64_t)1 << 40;
+
 inline int scale_blocks(int n) { return n / 128 + (n % 128 != 0); }
 
 // Which kernel a product takes, and its scratch (launch_fp8.hip).
@@ -31,23 +34,23 @@ struct Fp8Plan {
 // Whether the kernel for few rows takes a product.  It reads w once at the memory's rate and a
 // once for every 16 columns, in a wave's registers, so its time grows with the groups of 16
 // rows and their length; the tiles pay for shares of k and a second launch (us, few rows
-// against tiles: 28672x8192 at m = 1 44.9 / 49, m = 8 (2^30.8) 55.0 / 49; 8192x8192 at m = 8
-// (2^29) 17.7 / 18.5, 16 (2^30) 20.4 / 18.5, 24 26.6 / 19; 4096x4096 at m = 64 (2^30) 12.3 / 14.4;
-// 1024x8192 at m = 16 10.9 / 13.7, 64 (m k = 2^19) 20.8 / 14.7).  Rows that are not whole chunks
+// against tiles: 28672x8192 at m = 1 44.9 / 49, m = 8 55.0 / 49; 8192x8192 at m = 8 (2^29) 16.5 /
+// 16.7, 12 17.7 / 16.7; 8192x4096 at m = 16 (2^29) 11.1 / 13.7, 20 14.9 / 13.6; 4096x4096 at m = 32
+// 10.9 / 13.6, 64 12.3 / 14.2; 2048x8192 at m = 32 15.1 / 14.0).  Rows that are not whole chunks
 // cost the tiles a copy and this kernel slower loads: 8192x8193 at m = 4 (2^28) 44.9 / 46.3, 8
 // 50.1 / 46.6; 4096x4097 at m = 16 (2^28) 19.0 / 23.1, 24 (2^28.6) 23.9 / 23.2.
 inline bool fp8_few_rows(int m, int n, int k, bool whole)
 {
     const double work = (double)m * n * k;
     if (!whole) return m <= 2 || (m <= 64 && work <= 0x1.4p28);
-    return m <= 2 || (m <= 16 && work <= 0x1.8p29) || (m <= 64 && work <= 0x1p30 && (double)m * k <= 0x1p18);
+    return m <= 2 || (m <= 16 && work <= 0x1p29) || (m <= 64 && k <= 4096 && (double)n * k <= 0x1p24);
 }
 
 // `whole`: the operands are whole 16-byte chunks as they are; `precise`: the result is binary32
 inline Fp8Plan plan_fp8(int m, int n, int k, bool whole, bool precise)
 {
     Fp8Plan p = {};
-    if (fp8_few_rows(m, n, k, whole)) {
+    if (m == 0 || n == 0 || fp8_few_rows(m, n, k, whole)) {
         p.skinny = true;
         return p;
     }
@@ -56,9 +59,10 @@ inline Fp8Plan plan_fp8(int m, int n, int k, bool whole, bool precise)
     // The tile and the shares of k by the shortest estimate, in us: rounds of workgroups (one a
     // compute unit) times a share's steps, each as long as on large products, but no less than
     // the operands take from memory (w somewhat longer for each further row of tiles that reads
-    // it, all of it with fewer workgroups than compute units); shares cost a second launch, and their sums' way out and back.  (28672x8192, 64x128 / 64x256 / 128x128 / 128x256 / 256x256: 64 rows 49 / 57 / 51 / 58
-    // / 67 us, 128 72 / 64 / 58 / 65 / 73, 256 125 / 103 / 90 / 75 / 88, 1024 412 / 330 / 299 / 252
-    // / 219; 93x14336x4096 19 / 28 / 22 / 24 / 27.)
+    // it, all of it with fewer workgroups than compute units); shares cost a second launch, and
+    // their sums' way out and back.  (us of 64x128 / 64x256 / 128x128 / 128x256 / 256x256, n x k =
+    // 28672x8192: 64 rows 49 / 57 / 51 / 58 / 67, 128 72 / 64 / 58 / 65 / 73, 256 125 / 103 / 90 /
+    // 75 / 88, 1024 412 / 330 / 299 / 252 / 219; 93 rows of 14336x4096 19 / 28 / 22 / 24 / 27.)
     struct Shape { int fp, qg; double step, precise; };
     constexpr Shape shapes[] = {{2, 2, 0.46, 0.78}, {2, 4, 0.70, 1.20}, {4, 2, 0.64, 1.15}, {4, 4, 0.95, 1.75}, {8, 4, 1.65, 0}};
     double best = 0;

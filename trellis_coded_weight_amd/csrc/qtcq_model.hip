@@ -67,7 +67,8 @@ qtcq_status qtcq_quantize_blocks(const void* x, int dtype, int64_t rows, int col
                                  int64_t ldq, float* scale, int64_t scale_row, int64_t scale_col, void* stream)
 {
     if (rows < 0 || cols < 0 || ldx < cols || ldq < cols) return QTCQ_ERR_INVALID_ARG;
-    if (!float_type(dtype) || (block_rows != 1 && block_rows != 128) || rows > kDenseMaxDim || cols > kDenseMaxDim)
+    if (!float_type(dtype) || (block_rows != 1 && block_rows != 128) || rows > kDenseMaxDim || cols > kDenseMaxDim ||
+        rows * cols > kBlocksMaxElements)
         return QTCQ_ERR_UNSUPPORTED;
     const int64_t r = block_rows == 1 ? rows : scale_blocks((int)rows), c = scale_blocks(cols);
     if (!distinct(r, c, scale_row, scale_col)) return QTCQ_ERR_INVALID_ARG;
