@@ -116,6 +116,26 @@ def test_quantize_halves_and_small_values(api, block_rows):
             check(api, wide[r:r + 3], 128)
 
 
+def test_quantize_every_pair_of_short_numbers(api):
+    """Each 8-bit number by each as its block's largest, over 20 powers of two: many quotients
+    by 448ths of them lie half way."""
+    import torch
+    m = torch.arange(128, 256, device="cuda", dtype=torch.float32)
+    blocks = []
+    for e in range(20):
+        v = m.expand(128, 128) * 2.0 ** -e
+        v = torch.where(v <= m[:, None], v, v / 2)
+        for half in (v[:, :64], v[:, 64:]):
+            blocks.append(torch.cat([half, -half[:, 1:], m[:, None]], 1))
+    x = torch.cat(blocks, 1)
+    say("quantize_blocks every pair of short numbers")
+    for scale in (1.0, 2.0 ** -80, 2.0 ** 100):
+        check(api, (x * scale).bfloat16(), 1)
+        check(api, x * scale, 1)
+    for r in range(0, 128, 9):
+        check(api, (x[r] * 2.0 ** -20).bfloat16().view(40, 128).repeat(4, 1)[:128], 128)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("block_rows", [1, 128])
 def test_quantize_zero_and_non_finite_blocks(api, block_rows, dtype):

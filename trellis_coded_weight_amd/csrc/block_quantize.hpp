@@ -6,12 +6,15 @@
 // alone.  A block of zeros (or one so small that its scale underflows to 0) has s = 0 and
 // q = 0; a block that holds an infinity or NaN has s = NaN and q = 0.
 //
-// t = fl(x fl(1 / s)) is within 3 units in its last place of x / s, so rounding t is right
-// unless x / s lies that close to a point half way between two e4m3 values.  Those points
-// have bits 0x80000 below the three kept ones, in t itself or, under 2^-6 where e4m3 is evenly
-// spaced by 2^-9, in t + 2^-6.  A value found within 8 units of one is rounded in binary64
-// (x / s differs from such a point by 2^-29 relative at least or not at all, so the quotient
-// in binary64 decides as the exact one).  About 1 value in 60,000 of random ones is.
+// t = fl(x r), r the hardware's reciprocal of s (one unit off), is within 3 units in its last place
+// of x / s, so rounding t is right unless x / s lies that close to a point half way between two
+// e4m3 values.  Those points have bits 0x80000 below the three kept ones, in t itself or, under
+// 2^-6 where e4m3 is evenly spaced by 2^-9, in t + 2^-6.  A value found within 8 units of such a
+// point h is put on it or beside it by the sign of x - h s, which one fused step has exactly (h
+// has 5 digits, s 24, and s >= 2^-100 keeps the difference from underflowing).  About 1 value in
+// 60,000 of random binary32 ones is, but in bf16 6 in 100 where the block's largest is 7 times a
+// short number.  Where s is smaller, the quotient is taken in binary64 (it differs from h by
+// 2^-29 relative at least or not at all, so that decides as the exact one).
 //
 // The pass is bound by memory: x read once, held in registers between the largest magnitude
 // and the rounding.
@@ -33,10 +36,17 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax)
 {
     BlockScale o;
     const bool finite = amax < 0x7F800000u;
-    o.s = finite ? __builtin_bit_cast(float, amax) / 448.0f : __builtin_nanf("");
+    const float m = __builtin_bit_cast(float, amax);
+    // m / 448 rounded right: with y the constant's rounded reciprocal and q = fl(m y), q + y (m - 448 q)
+    // in two fused steps, as long as nothing underflows
+    constexpr float y = 1.0f / 448.0f;
+    const float q = m * y;
+    o.s = __builtin_fmaf(__builtin_fmaf(-448.0f, q, m), y, q);
+    if (__builtin_expect(m < 0x1p-90f, 0)) o.s = m / 448.0f;
+    o.s = finite ? o.s : __builtin_nanf("");
     o.zero = !finite || o.s == 0.0f;
     o.tiny = !o.zero && o.s < 0x1p-100f;
-    o.r = 1.0f / o.s;
+    o.r = __builtin_amdgcn_rcpf(o.s);
     return o;
 }
 
@@ -52,24 +62,44 @@ __device__ __forceinline__ float e4m3_of_quotient(float x, float s)
     return __builtin_copysignf((float)(rint(v * inv) * step), x);
 }
 
+// |t|, moved to where points half way between e4m3 values have the bits 0x80000 below the kept ones
+__device__ __forceinline__ uint32_t placed(float t)
+{
+    const float a = __builtin_fabsf(t);
+    return __builtin_bit_cast(uint32_t, a < 0x1p-6f ? a + 0x1p-6f : a);
+}
+
+// t, or if it is within 8 units of such a point h: h or a neighbour on the side of x / s, by the
+// sign of x - h s
+__device__ __forceinline__ float off_half_way(float t, float x, float s)
+{
+    const uint32_t b = placed(t), d = (b + 0x80008u) & 0xFFFFFu;
+    const float w = __builtin_bit_cast(float, b + 8u - d);
+    const float h = __builtin_fabsf(t) < 0x1p-6f ? w - 0x1p-6f : w;
+    const float over = __builtin_fmaf(-h, s, __builtin_fabsf(x));
+    const uint32_t side = __builtin_bit_cast(uint32_t, h) + (over > 0.0f ? 1u : 0u) - (over < 0.0f ? 1u : 0u);
+    return d <= 16u ? __builtin_copysignf(__builtin_bit_cast(float, side), x) : t;
+}
+
 // N values (a multiple of 4) to e4m3, four to a word.
 template <int N>
 __device__ __forceinline__ void to_e4m3(const float (&x)[N], const BlockScale& o, uint32_t (&w)[N / 4])
 {
     float t[N];
-    uint32_t near = 0xFFFFFu;
+    uint32_t near = ~0u;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
         t[e] = x[e] * o.r;
-        const float a = __builtin_fabsf(t[e]);
-        const uint32_t b = __builtin_bit_cast(uint32_t, a < 0x1p-6f ? a + 0x1p-6f : a);
-        // how far past 8 units below the half way point
-        const uint32_t d = (b + 0x80008u) & 0xFFFFFu;
+        // how far past 8 units below the half way point, times 2^12
+        const uint32_t d = (placed(t[e]) << 12) + 0x80008000u;
         near = d < near ? d : near;
     }
-    if (__builtin_expect(near <= 16u || o.tiny || o.zero, 0)) {
+    if (__builtin_expect(o.tiny || o.zero, 0)) {
 #pragma unroll
         for (int e = 0; e < N; ++e) t[e] = o.zero ? 0.0f : e4m3_of_quotient(x[e], o.s);
+    } else if (near <= 16u << 12) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) t[e] = off_half_way(t[e], x[e], o.s);
     }
 #pragma unroll
     for (int g = 0; g < N / 4; ++g) {
