@@ -453,7 +453,8 @@ def _workspace(workspace, nbytes: int, like: torch.Tensor):
     if workspace is None:
         if nbytes == 0:
             return None, None, 0
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        workspace = like.new_empty(nbytes, dtype=torch.uint8)
+        return workspace, workspace.data_ptr(), nbytes
     return workspace, workspace.data_ptr(), _dev_workspace(workspace)
 
 
@@ -620,9 +621,11 @@ FLOATS = (torch.float32, torch.bfloat16, torch.float16)
 def _not_recorded(name: str, *tensors) -> None:
     """Autograd does not see the calls, so inputs that require gradients are refused while it
     records."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        raise ValueError("%s does not record gradients: call it under torch.no_grad() or with "
-                         "detached inputs, and its vjp for the gradients" % name)
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError("%s does not record gradients: call it under torch.no_grad() or "
+                                 "with detached inputs, and its vjp for the gradients" % name)
 
 
 def _vector(x, name: str, dtypes, n: int, device: int):
