@@ -4,15 +4,17 @@
 // A workgroup of 8 waves takes all rows of a, MI groups of 16, and NJ groups of 16 rows of w; its waves share
 // k: wave v takes the blocks v, v + 8, ... of 128 bytes of every row.  Operands go from memory
 // to registers in the matrix instruction's layout with no LDS and no barrier on the way, DEPTH
-// blocks in flight a wave, a block's scales with it.  The waves' sums are added in wave order
+// blocks in flight a wave, a block's scales with it; blocks past the last are neither loaded nor
+// multiplied (1x26392x1024 10 us, 16 with zeros in their place).  The waves' sums are added in wave order
 // through LDS.
 //
 // ALIGNED: rows start on 16 bytes and are whole chunks; buffer loads whose range check returns
 // zeros past the matrices.  Otherwise rows past the last are read as the last one (their
-// results are not stored), and the last block of k is loaded with its end guarded.
+// results are not stored), and what is behind the last whole block of k is loaded apart.
 #pragma once
 
 #include "fp8_product.hpp"
+#include "rows.hpp"
 
 namespace qtcq {
 
@@ -33,7 +35,8 @@ fp8_skinny_product(Fp8Args a)
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int j0 = blockIdx.x * 16 * NJ;
     const int r = lane & 15, c = lane >> 4;
-    const int nblk = (a.k + 127) / 128;
+    // whole blocks, and where rows need not be whole chunks, what is left behind them
+    const int nblk = ALIGNED ? (a.k + 127) / 128 : a.k / 128, left = ALIGNED ? 0 : a.k % 128;
 
     __amdgpu_buffer_rsrc_t ra, rw;
     if constexpr (ALIGNED) {
@@ -47,7 +50,18 @@ fp8_skinny_product(Fp8Args a)
         rw = rsrc(a.w, a.ldw, j0, a.n, 16 * NJ);
     }
     struct Set { u32x4 p[2][MI], q[2][NJ]; float s[MI]; float t; };
+    auto a_row = [&](int i) { return a.a + (int64_t)(16 * i + r < a.m ? 16 * i + r : a.m - 1) * a.lda; };
+    auto w_row = [&](int j) { return a.w + (int64_t)(j0 + 16 * j + r < a.n ? j0 + 16 * j + r : a.n - 1) * a.ldw; };
+    auto load_scales = [&](int blk, Set& o) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const int row = 16 * i + r < a.m ? 16 * i + r : a.m - 1;
+            o.s[i] = a.a_scale[row * a.as_row + blk * a.as_col];
+        }
+        o.t = a.w_scale[(j0 >> 7) * a.ws_row + blk * a.ws_col];
+    };
     auto load = [&](int blk, Set& o) {
+        if (blk >= nblk) return;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int at = blk * 128 + 64 * h + 16 * c;
@@ -61,28 +75,13 @@ fp8_skinny_product(Fp8Args a)
                     o.p[h][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
                         ra, at < a.k ? (r + 16 * i) * (int)a.lda + at : 0x7FFFFFFF, 0, 0));
             } else {
-                auto chunk = [&](const uint8_t* base, int64_t ld, int row, int nrows) {
-                    const uint8_t* p = base + (int64_t)(row < nrows ? row : nrows - 1) * ld;
-                    return (blk + 1) * 128 <= a.k ? load_loose(p + at) : at < a.k ? load_chunk<uint8_t>(p, at, a.k)
-                                                                                  : u32x4{0u, 0u, 0u, 0u};
-                };
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) o.q[h][j] = chunk(a.w, a.ldw, j0 + 16 * j + r, a.n);
+                for (int j = 0; j < NJ; ++j) o.q[h][j] = load_loose(w_row(j) + at);
 #pragma unroll
-                for (int i = 0; i < MI; ++i) o.p[h][i] = chunk(a.a, a.lda, 16 * i + r, a.m);
+                for (int i = 0; i < MI; ++i) o.p[h][i] = load_loose(a_row(i) + at);
             }
         }
-        // a block past the last: scales of 0, so that nothing is added
-        const bool there = blk < nblk;
-        const int b = there ? blk : 0;
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            const int row = 16 * i + r < a.m ? 16 * i + r : a.m - 1;
-            const float s = a.a_scale[row * a.as_row + b * a.as_col];
-            o.s[i] = there ? s : 0.0f;
-        }
-        const float t = a.w_scale[(j0 >> 7) * a.ws_row + b * a.ws_col];
-        o.t = there ? t : 0.0f;
+        load_scales(blk, o);
     };
     f32x4 acc[MI][NJ] = {};
     auto multiply = [&](const Set& o) {
@@ -99,6 +98,25 @@ fp8_skinny_product(Fp8Args a)
             }
         }
     };
+    // What is left: chunks past a row's last byte are read as its last 16 bytes and moved into
+    // place when they are multiplied, by the wave whose turn it is.
+    Set rest;
+    const bool mine = left > 0 && wave == nblk % NW;
+    if (mine) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int n = nblk * 8 + 4 * h + c;
+            auto chunk = [&](const uint8_t* p) {
+                if (a.k < 16) return n == 0 ? load_chunk<uint8_t>(p, 0, a.k) : u32x4{0u, 0u, 0u, 0u};
+                return load_loose(p + place_of<uint8_t>(n, a.k).at);
+            };
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) rest.q[h][j] = chunk(w_row(j));
+#pragma unroll
+            for (int i = 0; i < MI; ++i) rest.p[h][i] = chunk(a_row(i));
+        }
+        load_scales(nblk, rest);
+    }
     if (wave < nblk) {
         Set set[DEPTH];
 #pragma unroll
@@ -107,9 +125,20 @@ fp8_skinny_product(Fp8Args a)
 #pragma unroll
             for (int d = 0; d < DEPTH; ++d) {
                 load(b + (d + DEPTH - 1) * NW, set[(d + DEPTH - 1) % DEPTH]);
-                multiply(set[d]);
+                if (b + d * NW < nblk) multiply(set[d]);
             }
         }
+    }
+    if (mine) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int bits = a.k < 16 ? 0 : place_of<uint8_t>(nblk * 8 + 4 * h + c, a.k).bits;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) rest.q[h][j] = behind(rest.q[h][j], bits);
+#pragma unroll
+            for (int i = 0; i < MI; ++i) rest.p[h][i] = behind(rest.p[h][i], bits);
+        }
+        multiply(rest);
     }
 #pragma unroll
     for (int f = 0; f < F; ++f) red[wave][f][lane] = acc[f / NJ][f % NJ];
