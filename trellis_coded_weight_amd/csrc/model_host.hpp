@@ -33,17 +33,18 @@ struct Fp8Plan {
 
 // Whether the kernel for few rows takes a product.  It reads w once at the memory's rate and a
 // once for every 16 columns, in a wave's registers, so its time grows with the groups of 16
-// rows and their length; the tiles pay for shares of k and a second launch (us, few rows
-// against tiles: 28672x8192 at m = 1 44.9 / 49, m = 8 55.0 / 49; 8192x8192 at m = 8 (2^29) 16.5 /
-// 16.7, 12 17.7 / 16.7; 8192x4096 at m = 16 (2^29) 11.1 / 13.7, 20 14.9 / 13.6; 4096x4096 at m = 32
-// 10.9 / 13.6, 64 12.3 / 14.2; 2048x8192 at m = 32 15.1 / 14.0).  Rows that are not whole chunks
-// cost the tiles a copy and this kernel slower loads: 8192x8193 at m = 4 (2^28) 44.9 / 46.3, 8
-// 50.1 / 46.6; 4096x4097 at m = 16 (2^28) 19.0 / 23.1, 24 (2^28.6) 23.9 / 23.2.
+// rows and their length; the tiles pay for shares of k and a second launch, which many columns
+// need not (us, few rows against tiles: 28672x8192 at m = 8 48.5 / 50.8, 16 59.8 / 49.7; 8192x8192
+// at m = 12 (1.5 2^29) 16.4 / 16.9, 16 17.6 / 16.9; 4096x8192 at m = 24 (1.5 2^29) 12.3 / 13.8;
+// 8192x4096 at m = 32 (2^30) 14.5 / 13.7; 4096x4096 at m = 64 12.8 / 14.3; 1024x8192 at m = 64
+// 21.3 / 13.9; 14336x1024 at m = 48 14.3 / 10.9).  Rows that are not whole chunks cost the tiles
+// a copy and this kernel slower loads: 8192x8193 at m = 4 43.4 / 43.5, 8 48.7 / 43.7; 4096x4097 at
+// m = 24 (1.5 2^28) 21.4 / 22.3; 4096x2047 at m = 40 16.7 / 19.2; 2000x2047 at m = 64 20.5 / 16.6.
 inline bool fp8_few_rows(int m, int n, int k, bool whole)
 {
     const double work = (double)m * n * k;
-    if (!whole) return m <= 2 || (m <= 64 && work <= 0x1.4p28);
-    return m <= 2 || (m <= 16 && work <= 0x1p29) || (m <= 64 && k <= 4096 && (double)n * k <= 0x1p24);
+    if (!whole) return m <= 4 || (m <= 48 && work <= 0x1.9p28);
+    return m <= 8 || (m <= 32 && work <= 0x1.8p29) || (m <= 64 && n <= 8192 && k <= 4096 && (double)n * k <= 0x1p24);
 }
 
 // `whole`: the operands are whole 16-byte chunks as they are; `precise`: the result is binary32
