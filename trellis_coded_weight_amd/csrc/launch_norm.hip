@@ -34,9 +34,9 @@ int part_pitch(int cols) { return (cols + 7) / 8 * 8; }
 
 // Whether the gradients take one launch that reads the rows a second time for the weights', by
 // the sizes alone: few rows, whose second reading comes from the caches (us, one launch against
-// two: 333x2731 float32 12.4 / 17.2, 512x4096 bf16 12.4 / 17.0, 768x4096 15.8 / 18.6, 512x8192
-// 15.8 / 20.5; 1024x2048 18.8 / 17.2, 1024x4096 23.6 / 20.4).
-bool norm_few_rows(int64_t rows, int cols) { return rows <= 768 && cols <= 8192; }
+// two: 333x2731 float32 12.4 / 17.2, 512x7168 18.1 / 18.6, 768x8192 26.8 / 22.0; 512x4096 bf16 12.4 /
+// 17.0, 768x4096 15.8 / 18.6, 512x8192 15.8 / 20.5, 1024x2048 18.8 / 17.2, 1024x4096 23.6 / 20.4).
+bool norm_few_rows(int64_t rows, int cols) { return rows <= 768 && cols <= 8192 && rows * cols <= 1 << 22; }
 
 template <typename T, typename W>
 qtcq_status grad_impl(NormGradArgs a, W* grad_weight, W* grad_bias, float* part, hipStream_t st)
