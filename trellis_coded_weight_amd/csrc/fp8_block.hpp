@@ -256,12 +256,12 @@ fp8_block_product(Fp8Args a)
                     *reinterpret_cast<f32x4*>(a.part + ((int64_t)share * a.m + row) * a.part_pitch + col) = acc[g][j];
             }
         }
-    } else if (sizeof(O) == 2 && i0 + ROWS <= a.m && j0 + COLS <= a.n) {
-        // a whole tile of 16-bit results goes out through LDS, in whole rows of the tile
-        constexpr int PITCH = COLS * 2 + 16;
+    } else if (i0 + ROWS <= a.m && j0 + COLS <= a.n) {
+        // a whole tile of results goes out through LDS, in whole rows of the tile
+        constexpr int E = 16 / (int)sizeof(O), PITCH = COLS * (int)sizeof(O) + 16;
         static_assert(ROWS * PITCH <= R * STEP, "the tile fits LDS");
-        struct __attribute__((aligned(8))) Four { O e[4]; };
-        struct __attribute__((packed, aligned(2))) Loose { u32x4 v; };
+        struct __attribute__((aligned(4 * sizeof(O)))) Four { O e[4]; };
+        struct __attribute__((packed, aligned(sizeof(O)))) Loose { u32x4 v; };
         landed(std::integral_constant<int, 0>{});         // LDS is no longer read or loaded
 #pragma unroll
         for (int g = 0; g < FP; ++g)
@@ -270,12 +270,12 @@ fp8_block_product(Fp8Args a)
                 Four o;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o.e[e] = from_f32<O>(acc[g][j][e]);
-                *reinterpret_cast<Four*>(lds + (row0 - i0 + g * 16) * PITCH + (col0 - j0 + j * 16) * 2) = o;
+                *reinterpret_cast<Four*>(lds + (row0 - i0 + g * 16) * PITCH + (col0 - j0 + j * 16) * (int)sizeof(O)) = o;
             }
         __syncthreads();
-        constexpr int LR = COLS / 8, RW = 64 / LR;        // lanes a row, rows a wave
+        constexpr int LR = COLS / E, RW = 64 / LR;        // lanes a row, rows a wave
         const int r = RW * wave + lane / LR, c = lane % LR;
-        O* o = static_cast<O*>(a.y) + (int64_t)(i0 + r) * a.ldy + j0 + c * 8;
+        O* o = static_cast<O*>(a.y) + (int64_t)(i0 + r) * a.ldy + j0 + c * E;
 #pragma unroll
         for (int h = 0; h < ROWS / (8 * RW); ++h) {
             reinterpret_cast<Loose*>(o)->v = *reinterpret_cast<const u32x4*>(lds + (r + h * 8 * RW) * PITCH + c * 16);
