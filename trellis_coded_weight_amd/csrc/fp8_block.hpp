@@ -256,8 +256,8 @@ fp8_block_product(Fp8Args a)
                     *reinterpret_cast<f32x4*>(a.part + ((int64_t)share * a.m + row) * a.part_pitch + col) = acc[g][j];
             }
         }
-    } else if (i0 + ROWS <= a.m && j0 + COLS <= a.n) {
-        // a whole tile of results goes out through LDS, in whole rows of the tile
+    } else if (j0 + COLS <= a.n) {
+        // results of all the tile's columns go out through LDS, in whole rows of the tile
         constexpr int E = 16 / (int)sizeof(O), PITCH = COLS * (int)sizeof(O) + 16;
         static_assert(ROWS * PITCH <= R * STEP, "the tile fits LDS");
         struct __attribute__((aligned(4 * sizeof(O)))) Four { O e[4]; };
@@ -278,7 +278,8 @@ fp8_block_product(Fp8Args a)
         O* o = static_cast<O*>(a.y) + (int64_t)(i0 + r) * a.ldy + j0 + c * E;
 #pragma unroll
         for (int h = 0; h < ROWS / (8 * RW); ++h) {
-            reinterpret_cast<Loose*>(o)->v = *reinterpret_cast<const u32x4*>(lds + (r + h * 8 * RW) * PITCH + c * 16);
+            if (i0 + r + h * 8 * RW < a.m)
+                reinterpret_cast<Loose*>(o)->v = *reinterpret_cast<const u32x4*>(lds + (r + h * 8 * RW) * PITCH + c * 16);
             o += 8 * RW * a.ldy;
         }
     } else {
