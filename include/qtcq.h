@@ -521,8 +521,9 @@ qtcq_status qtcq_gated_vjp(const void* x, int64_t ldx, const void* w_gate, const
  * model, given by its top logits.
  *
  * The rules of the dense operators hold here too (strides, empty sizes, outputs apart from
- * inputs, workspaces, non-finite inputs, determinism, capture).  8-bit floating point is e4m3: a sign, 4 bits of
- * exponent with bias 7, 3 of mantissa, largest value 448, 0x7F and 0xFF NaN.
+ * inputs, workspaces, non-finite inputs, capture), and sums are added in an order that the
+ * sizes alone fix: the same bits on every run.  8-bit floating point is e4m3: a sign, 4 bits
+ * of exponent with bias 7, 3 of mantissa, largest value 448, 0x7F and 0xFF NaN.
  * A scale matrix has a stride for its rows and one for its columns, in elements.
  */
 

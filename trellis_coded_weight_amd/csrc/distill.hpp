@@ -14,9 +14,13 @@
 // thread keeps a running maximum m and the sum s of exp((z - m) / tau), and the row is read
 // once for the loss.  (z - m) is formed first: neither a row of very low values (a masked
 // vocabulary) nor a large maximum costs digits.  A workgroup takes a row, and with the
-// gradient wanted in the same call reads it again at once, while the caches still hold it;
-// with few rows several workgroups share one (distill_partial, distill_join, distill_grad).
-// The k entries' own sums are in binary64.
+// gradient wanted in the same call holds it in registers until the sum is known; with few rows
+// several workgroups share one (distill_partial, distill_join, distill_grad).  The k entries'
+// own sums are in binary64.
+//
+// Bound by memory: 4096x128000 bf16 486 us with the gradient (4.3 TB/s; 717 when the row was read
+// again), 181 for the loss alone (5.8 TB/s), 395 for the gradient alone; 1001x50021 fp16 58 us, in
+// two rows a workgroup, of which the first's loads and the last's stores overlap nothing.
 //
 // stats [rows][kDistillStats]: m, log2 s, the same two of the teacher, and sum p.
 #pragma once

@@ -1,10 +1,10 @@
 // fp8_block.hpp -- the product of e4m3 matrices with block scales for any number of rows, in
-// workgroup tiles of 32 FP x 64 QG (256 or 128 columns), for operands whose rows start on 16 bytes and
-// hold whole 16-byte chunks, gfx950.
+// workgroup tiles of 32 FP x 64 QG (256 or 128 columns), for operands whose rows start on 16
+// bytes and hold whole 16-byte chunks, gfx950.
 //
 // Eight waves, 2 x 4, each 16 FP rows of a by 16 QG rows of w.  A step is one block of 128 of
-// k.  Its tiles (a's 4 FP KB, w's 8 QG KB) and its scales go from memory straight to LDS, into a ring
-// of 2 to 4 places, so the next one to three steps are on their way during a step.
+// k.  Its tiles (a's 4 FP KB, w's 8 QG KB) and its scales go from memory straight to LDS, into a
+// ring of 2 to 4 places, so the next one to three steps are on their way during a step.
 // LDS rows are 128 bytes, their 16-byte chunk c at place c ^ ((row >> 1) & 7): the 16 lanes
 // that read one chunk of 16 rows at once touch 16 different places of the 256-byte bank row.
 //
@@ -20,6 +20,14 @@
 //
 // Where tiles are fewer than the compute units, k is cut into shares; each writes its sums in
 // 32 bits, and join_shares adds them in order.
+//
+// 4096x28672x8192 to bf16: 775 us, 2.48 PFLOP/s, the matrix cores 67% busy at 1.7 to 1.8 GHz (on
+// operands of zeros 615 us at 2.4 GHz): power bounds it.  A loop of the instruction with its four
+// scaled additions and nothing else reaches 3.75 PFLOP/s on random operands; in tiles of 32 x 32
+// 3.34.  93x8192x14336 to fp16: 24 us and 4.5 for the shares, w at 4.9 TB/s.  Smaller tiles are
+// bound by the loads to LDS: 128 x 128 tiles take 0.64 us a step, their loads alone 0.45 to 0.58
+// (13 to 14 TB/s over the chip), the rest alone 0.5; a second set of registers, read a step
+// ahead, did not shorten it.
 #pragma once
 
 #include <type_traits>

@@ -8,6 +8,10 @@
 // multiplied (1x26392x1024 10 us, 16 with zeros in their place).  The waves' sums are added in wave order
 // through LDS.
 //
+// Bound by memory with one row (28672x8192 41 us, 5.7 TB/s), by the groups of 16 rows and their
+// conversions to fp16 with more (8 rows 48.5 us); small ones by the launch (1x4096x4096 6.4 us
+// in the kernel).
+//
 // ALIGNED: rows start on 16 bytes and are whole chunks; buffer loads whose range check returns
 // zeros past the matrices.  Otherwise rows past the last are read as the last one (their
 // results are not stored), and what is behind the last whole block of k is loaded apart.

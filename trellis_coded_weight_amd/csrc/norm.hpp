@@ -14,6 +14,10 @@
 // rows share, in registers.  So do the sums of dw and db: each group of RT threads adds
 // its rows in order, a workgroup its groups, and join_norm_sums the workgroups.  No atomics:
 // the same bits on every run.
+//
+// 8192x8192 bf16: forward 51.5 us in the kernel (5.2 TB/s), gradients 78 (5.2 TB/s) and 7.5 for
+// the 256 workgroups' sums; 333x2731 float32 gradients in one launch 9.3.  Without the next
+// rows' loads ahead of the work the forward took 78, the gradients 128.
 #pragma once
 
 #include "model_args.hpp"
