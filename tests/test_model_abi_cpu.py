@@ -37,7 +37,8 @@ def test_quantize_blocks(nat):
              dict(x=FAKE + 1), dict(scale=FAKE + 2), dict(dtype=nat.QTCQ_F32, x=FAKE + 2), dict(srow=0), dict(scol=0),
              dict(scol=3), dict(srow=-1), dict(srow=2, scol=1), dict(srow=1, scol=1), dict(br=128, srow=1, scol=0)),
             (dict(dtype=nat.QTCQ_I8), dict(dtype=-1), dict(dtype=4), dict(br=0), dict(br=64), dict(br=-1),
-             dict(rows=(1 << 24) + 1), dict(cols=(1 << 24) + 1, ldx=BIG, ldq=BIG)))
+             dict(rows=(1 << 24) + 1), dict(cols=(1 << 24) + 1, ldx=BIG, ldq=BIG),
+             dict(rows=1 << 24, cols=1 << 17, ldx=BIG, ldq=BIG, scol=BIG)))
     assert call(rows=0, x=None, q=None, scale=None) == nat.QTCQ_OK
     assert call(cols=0, x=None, q=None, scale=None) == nat.QTCQ_OK
 
