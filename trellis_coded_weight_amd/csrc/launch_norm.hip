@@ -96,7 +96,7 @@ qtcq_status grad_impl(NormGradArgs a, W* grad_weight, W* grad_bias, float* part,
             if (groups > 0)
                 hipLaunchKernelGGL(norm_column_sums<T>, dim3((unsigned)(chunks + 31) / 32, groups), dim3(256), 0, st, a, share);
         }
-        hipLaunchKernelGGL(join_norm_sums<W>, dim3((unsigned)(a.cols + 63) / 64, 2), dim3(256), 0, st, part, groups,
+        hipLaunchKernelGGL(join_norm_sums<W>, dim3((unsigned)(a.cols + 31) / 32, 2), dim3(256), 0, st, part, groups,
                            a.part_pitch, a.cols, grad_weight, grad_bias);
     }
     return launch_status();
