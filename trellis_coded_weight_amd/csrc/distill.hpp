@@ -455,9 +455,11 @@ distill_join(DistillArgs a)
     const int64_t row = blockIdx.x;
     const float* p = a.part + row * a.segments * 2;
     const float k2 = kLog2e / a.tau;
-    float m = -__builtin_inff(), s = 0.0f;
+    // (a thread's first segment is read beside the entries)
+    const bool any = (int)threadIdx.x < a.segments;
+    float m = any ? p[2 * threadIdx.x] : -__builtin_inff(), s = any ? p[2 * threadIdx.x + 1] : 0.0f;
     load_entries<T, NT>(a, row);
-    for (int i = threadIdx.x; i < a.segments; i += NT) {
+    for (int i = threadIdx.x + NT; i < a.segments; i += NT) {
         const float top = __builtin_fmaxf(m, p[2 * i]), ref = finite_ref(top);
         s = s * __builtin_amdgcn_exp2f((m - ref) * k2) + p[2 * i + 1] * __builtin_amdgcn_exp2f((p[2 * i] - ref) * k2);
         m = top;
