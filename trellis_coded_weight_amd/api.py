@@ -641,6 +641,11 @@ def _vector(x, name: str, dtypes, n: int, device: int):
     return x.data_ptr()
 
 
+def _result_rows(x: torch.Tensor) -> torch.Tensor:
+    """Contiguous rows for a result of the shape and dtype of x."""
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
+
+
 def _block_scales(s: torch.Tensor, name: str, shape, device: int):
     """A matrix of block scales with any strides, broadcast ones too.  Returns both strides."""
     if not (isinstance(s, torch.Tensor) and s.is_cuda and s.dtype == torch.float32
@@ -727,7 +732,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
     wp, bp, wt = _norm_weights(x, weight, bias, dev)
     _not_recorded("layer_norm", x, weight, bias)
     R, C = x.shape
-    y = x.new_empty((R, C))
+    y = _result_rows(x)
     mean, rstd = (x.new_empty(R, dtype=torch.float32), x.new_empty(R, dtype=torch.float32)) if save else (None, None)
     nat.qtcq_layer_norm(x.data_ptr(), DTYPES[x.dtype], R, C, ldx, wp, bp, DTYPES[wt], eps,
                         y.data_ptr(), C, mean.data_ptr() if save else None,
@@ -759,7 +764,7 @@ def layer_norm_vjp(x: torch.Tensor, weight: torch.Tensor | None, mean: torch.Ten
         raise ValueError("mean and rstd are those that layer_norm saved")
     need = nat.qtcq_layer_norm_vjp_workspace_bytes(R, C) if want_w else 0
     _keep, ws, ws_bytes = _workspace(workspace, need, x)
-    grad_x = x.new_empty((R, C)) if want_x else None
+    grad_x = _result_rows(x) if want_x else None
     grad_w, grad_b = (x.new_empty(C, dtype=wt), x.new_empty(C, dtype=wt)) if want_w else (None, None)
     nat.qtcq_layer_norm_vjp(x.data_ptr(), DTYPES[x.dtype], R, C, ldx, wp, DTYPES[wt], mp, rp,
                             grad_y.data_ptr(), ldgy, grad_x.data_ptr() if want_x else None, C,
@@ -810,7 +815,7 @@ def distill_topk(logits: torch.Tensor, index: torch.Tensor, teacher: torch.Tenso
     _keep, ws, ws_bytes = _workspace(workspace, nat.qtcq_distill_topk_workspace_bytes(R, V), logits)
     loss = logits.new_empty(R, dtype=torch.float32)
     stats = logits.new_empty((R, 5), dtype=torch.float32) if save else None
-    grad = logits.new_empty((R, V)) if grad_loss is not None else None
+    grad = _result_rows(logits) if grad_loss is not None else None
     nat.qtcq_distill_topk(logits.data_ptr(), DTYPES[logits.dtype], R, V, ldl, index.data_ptr(),
                           index.element_size(), ldi, teacher.data_ptr(), DTYPES[teacher.dtype], ldt,
                           k, temperature, zp, loss.data_ptr(), stats.data_ptr() if save else None,
@@ -832,7 +837,7 @@ def distill_topk_vjp(logits: torch.Tensor, index: torch.Tensor, teacher: torch.T
     if gp is None or not (isinstance(stats, torch.Tensor) and stats.shape == (R, 5)):
         raise ValueError("stats are those that distill_topk saved, grad_loss a value a row")
     sp = _vector(stats.view(-1), "stats", (torch.float32,), R * 5, dev)
-    grad = logits.new_empty((R, V))
+    grad = _result_rows(logits)
     nat.qtcq_distill_topk_vjp(logits.data_ptr(), DTYPES[logits.dtype], R, V, ldl, index.data_ptr(),
                               index.element_size(), ldi, teacher.data_ptr(), DTYPES[teacher.dtype],
                               ldt, k, temperature, sp, gp, grad.data_ptr(), V, _stream(dev))
