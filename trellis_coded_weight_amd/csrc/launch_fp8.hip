@@ -15,9 +15,9 @@ void skinny_shape(const Fp8Args& a, bool whole, hipStream_t st)
     const dim3 grid(blocks_for(a.n, 16)), block(Fp8SkinnyShape::kThreads);
     constexpr int DEPTH = MI == 1 ? 4 : (MI == 2 ? 3 : 2);
     if (whole)
-        hipLaunchKernelGGL((fp8_skinny_product<O, MI, 1, DEPTH, true>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((fp8_skinny_product<O, MI, DEPTH, true>), grid, block, 0, st, a);
     else
-        hipLaunchKernelGGL((fp8_skinny_product<O, MI, 1, DEPTH, false>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((fp8_skinny_product<O, MI, DEPTH, false>), grid, block, 0, st, a);
 }
 
 template <typename O, int FP, int QG>
