@@ -649,11 +649,12 @@ def _result_rows(x: torch.Tensor) -> torch.Tensor:
 def _block_scales(s: torch.Tensor, name: str, shape, device: int):
     """A matrix of block scales with any strides, broadcast ones too.  Returns both strides."""
     if not (isinstance(s, torch.Tensor) and s.is_cuda and s.dtype == torch.float32
-            and tuple(s.shape) == shape):
+            and s.shape == shape):
         raise ValueError("%s must be a float32 device tensor of %s" % (name, list(shape)))
     if s.get_device() != device:
         _on_current_device(s, name)
-    return s.stride(0) if shape[0] > 1 else 0, s.stride(1) if shape[1] > 1 else 0
+    row, col = s.stride()
+    return row if shape[0] > 1 else 0, col if shape[1] > 1 else 0
 
 
 def quantize_blocks(x: torch.Tensor, block_rows: int = 1):
@@ -733,7 +734,8 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
     _not_recorded("layer_norm", x, weight, bias)
     R, C = x.shape
     y = _result_rows(x)
-    mean, rstd = (x.new_empty(R, dtype=torch.float32), x.new_empty(R, dtype=torch.float32)) if save else (None, None)
+    mean = x.new_empty(R, dtype=torch.float32) if save else None
+    rstd = torch.empty_like(mean) if save else None
     nat.qtcq_layer_norm(x.data_ptr(), DTYPES[x.dtype], R, C, ldx, wp, bp, DTYPES[wt], eps,
                         y.data_ptr(), C, mean.data_ptr() if save else None,
                         rstd.data_ptr() if save else None, _stream(dev))
@@ -765,7 +767,10 @@ def layer_norm_vjp(x: torch.Tensor, weight: torch.Tensor | None, mean: torch.Ten
     need = nat.qtcq_layer_norm_vjp_workspace_bytes(R, C) if want_w else 0
     _keep, ws, ws_bytes = _workspace(workspace, need, x)
     grad_x = _result_rows(x) if want_x else None
-    grad_w, grad_b = (x.new_empty(C, dtype=wt), x.new_empty(C, dtype=wt)) if want_w else (None, None)
+    grad_w = grad_b = None
+    if want_w:
+        grad_w = x.new_empty(C) if weight is None else torch.empty_like(weight)
+        grad_b = torch.empty_like(grad_w)
     nat.qtcq_layer_norm_vjp(x.data_ptr(), DTYPES[x.dtype], R, C, ldx, wp, DTYPES[wt], mp, rp,
                             grad_y.data_ptr(), ldgy, grad_x.data_ptr() if want_x else None, C,
                             grad_w.data_ptr() if want_w else None,
