@@ -48,7 +48,7 @@ qtcq_status grad_impl(NormGradArgs a, W* grad_weight, W* grad_bias, float* part,
             constexpr int RT = decltype(rt)::value, NCH = decltype(nch)::value, R = NCH == 1 ? 2 : 1;
             constexpr int PER = kNormGradThreads / RT * R;
             const int nx = a.grad_x ? (int)((a.rows + PER - 1) / PER) : 0;
-            const int ny = grad_weight || grad_bias ? (chunks + 15) / 16 : 0;
+            const int ny = grad_weight || grad_bias ? (chunks + kNormFewChunks - 1) / kNormFewChunks : 0;
             hipLaunchKernelGGL((layer_norm_grad_few<T, W, RT, NCH, R>), dim3(nx + ny), dim3(kNormGradThreads), 0, st, a, grad_weight,
                                grad_bias, nx);
             return launch_status();

@@ -16,7 +16,7 @@
 // the same bits on every run.
 //
 // 8192x8192 bf16: forward 51.5 us in the kernel (5.2 TB/s), gradients 78 (5.2 TB/s) and 4.9 for
-// the 256 workgroups' sums; 333x2731 float32 gradients in one launch 9.3.  Without the next
+// the 256 workgroups' sums; 333x2731 float32 gradients in one launch 7.6.  Without the next
 // rows' loads ahead of the work the forward took 78, the gradients 128.
 #pragma once
 
@@ -328,10 +328,11 @@ layer_norm_grad(NormGradArgs a)
     norm_grad_rows<T, W, RT, NCH, R, LONG>(a, blockIdx.x, gridDim.x, sh);
 }
 
-// Few rows, in one launch: workgroups 0 .. nx - 1 write grad_x, and each of the others takes 16
-// chunks of columns over all rows, which it reads again, 64 rows at a time, and writes their
+// Few rows, in one launch: workgroups 0 .. nx - 1 write grad_x, and each of the others takes 8
+// chunks of columns over all rows, which it reads again, 512 rows at a time, and writes their
 // weights' gradients.
-//   grid.x = nx + ceil(chunks / 16) (nx alone where no weight's gradient is wanted)
+//   grid.x = nx + ceil(chunks / 8) (nx alone where no weight's gradient is wanted)
+constexpr int kNormFewChunks = 8;
 template <typename T, typename W, int RT, int NCH, int R>
 __global__ void __launch_bounds__(kNormGradThreads)
 layer_norm_grad_few(NormGradArgs a, W* __restrict__ dw, W* __restrict__ db, int nx)
@@ -341,20 +342,20 @@ layer_norm_grad_few(NormGradArgs a, W* __restrict__ dw, W* __restrict__ db, int 
         norm_grad_rows<T, W, RT, NCH, R, false>(a, blockIdx.x, nx, sh);
         return;
     }
-    constexpr int E = 16 / (int)sizeof(T), U = 4;
-    const int r = threadIdx.x >> 4, t = threadIdx.x & 15, n = a.cols;
-    const int c = ((int)blockIdx.x - nx) * 16 + t;
+    constexpr int E = 16 / (int)sizeof(T), U = 4, CW = kNormFewChunks, ROWS = kNormGradThreads / CW;
+    const int r = threadIdx.x / CW, t = threadIdx.x % CW, n = a.cols;
+    const int c = ((int)blockIdx.x - nx) * CW + t;
     const T* x = static_cast<const T*>(a.x);
     const T* gy = static_cast<const T*>(a.grad_y);
     float s[2 * E] = {};
     if (c * E < n)
-        for (int64_t row = r; row < a.rows; row += U * 64) {
+        for (int64_t row = r; row < a.rows; row += U * ROWS) {
             u32x4 xv[U], gv[U];
             float mean[U], rstd[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 // (rows past the last are read as it, and left out below)
-                const int64_t at = row + u * 64 < a.rows ? row + u * 64 : a.rows - 1;
+                const int64_t at = row + u * ROWS < a.rows ? row + u * ROWS : a.rows - 1;
                 xv[u] = load_zero<T>(x + at * a.ldx, c, n);
                 gv[u] = load_zero<T>(gy + at * a.ldgy, c, n);
                 mean[u] = a.mean[at];
@@ -362,7 +363,7 @@ layer_norm_grad_few(NormGradArgs a, W* __restrict__ dw, W* __restrict__ db, int 
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (row + u * 64 >= a.rows) continue;
+                if (row + u * ROWS >= a.rows) continue;
                 float xf[E], gf[E];
                 unpack<T>(xv[u], xf);
                 unpack<T>(gv[u], gf);
@@ -376,13 +377,15 @@ layer_norm_grad_few(NormGradArgs a, W* __restrict__ dw, W* __restrict__ db, int 
 #pragma unroll
     for (int e = 0; e < 2 * E; ++e) sh.sums[e * kNormGradThreads + threadIdx.x] = s[e];
     __syncthreads();
-    // sum e of chunk t, over the 64 rows' threads in order
+    // sum e of chunk t, over the rows' threads, in four runs side by side
     const int e = r;
     if (e >= 2 * E || c * E + e % E >= n) return;
-    float v = 0.0f;
-    for (int k = 0; k < 64; ++k) v += sh.sums[e * kNormGradThreads + k * 16 + t];
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k = 0; k < ROWS; k += 4)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += sh.sums[e * kNormGradThreads + (k + i) * CW + t];
     W* out = e < E ? dw : db;
-    if (out) out[c * E + e % E] = from_f32<W>(v);
+    if (out) out[c * E + e % E] = from_f32<W>((v.x + v.y) + (v.z + v.w));
 }
 
 // Sums of dw and db over the rows of one share, for rows too long to be held: a workgroup
