@@ -10,7 +10,7 @@ FP8 = [(20, 40, 160), (70, 40, 160), (70, 40, 2064), (130, 16400, 160), (20, 820
        (20, 40, 41), (70, 40, 41), (70, 40, 4099), (130, 16400, 41), (20, 8200, 4099), (70, 16400, 41),
        (70, 4300, 4099), (70, 33000, 41), (70, 16400, 4099), (200, 33000, 41)]
 # rows, columns
-NORM = [(800, 4000), (1030, 1024), (769, 8192)]
+NORM = [(800, 4000), (1030, 1024), (769, 8192), (1537, 100), (1540, 520), (1600, 1000), (1536, 2040), (1600, 2000)]
 # rows, vocabulary, entries
 DISTILL = [(1, 65537, 64), (100, 70001, 9), (127, 131072, 5), (127, 200000, 3), (127, 400001, 33), (130, 70000, 64),
            (128, 65537, 2), (3, 524288, 64)]

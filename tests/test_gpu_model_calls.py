@@ -54,7 +54,7 @@ def test_refusals_blocks(api):
 
 def test_refusals_layer_norm(api):
     import torch
-    x, gy = normal(900, 64, dtype="float16"), normal(900, 64, seed=2, dtype="float16")
+    x, gy = normal(1700, 64, dtype="float16"), normal(1700, 64, seed=2, dtype="float16")
     w, b = normal(64, seed=3), normal(64, seed=4)
     y, mean, rstd = api.layer_norm(x, w, b, save=True)
     small = torch.empty(64, dtype=torch.uint8, device="cuda")
@@ -113,7 +113,7 @@ def every_call(api, seed=0, scale=1.0):
         o[1].mul_(scale)
         w = ws(nat.qtcq_matmul_fp8_workspace_bytes(M, N, K, K % 16 == 0))
         calls.append((lambda o=o, w=w: api.matmul_fp8(*o, dtype=torch.bfloat16, workspace=w), [o[1]]))
-    for R, C in ((9, 1000), (900, 1000), (5, 20000)):
+    for R, C in ((9, 1000), (1700, 1000), (5, 20000)):
         x, gy = normal(R, C, seed=seed + 2, scale=scale), normal(R, C, seed=seed + 3)
         w, b = normal(C, seed=4), normal(C, seed=5)
         g = ws(nat.qtcq_layer_norm_vjp_workspace_bytes(R, C))

@@ -76,13 +76,13 @@ def test_layer_norm(nat):
 
 def test_layer_norm_vjp(nat):
     size = nat.qtcq_layer_norm_vjp_workspace_bytes
-    ws = size(800, 64)
+    ws = size(2000, 64)
     assert ws >= 2 * 64 * 4 and size(1 << 20, 128) > ws and size(4, 64) == 0
     assert size(-1, 8) == 0 and size(8, -1) == 0 and size((1 << 24) + 1, 8) == 0
     call = caller(nat, "qtcq_layer_norm_vjp",
                   ["x", "dtype", "rows", "cols", "ldx", "w", "wdtype", "mean", "rstd", "gy", "ldgy", "gx", "ldgx", "gw",
                    "gb", "ws", "wsb", "stream"],
-                  [FAKE, nat.QTCQ_F16, 800, 64, 64, FAKE, nat.QTCQ_F16, FAKE, FAKE, FAKE, 64, FAKE, 64, FAKE, FAKE, FAKE, ws,
+                  [FAKE, nat.QTCQ_F16, 2000, 64, 64, FAKE, nat.QTCQ_F16, FAKE, FAKE, FAKE, 64, FAKE, 64, FAKE, FAKE, FAKE, ws,
                    None])
     refused(nat, call,
             (dict(rows=-1), dict(cols=-1), dict(ldx=63), dict(ldgy=63), dict(ldgx=63), dict(x=None), dict(mean=None),

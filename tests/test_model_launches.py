@@ -103,8 +103,9 @@ def test_measured_choices(recorder):
                                "fp8 1 4 8192 8193 0", "fp8 1 40 4096 2047 0"],
         "fp8_block_product": ["fp8 1 16 28672 8192 1", "fp8 1 16 8192 8192 1", "fp8 1 64 1024 8192 1", "fp8 1 48 14336 1024 1",
                               "fp8 1 8 8192 8193 0", "fp8 1 64 2000 2047 0"],
-        "layer_norm_grad_few": ["norm_vjp 0 0 333 2731 3", "norm_vjp 1 0 512 8192 3", "norm_vjp 1 0 768 4096 3"],
-        "join_norm_sums": ["norm_vjp 1 0 1024 2048 3", "norm_vjp 1 0 1024 4096 3", "norm_vjp 0 0 768 8192 3"],
+        "layer_norm_grad_few": ["norm_vjp 0 0 333 2731 3", "norm_vjp 1 0 512 8192 3", "norm_vjp 1 0 768 4096 3",
+                                "norm_vjp 1 0 1024 2048 3", "norm_vjp 1 0 1536 1000 3"],
+        "join_norm_sums": ["norm_vjp 1 0 2048 1000 3", "norm_vjp 0 0 1024 4096 3", "norm_vjp 0 0 768 8192 3"],
         "distill_train": ["distill 1 64 50000 64 1", "distill 1 256 128000 64 1"],
         "distill_partial": ["distill 1 16 128000 64 1", "distill 1 64 128000 64 1", "distill 1 1 131072 64 1"],
     }

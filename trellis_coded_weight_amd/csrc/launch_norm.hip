@@ -33,10 +33,14 @@ qtcq_status norm_impl(const NormArgs& a, hipStream_t st)
 int part_pitch(int cols) { return (cols + 7) / 8 * 8; }
 
 // Whether the gradients take one launch that reads the rows a second time for the weights', by
-// the sizes alone: few rows, whose second reading comes from the caches (us, one launch against
-// two: 333x2731 float32 12.4 / 17.2, 512x7168 18.1 / 18.6, 768x8192 26.8 / 22.0; 512x4096 bf16 12.4 /
-// 17.0, 768x4096 15.8 / 18.6, 512x8192 15.8 / 20.5, 1024x2048 18.8 / 17.2, 1024x4096 23.6 / 20.4).
-bool norm_few_rows(int64_t rows, int cols) { return rows <= 768 && cols <= 8192 && rows * cols <= 1 << 22; }
+// the sizes alone: few rows, whose second reading comes from the caches, in up to three
+// readings of 512 rows (us, one launch against two: 333x2731 float32 12.4 / 16.2, 512x7168 16.2 /
+// 16.4, 1024x4096 20.3 / 16.3; 512x8192 bf16 13.5 / 18.2, 768x4096 13.4 / 16.4, 1024x2048 13.4 /
+// 16.2, 1536x1000 15.4 / 16.2, 1536x256 13.5 / 16.3, 2048x1000 19.5 / 16.3, 1000x8192 22.5 / 20.3).
+bool norm_few_rows(int64_t rows, int cols)
+{
+    return rows <= 512 ? cols <= 8192 : rows <= 1536 && rows * cols <= 3 << 20;
+}
 
 template <typename T, typename W>
 qtcq_status grad_impl(NormGradArgs a, W* grad_weight, W* grad_bias, float* part, hipStream_t st)
