@@ -87,6 +87,7 @@ def test_refusals_distill(api):
              lambda: api.distill_topk(z, index, t.double()), lambda: api.distill_topk(z.cpu(), index, t),
              lambda: api.distill_topk(z, index.cpu(), t), lambda: api.distill_topk(z, index, t, grad_loss=gl[:3]),
              lambda: api.distill_topk(z, index, t, grad_loss=gl.half()), lambda: api.distill_topk(z, index, t, grad_loss=gl, save=True),
+             lambda: api.distill_topk(z, index, t, teacher_log_z=3.0), lambda: api.distill_topk(z, index, t, grad_loss=1.0),
              lambda: api.distill_topk(z, index, t, teacher_log_z=gl[:1]), lambda: api.distill_topk(z, index, t, workspace=small),
              lambda: api.distill_topk(z.float().requires_grad_(), index, t),
              lambda: api.distill_topk(z, many, many.float()),

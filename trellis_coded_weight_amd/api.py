@@ -813,10 +813,10 @@ def distill_topk(logits: torch.Tensor, index: torch.Tensor, teacher: torch.Tenso
         raise ValueError("save is for distill_topk_vjp: not with grad_loss")
     dev = torch.cuda.current_device()
     ldl, ldi, ldt = _distill_inputs(logits, index, teacher, temperature, dev)
-    _not_recorded("distill_topk", logits, teacher, teacher_log_z)
     (R, V), k = logits.shape, index.shape[1]
     zp = _vector(teacher_log_z, "teacher_log_z", (torch.float32,), R, dev)
     gp = _vector(grad_loss, "grad_loss", (torch.float32,), R, dev)
+    _not_recorded("distill_topk", logits, teacher, teacher_log_z)
     _keep, ws, ws_bytes = _workspace(workspace, nat.qtcq_distill_topk_workspace_bytes(R, V), logits)
     loss = logits.new_empty(R, dtype=torch.float32)
     stats = logits.new_empty((R, 5), dtype=torch.float32) if save else None
