@@ -90,12 +90,14 @@ inline Fp8Plan plan_fp8(int m, int n, int k, bool whole, bool precise)
     return p;
 }
 
-// for either kind of result
+// For either kind of result; without `whole`, for any operands: where the kernel for few rows takes
+// those that are not whole chunks, others may go to the tiles, with shares of k (40x512x8192).
 inline size_t fp8_workspace_bytes(int M, int N, int K, bool whole)
 {
     size_t most = 0;
     for (int precise = 0; precise < 2; ++precise) {
-        const Fp8Plan p = plan_fp8(M, N, K, whole, precise != 0);
+        Fp8Plan p = plan_fp8(M, N, K, whole, precise != 0);
+        if (!whole && p.skinny) p = plan_fp8(M, N, K, true, precise != 0), p.a_bytes = p.w_bytes = 0;
         const size_t need = p.part_bytes + (whole ? 0 : p.a_bytes + p.w_bytes);
         most = need > most ? need : most;
     }
