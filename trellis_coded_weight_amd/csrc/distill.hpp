@@ -232,16 +232,18 @@ __device__ __forceinline__ RowStats finish_row(const DistillArgs& a, int64_t row
     const double k2 = 1.4426950408889634 / (double)a.tau;
     const double ls = log2_of(s);
     const double ref = (double)finite_ref(m);
-    // the teacher's maximum and sum, or those that the given sum stands for
-    float tm = 0.0f;
-    double tls = 0.0;
+    // the teacher's maximum, and the sum about it or the one that the given sum stands for: both
+    // of p's parts stay small, so that the gradient's binary32 p is that of the loss
+    float tm = -__builtin_inff();
+    for (int j = threadIdx.x; j < a.k; j += NT)
+        if (en[j].index >= 0) tm = __builtin_fmaxf(tm, en[j].t);
+    tm = block_max<NT>(tm, sh.red[0]);
+    double tls;
     if (a.teacher_log_z) {
-        tls = (double)a.teacher_log_z[row] * 1.4426950408889634;
+        tm = __builtin_fabsf(tm) < __builtin_inff() ? tm : 0.0f;
+        tls = (double)a.teacher_log_z[row] * 1.4426950408889634 - (double)tm * k2;
     } else {
-        tm = -__builtin_inff();
-        for (int j = threadIdx.x; j < a.k; j += NT)
-            if (en[j].index >= 0) tm = __builtin_fmaxf(tm, en[j].t);
-        tm = finite_ref(block_max<NT>(tm, sh.red[0]));
+        tm = finite_ref(tm);
         double e = 0.0;
         for (int j = threadIdx.x; j < a.k; j += NT)
             if (en[j].index >= 0) e += (double)exp2_of(((double)en[j].t - (double)tm) * k2);
