@@ -341,11 +341,11 @@ __device__ __forceinline__ void list_entries(const DistillArgs& a, int lo, int h
                     alone = false;
                     first = first && (int)l - 1 > j;
                 }
-            float p = first ? en[j].p : 0.0f;
+            double p = first ? (double)en[j].p : 0.0;
             if (first && !alone)
                 for (int l = j + 1; l < a.k; ++l)
-                    if (en[l].index == i) p += en[l].p;
-            en[j].t = p;
+                    if (en[l].index == i) p += (double)en[l].p;
+            en[j].t = (float)p;
         }
     __syncthreads();
 }
