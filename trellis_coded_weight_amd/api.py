@@ -620,12 +620,13 @@ FLOATS = (torch.float32, torch.bfloat16, torch.float16)
 
 def _not_recorded(name: str, *tensors) -> None:
     """Autograd does not see the calls, so inputs that require gradients are refused while it
-    records."""
+    records (in a backward pass too, if that is to be differentiated again)."""
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
                 raise ValueError("%s does not record gradients: call it under torch.no_grad() or "
-                                 "with detached inputs, and its vjp for the gradients" % name)
+                                 "with detached inputs (gradients come from the calls that compute "
+                                 "them)" % name)
 
 
 def _vector(x, name: str, dtypes, n: int, device: int):
@@ -667,6 +668,7 @@ def quantize_blocks(x: torch.Tensor, block_rows: int = 1):
         raise ValueError("block_rows must be 1 or 128")
     dev = torch.cuda.current_device()
     ldx = _rows(x, "x", FLOATS, dev)
+    _not_recorded("quantize_blocks", x)
     R, C = x.shape
     q = x.new_empty((R, C), dtype=torch.float8_e4m3fn)
     down = R if block_rows == 1 else (R + 127) // 128
@@ -702,6 +704,7 @@ def matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale:
     kb = (K + 127) // 128
     as_row, as_col = _block_scales(a_scale, "a_scale", (M, kb), dev)
     ws_row, ws_col = _block_scales(w_scale, "w_scale", ((N + 127) // 128, kb), dev)
+    _not_recorded("matmul_fp8", a, a_scale, w, w_scale)
     ap, wp = a.data_ptr(), w.data_ptr()
     need = nat.qtcq_matmul_fp8_workspace_bytes(M, N, K, _whole_rows(ap | wp, K, 1, lda, ldw))
     _keep, ws, ws_bytes = _workspace(workspace, need, a)
@@ -764,6 +767,7 @@ def layer_norm_vjp(x: torch.Tensor, weight: torch.Tensor | None, mean: torch.Ten
     rp = _vector(rstd, "rstd", (torch.float32,), R, dev)
     if mp is None or rp is None:
         raise ValueError("mean and rstd are those that layer_norm saved")
+    _not_recorded("layer_norm_vjp", x, weight, mean, rstd, grad_y)
     need = nat.qtcq_layer_norm_vjp_workspace_bytes(R, C) if want_w else 0
     _keep, ws, ws_bytes = _workspace(workspace, need, x)
     grad_x = _result_rows(x) if want_x else None
@@ -816,7 +820,7 @@ def distill_topk(logits: torch.Tensor, index: torch.Tensor, teacher: torch.Tenso
     (R, V), k = logits.shape, index.shape[1]
     zp = _vector(teacher_log_z, "teacher_log_z", (torch.float32,), R, dev)
     gp = _vector(grad_loss, "grad_loss", (torch.float32,), R, dev)
-    _not_recorded("distill_topk", logits, teacher, teacher_log_z)
+    _not_recorded("distill_topk", logits, teacher, teacher_log_z, grad_loss)
     _keep, ws, ws_bytes = _workspace(workspace, nat.qtcq_distill_topk_workspace_bytes(R, V), logits)
     loss = logits.new_empty(R, dtype=torch.float32)
     stats = logits.new_empty((R, 5), dtype=torch.float32) if save else None
@@ -842,6 +846,7 @@ def distill_topk_vjp(logits: torch.Tensor, index: torch.Tensor, teacher: torch.T
     if gp is None or not (isinstance(stats, torch.Tensor) and stats.shape == (R, 5)):
         raise ValueError("stats are those that distill_topk saved, grad_loss a value a row")
     sp = _vector(stats.view(-1), "stats", (torch.float32,), R * 5, dev)
+    _not_recorded("distill_topk_vjp", logits, teacher, stats, grad_loss)
     grad = _result_rows(logits)
     nat.qtcq_distill_topk_vjp(logits.data_ptr(), DTYPES[logits.dtype], R, V, ldl, index.data_ptr(),
                               index.element_size(), ldi, teacher.data_ptr(), DTYPES[teacher.dtype],
