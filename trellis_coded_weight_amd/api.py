@@ -717,7 +717,8 @@ def matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale:
 
 def _norm_weights(x, weight, bias, dev):
     """(pointers of weight and bias, their dtype): float32 or the dtype of x, both the same."""
-    dtype = x.dtype if weight is None and bias is None else (bias if weight is None else weight).dtype
+    given = bias if weight is None else weight
+    dtype = given.dtype if isinstance(given, torch.Tensor) else x.dtype
     kinds = (dtype,) if dtype in (torch.float32, x.dtype) else (torch.float32, x.dtype)
     return (_vector(weight, "weight", kinds, x.shape[1], dev),
             _vector(bias, "bias", kinds, x.shape[1], dev), dtype)
@@ -753,15 +754,22 @@ def layer_norm_vjp_workspace(R: int, C: int) -> torch.Tensor:
 
 def layer_norm_vjp(x: torch.Tensor, weight: torch.Tensor | None, mean: torch.Tensor,
                    rstd: torch.Tensor, grad_y: torch.Tensor, want_x: bool = True,
-                   want_w: bool = True, workspace: torch.Tensor | None = None):
+                   want_w: bool = True, workspace: torch.Tensor | None = None,
+                   weight_dtype: torch.dtype | None = None):
     """Gradients of sum(grad_y * y) for y of layer_norm(x, weight, bias), with the mean and
     rstd that it saved.  Returns (grad_x [R][C], grad_weight [C], grad_bias [C]), None where
-    not wanted; the last two in the dtype of weight (of x where weight is None).  `workspace`
-    (layer_norm_vjp_workspace(R, C)) is allocated when not given and needed."""
+    not wanted; the last two in the dtype of weight.  Where weight is None, in weight_dtype:
+    float32 or the dtype of x, which it is when not given (a bias alone may be either).
+    `workspace` (layer_norm_vjp_workspace(R, C)) is allocated when not given and needed."""
     dev = torch.cuda.current_device()
     ldx = _rows(x, "x", FLOATS, dev)
     ldgy = _rows(grad_y, "grad_y", (x.dtype,), dev, x.shape)
     wp, _, wt = _norm_weights(x, weight, None, dev)
+    if weight_dtype is not None:
+        if weight_dtype not in ((torch.float32, x.dtype) if weight is None else (wt,)):
+            raise ValueError("weight_dtype must be the dtype of weight, or without one float32 or "
+                             "the dtype of x")
+        wt = weight_dtype
     R, C = x.shape
     mp = _vector(mean, "mean", (torch.float32,), R, dev)
     rp = _vector(rstd, "rstd", (torch.float32,), R, dev)
@@ -773,7 +781,7 @@ def layer_norm_vjp(x: torch.Tensor, weight: torch.Tensor | None, mean: torch.Ten
     grad_x = _result_rows(x) if want_x else None
     grad_w = grad_b = None
     if want_w:
-        grad_w = x.new_empty(C) if weight is None else torch.empty_like(weight)
+        grad_w = x.new_empty(C, dtype=wt) if weight is None else torch.empty_like(weight)
         grad_b = torch.empty_like(grad_w)
     nat.qtcq_layer_norm_vjp(x.data_ptr(), DTYPES[x.dtype], R, C, ldx, wp, DTYPES[wt], mp, rp,
                             grad_y.data_ptr(), ldgy, grad_x.data_ptr() if want_x else None, C,
@@ -843,7 +851,8 @@ def distill_topk_vjp(logits: torch.Tensor, index: torch.Tensor, teacher: torch.T
     ldl, ldi, ldt = _distill_inputs(logits, index, teacher, temperature, dev)
     (R, V), k = logits.shape, index.shape[1]
     gp = _vector(grad_loss, "grad_loss", (torch.float32,), R, dev)
-    if gp is None or not (isinstance(stats, torch.Tensor) and stats.shape == (R, 5)):
+    if gp is None or not (isinstance(stats, torch.Tensor) and stats.shape == (R, 5)
+                          and stats.is_contiguous()):
         raise ValueError("stats are those that distill_topk saved, grad_loss a value a row")
     sp = _vector(stats.view(-1), "stats", (torch.float32,), R * 5, dev)
     _not_recorded("distill_topk_vjp", logits, teacher, stats, grad_loss)
