@@ -33,13 +33,18 @@ qtcq_status norm_impl(const NormArgs& a, hipStream_t st)
 int part_pitch(int cols) { return (cols + 7) / 8 * 8; }
 
 // Whether the gradients take one launch that reads the rows a second time for the weights', by
-// the sizes alone: few rows, whose second reading comes from the caches, in up to three
-// readings of 512 rows (us, one launch against two: 333x2731 float32 12.4 / 16.2, 512x7168 16.2 /
-// 16.4, 1024x4096 20.3 / 16.3; 512x8192 bf16 13.5 / 18.2, 768x4096 13.4 / 16.4, 1024x2048 13.4 /
-// 16.2, 1536x1000 15.4 / 16.2, 1536x256 13.5 / 16.3, 2048x1000 19.5 / 16.3, 1000x8192 22.5 / 20.3).
-bool norm_few_rows(int64_t rows, int cols)
+// the sizes and the bytes of an element: few rows, whose second reading comes from the caches, in up
+// to three readings of 512 rows, each longer the more columns there are (us of whole calls, one
+// launch against two; 16 bits: 512x8192 13.9 / 17.9, 768x4096 13.8 / 16.7, 1024x3000 15.9 / 17.4,
+// 1280x2048 14.9 / 16.5, 1536x1000 15.2 / 16.3, 1536x2048 16.2 / 16.9, 1400x2200 19.3 / 17.4, 2048x1000
+// 19.5 / 16.3, 1000x8192 22.5 / 20.3; float32: 333x2731 13.2 / 16.8, 512x8192 17.7 / 17.6, 768x4096 15.7 /
+// 16.8, 640x4900 19.9 / 17.2, 1024x2048 14.9 / 16.7, 1024x2560 18.0 / 16.6, 1536x1024 15.3 / 16.5, 1280x1600
+// 17.2 / 16.5, 1536x2048 19.1 / 16.4).
+bool norm_few_rows(int64_t rows, int cols, size_t size)
 {
-    return rows <= 512 ? cols <= 8192 : rows <= 1536 && rows * cols <= 3 << 20;
+    if (rows <= 512) return cols <= 8192;
+    if (size == 2) return rows <= 1024 ? rows * cols <= 3 << 20 : rows <= 1536 && cols <= 2048;
+    return rows <= 768 ? cols <= 4096 : rows <= 1024 ? cols <= 2048 : rows <= 1536 && cols <= 1024;
 }
 
 template <typename T, typename W>
@@ -47,7 +52,7 @@ qtcq_status grad_impl(NormGradArgs a, W* grad_weight, W* grad_bias, float* part,
 {
     constexpr int E = 16 / (int)sizeof(T);
     const int chunks = (a.cols + E - 1) / E;
-    if (norm_few_rows(a.rows, a.cols)) {
+    if (norm_few_rows(a.rows, a.cols, sizeof(T))) {
         auto few = [&](auto rt, auto nch) {
             constexpr int RT = decltype(rt)::value, NCH = decltype(nch)::value, R = NCH == 1 ? 2 : 1;
             constexpr int PER = kNormGradThreads / RT * R;
@@ -116,9 +121,9 @@ qtcq_status with_types(int dtype, int weight_dtype, F&& f)
 
 }  // namespace
 
-size_t norm_grad_workspace_bytes(int64_t rows, int cols)
+size_t norm_grad_workspace_bytes(int64_t rows, int cols, size_t size)
 {
-    if (norm_few_rows(rows, cols)) return 0;
+    if (norm_few_rows(rows, cols, size)) return 0;
     return (size_t)(rows < kMostWorkgroups ? rows : kMostWorkgroups) * 2 * part_pitch(cols) * 4;
 }
 

@@ -104,7 +104,8 @@ inline size_t fp8_workspace_bytes(int M, int N, int K, bool whole)
     return most;
 }
 
-size_t norm_grad_workspace_bytes(int64_t rows, int cols);
+// size: bytes of an element; float32 needs no less than 16 bits do
+size_t norm_grad_workspace_bytes(int64_t rows, int cols, size_t size);
 size_t distill_workspace_bytes(int64_t rows, int vocab);
 
 qtcq_status launch_quantize_blocks(const void* x, int dtype, int64_t rows, int cols, int64_t ldx, int block_rows, uint8_t* q,

@@ -136,7 +136,7 @@ qtcq_status qtcq_layer_norm(const void* x, int dtype, int64_t rows, int cols, in
 size_t qtcq_layer_norm_vjp_workspace_bytes(int64_t rows, int cols)
 {
     if (rows < 0 || cols < 0 || rows > kDenseMaxDim || cols > kDenseMaxDim) return 0;
-    return host::norm_grad_workspace_bytes(rows, cols);
+    return host::norm_grad_workspace_bytes(rows, cols, 4);
 }
 
 qtcq_status qtcq_layer_norm_vjp(const void* x, int dtype, int64_t rows, int cols, int64_t ldx, const void* weight,
@@ -153,7 +153,7 @@ qtcq_status qtcq_layer_norm_vjp(const void* x, int dtype, int64_t rows, int cols
     if (!there(x, rows, cols, t) || !there(grad_y, rows, cols, t) || !there(mean, rows, 1, 4) || !there(rstd, rows, 1, 4) ||
         !optional(grad_x, t) || !optional(weight, w) || !optional(grad_weight, w) || !optional(grad_bias, w))
         return QTCQ_ERR_INVALID_ARG;
-    if (want_w && !workspace_ok(workspace, workspace_bytes, host::norm_grad_workspace_bytes(rows, cols)))
+    if (want_w && !workspace_ok(workspace, workspace_bytes, host::norm_grad_workspace_bytes(rows, cols, t)))
         return QTCQ_ERR_WORKSPACE;
     qtcq::NormGradArgs a = {};
     a.x = x;
