@@ -40,10 +40,16 @@ struct Fp8Plan {
 // 21.3 / 13.9; 14336x1024 at m = 48 14.3 / 10.9).  Rows that are not whole chunks cost the tiles
 // a copy and this kernel slower loads: 8192x8193 at m = 4 43.4 / 43.5, 8 48.7 / 43.7; 4096x4097 at
 // m = 24 (1.5 2^28) 21.4 / 22.3; 4096x2047 at m = 40 16.7 / 19.2; 2000x2047 at m = 64 20.5 / 16.6.
-inline bool fp8_few_rows(int m, int n, int k, bool whole)
+// Past 22528 columns the groups of 16 columns a compute unit takes in turn are the time, and a
+// tile of 128 needs no shares (16 bits: 16x20480x2048 12.8 / 14.6, 24x20480x1024 11.6 / 11.0, 9x24576x2048
+// 13.0 / 11.4, 32x24576x1024 14.2 / 11.2, 9x28672x2048 15.2 / 11.9, 16x28672x1536 13.8 / 11.3); float32 tiles,
+// at half the rate, from 17 rows on (16x24576x2048 14.9 / 16.8, 16x28672x1536 14.1 / 14.3, 24x24576x1024
+// 13.5 / 11.4, 32x24576x1024 14.7 / 11.4).
+inline bool fp8_few_rows(int m, int n, int k, bool whole, bool precise)
 {
     const double work = (double)m * n * k;
     if (!whole) return m <= 4 || (m <= 48 && work <= 0x1.9p28);
+    if (n > 22 << 10 && m > (precise ? 16 : 8)) return false;
     return m <= 8 || (m <= 32 && work <= 0x1.8p29) || (m <= 64 && n <= 8192 && k <= 4096 && (double)n * k <= 0x1p24);
 }
 
@@ -51,7 +57,7 @@ inline bool fp8_few_rows(int m, int n, int k, bool whole)
 inline Fp8Plan plan_fp8(int m, int n, int k, bool whole, bool precise)
 {
     Fp8Plan p = {};
-    if (m == 0 || n == 0 || fp8_few_rows(m, n, k, whole)) {
+    if (m == 0 || n == 0 || fp8_few_rows(m, n, k, whole, precise)) {
         p.skinny = true;
         return p;
     }
