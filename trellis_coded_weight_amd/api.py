@@ -618,15 +618,16 @@ def gated_vjp(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, gate: t
 FLOATS = (torch.float32, torch.bfloat16, torch.float16)
 
 
-def _not_recorded(name: str, *tensors) -> None:
-    """Autograd does not see the calls, so inputs that require gradients are refused while it
-    records (in a backward pass too, if that is to be differentiated again)."""
+def _not_recorded(name: str) -> None:
+    """For a call with inputs that require gradients: autograd does not see it, so it is refused
+    while autograd records (in a backward pass too, if that is to be differentiated again)."""
     if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad:
-                raise ValueError("%s does not record gradients: call it under torch.no_grad() or "
-                                 "with detached inputs (gradients come from the calls that compute "
-                                 "them)" % name)
+        raise ValueError("%s does not record gradients: call it under torch.no_grad() or with detached "
+                         "inputs (gradients come from the calls that compute them)" % name)
+
+
+def _grad(x) -> bool:
+    return x is not None and x.requires_grad
 
 
 def _vector(x, name: str, dtypes, n: int, device: int):
@@ -668,7 +669,8 @@ def quantize_blocks(x: torch.Tensor, block_rows: int = 1):
         raise ValueError("block_rows must be 1 or 128")
     dev = torch.cuda.current_device()
     ldx = _rows(x, "x", FLOATS, dev)
-    _not_recorded("quantize_blocks", x)
+    if x.requires_grad:
+        _not_recorded("quantize_blocks")
     R, C = x.shape
     q = x.new_empty((R, C), dtype=torch.float8_e4m3fn)
     down = R if block_rows == 1 else (R + 127) // 128
@@ -707,7 +709,8 @@ def matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale:
     kb = (K + 127) // 128
     as_row, as_col = _block_scales(a_scale, "a_scale", (M, kb), dev)
     ws_row, ws_col = _block_scales(w_scale, "w_scale", ((N + 127) // 128, kb), dev)
-    _not_recorded("matmul_fp8", a, a_scale, w, w_scale)
+    if a.requires_grad or a_scale.requires_grad or w.requires_grad or w_scale.requires_grad:
+        _not_recorded("matmul_fp8")
     ap, wp = a.data_ptr(), w.data_ptr()
     need = nat.qtcq_matmul_fp8_workspace_bytes(M, N, K, _whole_rows(ap | wp, K, 1, lda, ldw))
     _keep, ws, ws_bytes = _workspace(workspace, need, a)
@@ -738,7 +741,8 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
     dev = torch.cuda.current_device()
     ldx = _rows(x, "x", FLOATS, dev)
     wp, bp, wt = _norm_weights(x, weight, bias, dev)
-    _not_recorded("layer_norm", x, weight, bias)
+    if x.requires_grad or _grad(weight) or _grad(bias):
+        _not_recorded("layer_norm")
     R, C = x.shape
     y = _result_rows(x)
     mean = x.new_empty(R, dtype=torch.float32) if save else None
@@ -778,7 +782,8 @@ def layer_norm_vjp(x: torch.Tensor, weight: torch.Tensor | None, mean: torch.Ten
     rp = _vector(rstd, "rstd", (torch.float32,), R, dev)
     if mp is None or rp is None:
         raise ValueError("mean and rstd are those that layer_norm saved")
-    _not_recorded("layer_norm_vjp", x, weight, mean, rstd, grad_y)
+    if x.requires_grad or grad_y.requires_grad or mean.requires_grad or rstd.requires_grad or _grad(weight):
+        _not_recorded("layer_norm_vjp")
     need = nat.qtcq_layer_norm_vjp_workspace_bytes(R, C) if want_w else 0
     _keep, ws, ws_bytes = _workspace(workspace, need, x)
     grad_x = _result_rows(x) if want_x else None
@@ -831,7 +836,8 @@ def distill_topk(logits: torch.Tensor, index: torch.Tensor, teacher: torch.Tenso
     (R, V), k = logits.shape, index.shape[1]
     zp = _vector(teacher_log_z, "teacher_log_z", (torch.float32,), R, dev)
     gp = _vector(grad_loss, "grad_loss", (torch.float32,), R, dev)
-    _not_recorded("distill_topk", logits, teacher, teacher_log_z, grad_loss)
+    if logits.requires_grad or teacher.requires_grad or _grad(teacher_log_z) or _grad(grad_loss):
+        _not_recorded("distill_topk")
     _keep, ws, ws_bytes = _workspace(workspace, nat.qtcq_distill_topk_workspace_bytes(R, V), logits)
     loss = logits.new_empty(R, dtype=torch.float32)
     stats = logits.new_empty((R, 5), dtype=torch.float32) if save else None
@@ -858,7 +864,8 @@ def distill_topk_vjp(logits: torch.Tensor, index: torch.Tensor, teacher: torch.T
                           and stats.is_contiguous()):
         raise ValueError("stats are those that distill_topk saved, grad_loss a value a row")
     sp = _vector(stats.view(-1), "stats", (torch.float32,), R * 5, dev)
-    _not_recorded("distill_topk_vjp", logits, teacher, stats, grad_loss)
+    if logits.requires_grad or teacher.requires_grad or stats.requires_grad or grad_loss.requires_grad:
+        _not_recorded("distill_topk_vjp")
     grad = _result_rows(logits)
     nat.qtcq_distill_topk_vjp(logits.data_ptr(), DTYPES[logits.dtype], R, V, ldl, index.data_ptr(),
                               index.element_size(), ldi, teacher.data_ptr(), DTYPES[teacher.dtype],

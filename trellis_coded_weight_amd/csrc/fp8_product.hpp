@@ -26,7 +26,7 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 // Gaussian, 3e-6 where all products have one sign, 6.5e-5 where 3 columns of a in 100 are 64 times
 // the others: far below the rounding to bf16 (1.7e-3 of the norm), and a fifteenth to a third of
 // that to fp16 (2.1e-4), at twice the rate of the 16-bit instructions.  A group never loses more
-// than 7 2^-13 of that power of two, an eighth of a step of bf16 and one of fp16.  Where the
+// than 7 2^-13 of that power of two, a ninth of a step of bf16 there and most of one of fp16.  Where the
 // results are binary32, or the weights' bytes are the work, the e4m3 values go to fp16, which
 // holds them exactly, and the sums are those of binary32 (a float32 result at half the rate).
 __device__ __forceinline__ f16x8 e4m3_to_f16(uint32_t lo, uint32_t hi)
