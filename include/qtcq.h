@@ -589,8 +589,8 @@ qtcq_status qtcq_layer_norm(const void* x, int dtype, int64_t rows, int cols, in
  *   grad_y       [rows][cols] of dtype, row stride ldgy
  *   grad_x       [rows][cols] of dtype (out), row stride ldgx, or NULL
  *   grad_weight, grad_bias  [cols] of weight_dtype (out), each may be NULL
- *   workspace    >= qtcq_layer_norm_vjp_workspace_bytes(rows, cols) (0 for few rows); not
- *                needed where grad_weight and grad_bias are both NULL
+ *   workspace    >= qtcq_layer_norm_vjp_workspace_bytes(rows, cols) (0 for few rows), which
+ *                holds for every dtype; not needed where grad_weight and grad_bias are both NULL
  * Errors: as qtcq_layer_norm, and QTCQ_ERR_WORKSPACE. */
 size_t qtcq_layer_norm_vjp_workspace_bytes(int64_t rows, int cols);
 qtcq_status qtcq_layer_norm_vjp(const void* x, int dtype, int64_t rows, int cols, int64_t ldx,

@@ -17,8 +17,8 @@
 // 2^-29 relative at least or not at all, so that decides as the exact one).
 //
 // The pass is bound by memory: x read once, held in registers between the largest magnitude
-// and the rounding (28672x8192 bf16: 135 us in square blocks, 5.2 TB/s, 144 us by rows, 8192x8192
-// 45 us; 1x8192 3.5 us in the kernel).  With about 20 instructions an element the units are busy
+// and the rounding (28672x8192 bf16, calls in a row: 136 us in square blocks, 5.2 TB/s, 144 us by rows,
+// 8192x8192 45 us; 1x8192 3.1 us in the kernel).  With about 20 instructions an element the units are busy
 // a third of that time, which is why the exact quotients above are kept off the common path.
 #pragma once
 

@@ -21,8 +21,9 @@
 // Where tiles are fewer than the compute units, k is cut into shares; each writes its sums in
 // 32 bits, and join_shares adds them in order.
 //
-// 4096x28672x8192 to bf16: 775 us, 2.48 PFLOP/s, the matrix cores 67% busy at 1.7 to 1.8 GHz (on
-// operands of zeros 615 us at 2.4 GHz): power bounds it.  A loop of the instruction with its four
+// 4096x28672x8192 to bf16, in calls in a row: 774 us, 2.49 PFLOP/s, the matrix cores 67% busy at 1.7
+// to 1.8 GHz (on operands of zeros 615 us at 2.4 GHz): power bounds it.  After a pause launches take
+// 766 to 1045 us, until the clock has settled some 30 launches on.  A loop of the instruction with its four
 // scaled additions and nothing else reaches 3.75 PFLOP/s on random operands; in tiles of 32 x 32
 // 3.34.  93x8192x14336 to fp16: 24 us and 4.5 for the shares, w at 4.9 TB/s.  Smaller tiles are
 // bound by the loads to LDS: 128 x 128 tiles take 0.64 us a step, their loads alone 0.45 to 0.58

@@ -15,9 +15,9 @@
 // its rows in order, a workgroup its groups, and join_norm_sums the workgroups.  No atomics:
 // the same bits on every run.
 //
-// 8192x8192 bf16: forward 51.5 us in the kernel (5.2 TB/s), gradients 78 (5.2 TB/s) and 4.9 for
-// the 256 workgroups' sums; 333x2731 float32 gradients in one launch 7.6.  Without the next
-// rows' loads ahead of the work the forward took 78, the gradients 128.
+// 8192x8192 bf16, calls in a row: forward 54 us (5.0 TB/s), gradients 83, of which 78 (5.2 TB/s) and
+// 5 for the 256 workgroups' sums; 333x2731 float32 gradients in one launch 7.2 in the kernel.
+// Without the next rows' loads ahead of the work the forward took 78, the gradients 128.
 #pragma once
 
 #include "model_args.hpp"
